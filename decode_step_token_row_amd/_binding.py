@@ -9,6 +9,7 @@ missing or a call fails, it raises.
 
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 from typing import Optional
@@ -37,6 +38,8 @@ ERR_BAD_CAPACITY = -11
 ERR_SCRATCH_TOO_SMALL = -12
 ERR_BAD_BUDGET = -13
 ERR_BAD_DRY = -14
+ERR_BAD_HIDDEN = -15
+ERR_BAD_GROUP = -16
 DRY_MAX_WINDOW = 2048
 DRY_MAX_BREAKERS = 64
 NOALLOC_SCRATCH_BYTES = 16384
@@ -49,6 +52,8 @@ ROW_BAD_FLAGS = 5
 ROW_TIES_WIDE = 1  # arcs_row_params.flags bit
 ROW_HISTORY_TOO_LONG = 6
 ROW_VOCAB_TOO_LARGE = 7
+ROW_BAD_TARGET = 8
+MAX_HIDDEN = 65536  # ARCS_MAX_HIDDEN
 MAX_HISTORY = 4096
 MAX_PENALTY_VOCAB = 262144
 TOP_LOGPROBS_MAX_VOCAB = 262144  # ARCS_TOP_LOGPROBS_MAX_VOCAB
@@ -119,6 +124,18 @@ def library() -> ctypes.CDLL:
         lib.arcs_top_logprobs.restype = c_i
         lib.arcs_commit_tokens.argtypes = [c_p, c_i64, c_i64, c_p, c_p, c_p, c_u64, c_p, c_p, c_p, c_p]
         lib.arcs_commit_tokens.restype = c_i
+        lib.arcs_w4_logits.argtypes = [c_p, c_i64, c_i64, c_i64, c_p, c_i64, c_i64, c_p, c_i, c_i64, c_p, c_i64,
+                                       c_i, c_p, c_i, c_i64, c_p]
+        lib.arcs_w4_logits.restype = c_i
+        lib.arcs_linear_cross_entropy.argtypes = [c_p, c_i64, c_p, c_i64, c_i, c_i64, c_i64, c_i64, c_p,
+                                                  ctypes.c_int32, c_p, c_p, c_p, c_p, c_p, ctypes.c_size_t, c_p]
+        lib.arcs_linear_cross_entropy.restype = c_i
+        lib.arcs_linear_cross_entropy_backward.argtypes = [c_p, c_i64, c_p, c_i64, c_i, c_i64, c_i64, c_i64, c_p,
+                                                           ctypes.c_int32, c_p, c_p, c_p, c_p, c_p, c_p,
+                                                           ctypes.c_size_t, c_p]
+        lib.arcs_linear_cross_entropy_backward.restype = c_i
+        lib.arcs_linear_cross_entropy_workspace_bytes.argtypes = [c_i64, c_i64, c_i64, c_i, c_i]
+        lib.arcs_linear_cross_entropy_workspace_bytes.restype = ctypes.c_size_t
         lib.arcs_sample_workspace_bytes.argtypes = [c_i64, c_i64, c_i]
         lib.arcs_sample_workspace_bytes.restype = ctypes.c_size_t
         lib.arcs_long_history_workspace_bytes.argtypes = [c_i64, c_i64]
@@ -145,6 +162,11 @@ def workspace_bytes(B: int, V: int, dtype: int) -> int:
 
 def long_history_workspace_bytes(B: int, V: int) -> int:
     return int(library().arcs_long_history_workspace_bytes(int(B), int(V)))
+
+
+def linear_cross_entropy_workspace_bytes(N: int, V: int, D: int, dtype: int, backward: bool = False) -> int:
+    return int(library().arcs_linear_cross_entropy_workspace_bytes(int(N), int(V), int(D), int(dtype),
+                                                                   1 if backward else 0))
 
 
 # --------------------------------------------------------------------------
@@ -470,3 +492,165 @@ def sample_debug(logits, params, hist_ids=None, hist_offsets=None, seed: int = 0
     torch.cuda.synchronize(dev)
     st_np = stats.cpu().numpy().view(ROW_STATS_DTYPE)
     return out, status, st_np, probs
+
+
+# --------------------------------------------------------------------------
+# the vocabulary head: 4-bit logits and the linear cross entropy
+# --------------------------------------------------------------------------
+def _work_on(device, stream):
+    """The device and stream a head call runs on: the given stream, which has to
+    be one of the tensors' device, or that device's current stream.  What the
+    call allocates then belongs to that stream."""
+    torch = _torch()
+    if stream is not None:
+        if stream.device != device:
+            raise ValueError(f"stream is on {stream.device}, the tensors are on {device}")
+        return torch.cuda.stream(stream)
+    if torch.cuda.current_device() != device.index:
+        return torch.cuda.device(device)
+    return contextlib.nullcontext()
+
+
+def _matrix(t, name: str, dtype, rows: int, cols: int, device):
+    """A device matrix with unit column stride; returns its row stride."""
+    if t.dtype != dtype or t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols or t.device != device:
+        raise ValueError(f"{name} must be a [{rows}, {cols}] {dtype} tensor on {device}")
+    if t.stride(1) != 1 and cols > 1:
+        raise ValueError(f"{name} rows must be contiguous (stride(1) == 1)")
+    return cols if rows == 1 else t.stride(0)
+
+
+def _vector(t, name: str, dtype, n: int, device):
+    if t.dtype != dtype or t.numel() != n or t.device != device or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} elements on {device}")
+
+
+def _hidden_shape(hidden, what: str = "hidden"):
+    if not hidden.is_cuda:
+        raise ValueError(f"{what} must be a device tensor")
+    if hidden.dim() != 2:
+        raise ValueError(f"{what} must be [rows, D]")
+    return hidden.shape[0], hidden.shape[1], hidden.device
+
+
+def w4_logits(hidden, qweight, scales, group_size: int, zeros=None, out=None, out_dtype=None, stream=None):
+    """arcs_w4_logits: [B, V] logits of a 4-bit head, ready for argmax, sample and top_logprobs.
+
+    ``hidden`` bfloat16 [B, D]; ``qweight`` uint8 [V, D / 2], the even weight in
+    the low nibble; ``scales`` bfloat16 or float32 [V, D / group_size]; ``zeros``
+    uint8 [V, D / group_size] or None (8).  ``out`` [B, V] bfloat16 or float32
+    with contiguous rows, or None: a new tensor of ``out_dtype`` (bfloat16).
+    """
+    torch = _torch()
+    B, D, dev = _hidden_shape(hidden)
+    V, G = qweight.shape[0], int(group_size)
+    groups = D // G if G > 0 else 0
+    hs = _matrix(hidden, "hidden", torch.bfloat16, B, D, dev)
+    qs = _matrix(qweight, "qweight", torch.uint8, V, D // 2, dev)
+    sdt = _dtype_code_of(scales, "scales")
+    ss = _matrix(scales, "scales", scales.dtype, V, groups, dev)
+    zs = 0 if zeros is None else _matrix(zeros, "zeros", torch.uint8, V, groups, dev)
+    with _work_on(dev, stream):
+        if out is None:
+            out = torch.empty((B, V), dtype=torch.bfloat16 if out_dtype is None else out_dtype, device=dev)
+        elif out_dtype is not None and out.dtype != out_dtype:
+            raise ValueError("out is not of out_dtype")
+        odt = _dtype_code_of(out, "out")
+        ls = _matrix(out, "out", out.dtype, B, V, dev)
+        st = library().arcs_w4_logits(_ptr(hidden), B, D, hs, _ptr(qweight), V, qs, _ptr(scales), sdt, ss,
+                                      _ptr(zeros), zs, G, _ptr(out), odt, ls, _stream_ptr(stream))
+    if st != OK:
+        raise ArcsError(st, "arcs_w4_logits")
+    return out
+
+
+def _dtype_code_of(t, name: str) -> int:
+    torch = _torch()
+    if t.dtype == torch.bfloat16:
+        return DTYPE_BF16
+    if t.dtype == torch.float32:
+        return DTYPE_F32
+    raise TypeError(f"{name} must be bfloat16 or float32, got {t.dtype}")
+
+
+def _cross_entropy_inputs(hidden, weight, targets, temperature):
+    torch = _torch()
+    N, D, dev = _hidden_shape(hidden)
+    dt = _dtype_code_of(hidden, "hidden")
+    hs = _matrix(hidden, "hidden", hidden.dtype, N, D, dev)
+    V = weight.shape[0]
+    ws = _matrix(weight, "weight", hidden.dtype, V, D, dev)
+    _vector(targets, "targets", torch.int32, N, dev)
+    if temperature is not None:
+        _vector(temperature, "temperature", torch.float32, N, dev)
+    return N, V, D, dev, dt, hs, ws
+
+
+def _cross_entropy_workspace(workspace, N, V, D, dt, backward, dev):
+    torch = _torch()
+    if workspace is None:
+        # sizes the library refuses need none: the call itself reports them
+        need = max(256, linear_cross_entropy_workspace_bytes(N, V, D, dt, backward))
+        return torch.empty(need, dtype=torch.uint8, device=dev), need
+    if workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError(f"workspace must be a contiguous tensor on {dev}")
+    return workspace, workspace.numel() * workspace.element_size()
+
+
+def linear_cross_entropy(hidden, weight, targets, temperature=None, ignore_index: int = -100, out_loss=None,
+                         out_lse=None, out_status=None, workspace=None, stream=None):
+    """arcs_linear_cross_entropy: (loss, lse), float32 [N] each, of int32 ``targets`` under
+    softmax(hidden weight^T / temperature), without the [N, V] logits.
+
+    -loss is each target's log-probability; lse goes to
+    linear_cross_entropy_backward.  The result has no autograd graph: gradients
+    are computed by that call.
+    """
+    torch = _torch()
+    N, V, D, dev, dt, hs, ws = _cross_entropy_inputs(hidden, weight, targets, temperature)
+    with _work_on(dev, stream):
+        if out_loss is None:
+            out_loss = torch.empty(N, dtype=torch.float32, device=dev)
+        if out_lse is None:
+            out_lse = torch.empty(N, dtype=torch.float32, device=dev)
+        _vector(out_loss, "out_loss", torch.float32, N, dev)
+        _vector(out_lse, "out_lse", torch.float32, N, dev)
+        if out_status is not None:
+            _vector(out_status, "out_status", torch.int32, N, dev)
+        workspace, ws_bytes = _cross_entropy_workspace(workspace, N, V, D, dt, False, dev)
+        st = library().arcs_linear_cross_entropy(_ptr(hidden), hs, _ptr(weight), ws, dt, N, V, D, _ptr(targets),
+                                                 int(ignore_index), _ptr(temperature), _ptr(out_loss),
+                                                 _ptr(out_lse), _ptr(out_status), _ptr(workspace), ws_bytes,
+                                                 _stream_ptr(stream))
+    if st != OK:
+        raise ArcsError(st, "arcs_linear_cross_entropy")
+    return out_loss, out_lse
+
+
+def linear_cross_entropy_backward(hidden, weight, targets, lse, grad_loss, temperature=None,
+                                  ignore_index: int = -100, out_dhidden=None, out_dweight=None,
+                                  want_hidden: bool = True, want_weight: bool = True, workspace=None, stream=None):
+    """arcs_linear_cross_entropy_backward: (dhidden [N, D], dweight [V, D]) of
+    sum(grad_loss * loss), in the inputs' type; None in place of one not wanted.
+    ``lse`` is the forward call's, ``grad_loss`` float32 [N]."""
+    torch = _torch()
+    N, V, D, dev, dt, hs, ws = _cross_entropy_inputs(hidden, weight, targets, temperature)
+    _vector(lse, "lse", torch.float32, N, dev)
+    _vector(grad_loss, "grad_loss", torch.float32, N, dev)
+    with _work_on(dev, stream):
+        if want_hidden and out_dhidden is None:
+            out_dhidden = torch.empty((N, D), dtype=hidden.dtype, device=dev)
+        if want_weight and out_dweight is None:
+            out_dweight = torch.empty((V, D), dtype=hidden.dtype, device=dev)
+        if out_dhidden is not None:
+            _vector(out_dhidden, "out_dhidden", hidden.dtype, N * D, dev)
+        if out_dweight is not None:
+            _vector(out_dweight, "out_dweight", hidden.dtype, V * D, dev)
+        workspace, ws_bytes = _cross_entropy_workspace(workspace, N, V, D, dt, True, dev)
+        st = library().arcs_linear_cross_entropy_backward(
+            _ptr(hidden), hs, _ptr(weight), ws, dt, N, V, D, _ptr(targets), int(ignore_index), _ptr(temperature),
+            _ptr(lse), _ptr(grad_loss), _ptr(out_dhidden), _ptr(out_dweight), _ptr(workspace), ws_bytes,
+            _stream_ptr(stream))
+    if st != OK:
+        raise ArcsError(st, "arcs_linear_cross_entropy_backward")
+    return out_dhidden, out_dweight

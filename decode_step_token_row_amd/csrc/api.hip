@@ -9,6 +9,7 @@
 #include <atomic>
 
 #include "arcs.h"
+#include "cross_entropy.hpp"
 #include "launch.hpp"
 
 // Device scratch of arcs_sample_noalloc: one copy per GPU, held until the
@@ -124,6 +125,60 @@ int sample_impl(const void* logits, int dtype, int64_t B, int64_t V, int64_t row
   a.split_P = split ? arcs::split_slices(B) : 0;
   hipError_t e = arcs::launch_sample(a, dtype, B, vec, (hipStream_t)stream);
   return e == hipSuccess ? ARCS_OK : ARCS_ERR_LAUNCH;
+}
+
+bool misaligned(const void* p, uintptr_t to) { return ((uintptr_t)p) % to != 0; }
+
+// Arguments the two directions of the linear cross entropy share.
+int check_cross_entropy(const void* hidden, int64_t hidden_stride, const void* weight, int64_t weight_stride,
+                        int dtype, int64_t N, int64_t V, int64_t D, const int32_t* targets,
+                        const float* temperature, const void* workspace, size_t workspace_bytes, bool backward,
+                        arcs::CePlan* plan) {
+  if (hidden == nullptr || weight == nullptr || targets == nullptr) return ARCS_ERR_NULL_POINTER;
+  if (dtype != ARCS_DTYPE_BF16 && dtype != ARCS_DTYPE_F32) return ARCS_ERR_BAD_DTYPE;
+  if (N <= 0 || N > kMaxDim) return ARCS_ERR_BAD_BATCH;
+  if (V <= 0 || V > kMaxDim) return ARCS_ERR_BAD_VOCAB;
+  if (D <= 0 || D > ARCS_MAX_HIDDEN) return ARCS_ERR_BAD_HIDDEN;
+  if (hidden_stride < D || weight_stride < D) return ARCS_ERR_BAD_STRIDE;
+  const uintptr_t es = dtype == ARCS_DTYPE_BF16 ? 2 : 4;
+  if (misaligned(hidden, es) || misaligned(weight, es) || misaligned(targets, 4) || misaligned(temperature, 4))
+    return ARCS_ERR_MISALIGNED;
+  *plan = arcs::cross_entropy_plan(N, V, D, dtype, backward);
+  if (!plan->fits) return ARCS_ERR_BAD_BATCH;
+  if (workspace_bytes < plan->total) return ARCS_ERR_WORKSPACE_TOO_SMALL;
+  if (workspace == nullptr) return ARCS_ERR_NULL_POINTER;
+  if (misaligned(workspace, 256)) return ARCS_ERR_MISALIGNED;
+  return ARCS_OK;
+}
+
+arcs::CeArgs cross_entropy_args(const void* hidden, int64_t hidden_stride, const void* weight,
+                                int64_t weight_stride, int64_t N, int64_t V, int64_t D, const int32_t* targets,
+                                int32_t ignore_index, const float* temperature, const arcs::CePlan& p,
+                                void* workspace) {
+  arcs::CeArgs a = {};
+  a.hidden = hidden;
+  a.hidden_stride = hidden_stride;
+  a.weight = weight;
+  a.weight_stride = weight_stride;
+  a.N = N;
+  a.V = V;
+  a.D = D;
+  a.targets = targets;
+  a.ignore_index = ignore_index;
+  a.temperature = temperature;
+  char* w = (char*)workspace;
+  a.head = (arcs::CeHeader*)w;
+  a.rows = (arcs::CeRow*)(w + p.rows);
+  a.place = (int32_t*)(w + p.place);
+  a.partial = (float2*)(w + p.partial);
+  a.slices = p.slices;
+  a.ytarget = (float*)(w + p.ytarget);
+  a.ds = w + p.ds;
+  a.ds_ld = p.piece;
+  a.slab = (float*)(w + p.slab);
+  a.splits = p.splits;
+  a.hc = w + p.hc;
+  return a;
 }
 
 }  // namespace
@@ -248,6 +303,96 @@ int arcs_top_logprobs(const void* logits, int dtype, int64_t B, int64_t V, int64
   return e == hipSuccess ? ARCS_OK : ARCS_ERR_LAUNCH;
 }
 
+int arcs_w4_logits(const void* hidden, int64_t B, int64_t D, int64_t hidden_stride, const uint8_t* qweight,
+                   int64_t V, int64_t qweight_stride, const void* scales, int scale_dtype,
+                   int64_t scale_stride, const uint8_t* zeros, int64_t zero_stride, int group_size,
+                   void* logits, int logits_dtype, int64_t row_stride, void* stream) {
+  if (hidden == nullptr || qweight == nullptr || scales == nullptr || logits == nullptr) return ARCS_ERR_NULL_POINTER;
+  if ((scale_dtype != ARCS_DTYPE_BF16 && scale_dtype != ARCS_DTYPE_F32) ||
+      (logits_dtype != ARCS_DTYPE_BF16 && logits_dtype != ARCS_DTYPE_F32))
+    return ARCS_ERR_BAD_DTYPE;
+  if (B <= 0 || B > ARCS_W4_MAX_BATCH) return ARCS_ERR_BAD_BATCH;
+  if (V <= 0 || V > kMaxDim) return ARCS_ERR_BAD_VOCAB;
+  if (D <= 0 || D > ARCS_MAX_HIDDEN) return ARCS_ERR_BAD_HIDDEN;
+  if ((group_size != 32 && group_size != 64 && group_size != 128) || D % group_size != 0) return ARCS_ERR_BAD_GROUP;
+  const int64_t groups = D / group_size;
+  if (hidden_stride < D || qweight_stride < D / 2 || scale_stride < groups || row_stride < V ||
+      (zeros != nullptr && zero_stride < groups))
+    return ARCS_ERR_BAD_STRIDE;
+  if (misaligned(hidden, 16) || hidden_stride % 8 != 0 || misaligned(qweight, 16) || qweight_stride % 16 != 0 ||
+      misaligned(scales, scale_dtype == ARCS_DTYPE_BF16 ? 2 : 4) ||
+      misaligned(logits, logits_dtype == ARCS_DTYPE_BF16 ? 2 : 4))
+    return ARCS_ERR_MISALIGNED;
+  arcs::W4Args a;
+  a.hidden = (const uint16_t*)hidden;
+  a.B = B;
+  a.D = D;
+  a.hidden_stride = hidden_stride;
+  a.qweight = qweight;
+  a.V = V;
+  a.qweight_stride = qweight_stride;
+  a.scales = scales;
+  a.scale_stride = scale_stride;
+  a.zeros = zeros;
+  a.zero_stride = zero_stride;
+  a.logits = logits;
+  a.row_stride = row_stride;
+  hipError_t e = arcs::launch_w4_logits(a, scale_dtype, logits_dtype, group_size, (hipStream_t)stream);
+  return e == hipSuccess ? ARCS_OK : ARCS_ERR_LAUNCH;
+}
+
+int arcs_linear_cross_entropy(const void* hidden, int64_t hidden_stride, const void* weight,
+                              int64_t weight_stride, int dtype, int64_t N, int64_t V, int64_t D,
+                              const int32_t* targets, int32_t ignore_index, const float* temperature,
+                              float* out_loss, float* out_lse, int32_t* out_status, void* workspace,
+                              size_t workspace_bytes, void* stream) {
+  if (out_loss == nullptr || out_lse == nullptr) return ARCS_ERR_NULL_POINTER;
+  arcs::CePlan plan;
+  int st = check_cross_entropy(hidden, hidden_stride, weight, weight_stride, dtype, N, V, D, targets, temperature,
+                               workspace, workspace_bytes, false, &plan);
+  if (st != ARCS_OK) return st;
+  if (misaligned(out_loss, 4) || misaligned(out_lse, 4) || misaligned(out_status, 4)) return ARCS_ERR_MISALIGNED;
+  arcs::CeArgs a = cross_entropy_args(hidden, hidden_stride, weight, weight_stride, N, V, D, targets, ignore_index,
+                                      temperature, plan, workspace);
+  a.out_loss = out_loss;
+  a.out_lse = out_lse;
+  a.out_status = out_status;
+  hipError_t e = arcs::launch_cross_entropy(a, dtype, false, (hipStream_t)stream);
+  return e == hipSuccess ? ARCS_OK : ARCS_ERR_LAUNCH;
+}
+
+int arcs_linear_cross_entropy_backward(const void* hidden, int64_t hidden_stride, const void* weight,
+                                       int64_t weight_stride, int dtype, int64_t N, int64_t V, int64_t D,
+                                       const int32_t* targets, int32_t ignore_index, const float* temperature,
+                                       const float* lse, const float* grad_loss, void* out_dhidden,
+                                       void* out_dweight, void* workspace, size_t workspace_bytes, void* stream) {
+  if (lse == nullptr || grad_loss == nullptr || (out_dhidden == nullptr && out_dweight == nullptr))
+    return ARCS_ERR_NULL_POINTER;
+  arcs::CePlan plan;
+  int st = check_cross_entropy(hidden, hidden_stride, weight, weight_stride, dtype, N, V, D, targets, temperature,
+                               workspace, workspace_bytes, true, &plan);
+  if (st != ARCS_OK) return st;
+  const uintptr_t es = dtype == ARCS_DTYPE_BF16 ? 2 : 4;
+  if (misaligned(lse, 4) || misaligned(grad_loss, 4) || misaligned(out_dhidden, es) || misaligned(out_dweight, es))
+    return ARCS_ERR_MISALIGNED;
+  arcs::CeArgs a = cross_entropy_args(hidden, hidden_stride, weight, weight_stride, N, V, D, targets, ignore_index,
+                                      temperature, plan, workspace);
+  a.lse = lse;
+  a.grad_loss = grad_loss;
+  a.out_dhidden = out_dhidden;
+  a.out_dweight = out_dweight;
+  hipError_t e = arcs::launch_cross_entropy(a, dtype, true, (hipStream_t)stream);
+  return e == hipSuccess ? ARCS_OK : ARCS_ERR_LAUNCH;
+}
+
+size_t arcs_linear_cross_entropy_workspace_bytes(int64_t N, int64_t V, int64_t D, int dtype, int backward) {
+  if (N <= 0 || N > kMaxDim || V <= 0 || V > kMaxDim || D <= 0 || D > ARCS_MAX_HIDDEN ||
+      (dtype != ARCS_DTYPE_BF16 && dtype != ARCS_DTYPE_F32))
+    return 0;
+  const arcs::CePlan p = arcs::cross_entropy_plan(N, V, D, dtype, backward != 0);
+  return p.fits ? p.total : 0;
+}
+
 size_t arcs_long_history_workspace_bytes(int64_t B, int64_t V) {
   if (B <= 0 || V <= 0) return 0;
   const unsigned __int128 n = (unsigned __int128)B * (unsigned __int128)V * 4u;
@@ -272,6 +417,8 @@ const char* arcs_status_string(int code) {
     case ARCS_ERR_BAD_DRY: return "DRY breakers: NULL with n_breakers > 0, or n_breakers outside [0, 64]";
     case ARCS_ERR_SCRATCH_TOO_SMALL:
       return "the shape needs more workspace than arcs_sample_noalloc's scratch (ARCS_NOALLOC_SCRATCH_BYTES)";
+    case ARCS_ERR_BAD_HIDDEN: return "hidden size D must be in [1, ARCS_MAX_HIDDEN]";
+    case ARCS_ERR_BAD_GROUP: return "group_size must be 32, 64 or 128 and divide D";
     case ARCS_ERR_LAUNCH: return "kernel launch failed";
     case ARCS_ERR_MISALIGNED: return "logits pointer not aligned to its element size";
     case ARCS_ERR_BAD_HISTORY: return "hist_ids and hist_offsets must both be NULL or both be set";
@@ -284,6 +431,7 @@ const char* arcs_status_string(int code) {
     case ARCS_ROW_BAD_FLAGS: return "row: flags must be 0";
     case ARCS_ROW_HISTORY_TOO_LONG: return "row: penalties need at most ARCS_MAX_HISTORY distinct history ids";
     case ARCS_ROW_VOCAB_TOO_LARGE: return "row: penalties need V <= ARCS_MAX_PENALTY_VOCAB";
+    case ARCS_ROW_BAD_TARGET: return "row: target outside [0, V) and not ignore_index";
     default: return "unknown status";
   }
 }

@@ -1,0 +1,82 @@
+// Host and device declarations shared by the linear cross entropy's kernels.
+//
+//   z = hidden weight^T / T          [N, V], never kept whole
+//   loss_n = logsumexp(z_n) - z_n[t_n]
+//   dz = (softmax(z) - onehot(t)) * grad_loss / T
+//   dhidden = dz weight,  dweight = dz^T hidden
+//
+// Rows whose target is ignore_index (masked) or refused (a target outside the
+// vocabulary, a temperature that is no positive finite number) are left out of
+// every product: a row list built on the device holds the others, and their
+// hidden states are never read (NaN there reaches nothing).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+#include "arcs.h"
+
+namespace arcs {
+
+// What the device knows of a call's rows once the list is built.
+struct CeHeader {
+  int32_t count;  // rows in the list
+  float gmax;     // largest finite |grad_loss / T| of them (1 if that is 0)
+  int32_t pad[62];
+};
+static_assert(sizeof(CeHeader) == 256, "workspace header");
+
+// One listed row.
+struct CeRow {
+  int32_t row;     // its place in the call's arrays
+  int32_t target;  // in [0, V)
+  float a;         // log2(e) / T: logits in base 2 are dot * a
+  float c;         // (grad_loss / T) / gmax
+  float lse2;      // its logsumexp in base 2 (backward)
+  int32_t pad[3];
+};
+static_assert(sizeof(CeRow) == 32, "row record");
+
+struct CeArgs {
+  const void* hidden;
+  int64_t hidden_stride;
+  const void* weight;
+  int64_t weight_stride;
+  int64_t N, V, D;
+  const int32_t* targets;
+  int32_t ignore_index;
+  const float* temperature;  // [N] or NULL
+  float* out_loss;           // forward
+  float* out_lse;
+  int32_t* out_status;       // or NULL
+  const float* lse;          // backward
+  const float* grad_loss;
+  void* out_dhidden;         // [N, D] or NULL
+  void* out_dweight;         // [V, D] or NULL
+  // workspace
+  CeHeader* head;
+  CeRow* rows;      // [N]
+  int32_t* place;   // [N] backward: a row's place in the list, -1 if it is not listed
+  float2* partial;  // forward: [N][slices] (maximum, sum of 2^(y - maximum)) of y = z * log2(e)
+  int64_t slices;
+  float* ytarget;   // forward: [N] y of the target
+  void* ds;         // backward: [N][ds_ld] dz / gmax of one piece of the vocabulary
+  int64_t ds_ld;    // (also the piece's length)
+  float* slab;      // backward: [splits][N][D] partial sums of dhidden / gmax
+  int splits;
+  void* hc;         // backward, matrix kernels: [N][D] hidden states of the listed rows
+};
+
+// The workspace's parts, in bytes from its start.
+struct CePlan {
+  size_t rows, place, partial, ytarget, ds, slab, hc, total;
+  int64_t slices, piece;
+  int splits;
+  bool fits;  // the sizes fit size_t and the launch grids
+};
+CePlan cross_entropy_plan(int64_t N, int64_t V, int64_t D, int dtype, bool backward);
+
+hipError_t launch_cross_entropy(const CeArgs& a, int dtype, bool backward, hipStream_t stream);
+
+}  // namespace arcs

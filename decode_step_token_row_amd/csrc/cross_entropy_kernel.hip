@@ -1,0 +1,440 @@
+// Linear cross entropy: row list, reductions and the general matrix kernel.
+//
+// The general kernel runs every type, alignment and size: operands are
+// widened to float32 on their way into LDS and multiplied with the float32
+// matrix instruction, so its products are those of float32 arithmetic.
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "cross_entropy.hpp"
+#include "device_common.hpp"
+#include "launch.hpp"
+
+namespace arcs {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+__device__ __forceinline__ float finite_or_zero(float m) { return m == -__builtin_inff() ? 0.0f : m; }
+
+// ---------------------------------------------------------------------------
+// The row list.  One workgroup: rows keep their order, so sums over rows do
+// not depend on timing.
+// ---------------------------------------------------------------------------
+constexpr int kPrepNT = 1024;
+
+template <bool BACKWARD>
+__global__ __launch_bounds__(kPrepNT) void ce_prep_kernel(CeArgs a) {
+  __shared__ int s_count[kPrepNT / kWave];
+  __shared__ float s_max[kPrepNT / kWave];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  // 0: listed, 1: masked, otherwise a row status code
+  auto kind = [&](int64_t n, int32_t& t, float& T) {
+    t = a.targets[n];
+    T = a.temperature ? a.temperature[n] : 1.0f;
+    if (t == a.ignore_index) return -1;
+    if (t < 0 || (int64_t)t >= a.V) return (int)ARCS_ROW_BAD_TARGET;
+    if (!(T > 0.0f) || T == __builtin_inff()) return (int)ARCS_ROW_BAD_TEMPERATURE;
+    return 0;
+  };
+  float gmax = 1.0f;
+  if (BACKWARD) {
+    float m = 0.0f;
+    for (int64_t n = tid; n < a.N; n += kPrepNT) {
+      int32_t t;
+      float T;
+      if (kind(n, t, T) != 0) continue;
+      const float g = fabsf(a.grad_loss[n] / T);
+      if (g < __builtin_inff() && g > m) m = g;
+    }
+    m = wave_max_f32(m);
+    if (lane == 0) s_max[wave] = m;
+    __syncthreads();
+    for (int w = 0; w < kPrepNT / kWave; ++w) m = fmaxf(m, s_max[w]);
+    if (m > 0.0f) gmax = m;
+  }
+  int base = 0;
+  for (int64_t n0 = 0; n0 < a.N; n0 += kPrepNT) {
+    const int64_t n = n0 + tid;
+    int32_t t = 0;
+    float T = 1.0f;
+    const int k = n < a.N ? kind(n, t, T) : 1;
+    const uint64_t mask = __ballot(k == 0);
+    __syncthreads();  // the last round's counts have been read
+    if (lane == 0) s_count[wave] = __popcll(mask);
+    __syncthreads();
+    int before = 0, all = 0;
+    for (int w = 0; w < kPrepNT / kWave; ++w) {
+      const int c = s_count[w];
+      before += w < wave ? c : 0;
+      all += c;
+    }
+    const int at = base + before + __popcll(mask & ((1ull << lane) - 1ull));
+    base += all;
+    if (n >= a.N) continue;
+    if (k == 0) {
+      CeRow r;
+      r.row = (int32_t)n;
+      r.target = t;
+      r.a = kLog2e / T;
+      r.c = BACKWARD ? (a.grad_loss[n] / T) / gmax : 0.0f;
+      r.lse2 = BACKWARD ? a.lse[n] * kLog2e : 0.0f;
+      r.pad[0] = r.pad[1] = r.pad[2] = 0;
+      a.rows[at] = r;
+    }
+    if (BACKWARD) {
+      a.place[n] = k == 0 ? at : -1;
+    } else {
+      if (k != 0) {
+        const float v = k < 0 ? 0.0f : __builtin_nanf("");
+        a.out_loss[n] = v;
+        a.out_lse[n] = v;
+      }
+      if (a.out_status) a.out_status[n] = k < 0 ? 0 : k;
+    }
+  }
+  if (tid == 0) {
+    a.head->count = base;
+    a.head->gmax = gmax;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Forward: the slices of a row joined, one wave per listed row.
+// ---------------------------------------------------------------------------
+__global__ __launch_bounds__(256) void ce_combine_kernel(CeArgs a) {
+  const int64_t i = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
+  const int lane = threadIdx.x & 63;
+  if (i >= a.head->count) return;
+  const float2* p = a.partial + i * a.slices;
+  float m = -__builtin_inff();
+  for (int64_t s = lane; s < a.slices; s += kWave) m = fmaxf(m, p[s].x);
+  for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, kWave));
+  const float m0 = finite_or_zero(m);
+  float sum = 0.0f;
+  for (int64_t s = lane; s < a.slices; s += kWave) {
+    const float2 q = p[s];
+    sum = fmaf(q.y, exp2_fast(q.x - m0), sum);
+  }
+  for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o, kWave);
+  if (lane == 0) {
+    const float l2 = m + log2f(sum);
+    const int32_t n = a.rows[i].row;
+    a.out_lse[n] = l2 * kLn2;
+    a.out_loss[n] = (l2 - a.ytarget[i]) * kLn2;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Backward: dhidden rows from the slabs, and zeros for rows not listed.
+// ---------------------------------------------------------------------------
+template <bool BF16>
+__global__ __launch_bounds__(256) void ce_dhidden_kernel(CeArgs a) {
+  const int64_t n = blockIdx.x;
+  const int i = a.place[n];
+  const float g = a.head->gmax;
+  const int64_t step = a.N * a.D;
+  for (int64_t d = threadIdx.x; d < a.D; d += 256) {
+    float v = 0.0f;
+    if (i >= 0) {
+      const float* p = a.slab + (int64_t)i * a.D + d;
+      for (int s = 0; s < a.splits; ++s) v += p[s * step];
+      v *= g;
+    }
+    if (BF16) ((__bf16*)a.out_dhidden)[n * a.D + d] = (__bf16)v;
+    else ((float*)a.out_dhidden)[n * a.D + d] = v;
+  }
+}
+
+// ---------------------------------------------------------------------------
+// The general matrix kernel: C[m, n] = sum_k A[m, k] B[n, k] on 128 x 128
+// tiles, four waves of 64 x 64 (two by two 32x32x2 float32 products), 16 k at
+// a time through LDS.
+//   STATS    m: vocabulary, n: listed rows, k: D    maximum and sum per tile
+//   DS       the same                               dz / gmax of the piece
+//   DHIDDEN  m: D, n: listed rows, k: the piece     adds to the split's slab
+//   DWEIGHT  m: D, n: the piece, k: listed rows     rows of dweight
+// ---------------------------------------------------------------------------
+enum CeMode { kCeStats, kCeDs, kCeDhidden, kCeDweight };
+
+constexpr int kGenTile = 128, kGenK = 16, kGenLd = kGenTile + 4;
+
+// Eight consecutive elements of a row from `at` on, zeros from `len` on.
+template <typename T>
+__device__ __forceinline__ void load8(const T* row, int64_t at, int64_t len, float out[8]) {
+  if (row != nullptr && at + 8 <= len && (((uintptr_t)(row + at)) & 15u) == 0) {
+    if (sizeof(T) == 2) {
+      const u32x4 x = *(const u32x4*)(row + at);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        out[2 * e] = bf16_lo(x[e]);
+        out[2 * e + 1] = bf16_hi(x[e]);
+      }
+    } else {
+      const f32x4 x = *(const f32x4*)(row + at), y = *(const f32x4*)(row + at + 4);
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        out[e] = x[e];
+        out[4 + e] = y[e];
+      }
+    }
+    return;
+  }
+#pragma unroll
+  for (int e = 0; e < 8; ++e) out[e] = row != nullptr && at + e < len ? (float)row[at + e] : 0.0f;
+}
+
+struct GenPiece {
+  int64_t v0, len;  // the piece of the vocabulary
+  int first;        // DHIDDEN: the slab holds nothing yet
+};
+
+template <typename T, int MODE>
+__global__ __launch_bounds__(256) void ce_general_kernel(CeArgs a, GenPiece pc) {
+  __shared__ float sA[kGenK * kGenLd], sB[kGenK * kGenLd];
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  const int64_t count = a.head->count;
+  constexpr bool kLogits = MODE == kCeStats || MODE == kCeDs;
+  const int64_t M = kLogits ? pc.len : a.D;
+  const int64_t N = MODE == kCeDweight ? pc.len : count;
+  const int64_t m0 = (int64_t)(MODE == kCeDweight ? blockIdx.y : blockIdx.x) * kGenTile;
+  const int64_t n0 = (int64_t)(MODE == kCeDweight ? blockIdx.x : blockIdx.y) * kGenTile;
+  if (n0 >= N) return;
+  int64_t k_lo = 0, k_hi = kLogits ? a.D : MODE == kCeDhidden ? pc.len : count;
+  if (MODE == kCeDhidden) {  // this split's part of the piece
+    const int64_t part = ((k_hi + a.splits - 1) / a.splits + kGenK - 1) / kGenK * kGenK;
+    k_lo = part * blockIdx.z;
+    k_hi = k_lo + part < k_hi ? k_lo + part : k_hi;
+  }
+  const T* W = (const T*)a.weight + pc.v0 * a.weight_stride;
+  const T* H = (const T*)a.hidden;
+  const float* S = (const float*)a.ds;
+  constexpr bool kAOuter = !kLogits, kBOuter = MODE == kCeDweight;  // k is the row index in memory
+
+  // this thread's eight elements of a tile: along k of one m, or along m of one k
+  const int in_r = tid >> 1, in_k = (tid & 1) * 8;
+  const int out_k = tid >> 4, out_m = (tid & 15) * 8;
+  auto load_a = [&](int64_t k0, float v[8]) {
+    if (!kAOuter) {
+      const int64_t m = m0 + in_r;
+      load8<T>(m < M ? W + m * a.weight_stride : nullptr, k0 + in_k, k_hi, v);
+    } else {
+      const int64_t k = k0 + out_k;
+      const T* row = nullptr;
+      if (k < k_hi)
+        row = MODE == kCeDhidden ? W + k * a.weight_stride : H + (int64_t)a.rows[k].row * a.hidden_stride;
+      load8<T>(row, m0 + out_m, M, v);
+    }
+  };
+  const int64_t bn = n0 + in_r;
+  const T* hrow = kLogits && bn < N ? H + (int64_t)a.rows[bn].row * a.hidden_stride : nullptr;
+  auto load_b = [&](int64_t k0, float v[8]) {
+    if (kLogits) {
+      load8<T>(hrow, k0 + in_k, k_hi, v);
+    } else if (!kBOuter) {
+      load8<float>(bn < N ? S + bn * a.ds_ld : nullptr, k0 + in_k, k_hi, v);
+    } else {
+      const int64_t k = k0 + out_k;
+      load8<float>(k < k_hi ? S + k * a.ds_ld : nullptr, n0 + out_m, N, v);
+    }
+  };
+  auto store = [&](float* s, bool outer, const float v[8]) {
+    if (outer) {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s[out_k * kGenLd + out_m + e] = v[e];
+    } else {
+#pragma unroll
+      for (int e = 0; e < 8; ++e) s[(in_k + e) * kGenLd + in_r] = v[e];
+    }
+  };
+
+  f32x16 acc[2][2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+  const int wm = (wave & 1) * 64, wn = (wave >> 1) * 64;
+  const int fr = lane & 31, fk = lane >> 5;
+
+  float va[8], vb[8];
+  if (k_lo < k_hi) {
+    load_a(k_lo, va);
+    load_b(k_lo, vb);
+  }
+  for (int64_t k0 = k_lo; k0 < k_hi; k0 += kGenK) {
+    store(sA, kAOuter, va);
+    store(sB, kBOuter, vb);
+    __syncthreads();
+    if (k0 + kGenK < k_hi) {
+      load_a(k0 + kGenK, va);
+      load_b(k0 + kGenK, vb);
+    }
+#pragma unroll
+    for (int kk = 0; kk < kGenK; kk += 2) {
+      float fa[2], fb[2];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        fa[i] = sA[(kk + fk) * kGenLd + wm + i * 32 + fr];
+        fb[i] = sB[(kk + fk) * kGenLd + wn + i * 32 + fr];
+      }
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x2f32(fa[i], fb[j], acc[i][j], 0, 0, 0);
+    }
+    __syncthreads();
+  }
+
+  // a lane holds column n = lane % 32 of each product, rows 8 (r / 4) + 4 (lane / 32) + r % 4
+  auto row_of = [&](int i, int r) { return m0 + wm + i * 32 + 8 * (r >> 2) + 4 * fk + (r & 3); };
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int64_t n = n0 + wn + j * 32 + fr;
+    if (kLogits) {
+      CeRow row;
+      row.target = -1;
+      row.a = row.c = row.lse2 = 0.0f;
+      if (n < N) row = a.rows[n];
+      if (MODE == kCeStats) {
+        float m = -__builtin_inff();
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            const int64_t v = row_of(i, r);
+            const float y = acc[i][j][r] * row.a;
+            acc[i][j][r] = y;
+            if (v < M) {
+              m = fmaxf(m, y);
+              if (pc.v0 + v == row.target) a.ytarget[n] = y;
+            }
+          }
+        m = fmaxf(m, __shfl_xor(m, 32, kWave));
+        const float mz = finite_or_zero(m);
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int r = 0; r < 16; ++r)
+            if (row_of(i, r) < M) sum += exp2_fast(acc[i][j][r] - mz);
+        sum += __shfl_xor(sum, 32, kWave);
+        // a slice is a wave's 64 rows of the tile
+        if (fk == 0 && n < N) a.partial[n * a.slices + 2 * (int64_t)blockIdx.x + (wave & 1)] = make_float2(m, sum);
+      } else if (n < N) {
+        float* out = (float*)a.ds + n * a.ds_ld;
+#pragma unroll
+        for (int i = 0; i < 2; ++i)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) {
+            const int64_t v = row_of(i, r);
+            if (v >= M) continue;
+            float p = exp2_fast(fmaf(acc[i][j][r], row.a, -row.lse2));
+            if (pc.v0 + v == row.target) p -= 1.0f;
+            out[v] = p * row.c;
+          }
+      }
+    } else if (n < N) {
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const int64_t m = row_of(i, r);
+          if (m >= M) continue;
+          if (MODE == kCeDhidden) {
+            float* out = a.slab + ((int64_t)blockIdx.z * a.N + n) * a.D + m;
+            *out = pc.first ? acc[i][j][r] : *out + acc[i][j][r];
+          } else {
+            ((T*)a.out_dweight)[(pc.v0 + n) * a.D + m] = (T)(acc[i][j][r] * a.head->gmax);
+          }
+        }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Launches
+// ---------------------------------------------------------------------------
+namespace {
+
+constexpr int64_t kMaxTiles = int64_t(1) << 23;  // of a launch (its threads fit 32 bits)
+constexpr int64_t kPieceBytes = int64_t(1) << 28;  // dz of one piece, about
+
+int64_t tiles(int64_t n, int64_t t) { return (n + t - 1) / t; }
+
+}  // namespace
+
+CePlan cross_entropy_plan(int64_t N, int64_t V, int64_t D, int dtype, bool backward) {
+  CePlan p = {};
+  p.fits = N > 0 && V > 0 && D > 0 && tiles(N, kGenTile) <= 65535 &&
+           (unsigned __int128)tiles(N, kGenTile) * (unsigned __int128)tiles(V > D ? V : D, kGenTile) <= kMaxTiles;
+  if (!p.fits) return p;
+  unsigned __int128 at = sizeof(CeHeader);
+  auto take = [&](unsigned __int128 bytes) {
+    const size_t off = (size_t)at;
+    at += (bytes + 255) / 256 * 256;
+    return off;
+  };
+  typedef unsigned __int128 u128;
+  p.rows = take((u128)N * sizeof(CeRow));
+  p.slices = 2 * tiles(V, kGenTile);
+  p.piece = V;
+  p.splits = 1;
+  if (!backward) {
+    p.ytarget = take((u128)N * 4);
+    p.partial = take((u128)N * p.slices * sizeof(float2));
+  } else {
+    int64_t piece = kPieceBytes / 4 / N / kGenTile * kGenTile;
+    if (piece < 1024) piece = 1024;
+    const int64_t whole = tiles(V, kGenTile) * kGenTile;
+    p.piece = piece < whole ? piece : whole;
+    const int64_t t = tiles(N, kGenTile) * tiles(D, kGenTile);
+    int64_t splits = 512 / t, most = p.piece / 512;
+    if (splits > most) splits = most;
+    p.splits = (int)(splits < 1 ? 1 : splits);
+    p.place = take((u128)N * 4);
+    p.ds = take((u128)N * p.piece * 4);
+    p.slab = take((u128)p.splits * N * D * 4);
+  }
+  if (at > (u128)INT64_MAX) p.fits = false;
+  p.total = (size_t)at;
+  return p;
+}
+
+template <typename T>
+static hipError_t launch_general(const CeArgs& a, bool backward, hipStream_t stream) {
+  const dim3 block(256);
+  const unsigned nt = (unsigned)tiles(a.N, kGenTile), dt = (unsigned)tiles(a.D, kGenTile);
+  if (!backward) {
+    const GenPiece pc = {0, a.V, 1};
+    hipLaunchKernelGGL((ce_general_kernel<T, kCeStats>), dim3((unsigned)tiles(a.V, kGenTile), nt), block, 0, stream, a, pc);
+    hipLaunchKernelGGL(ce_combine_kernel, dim3((unsigned)tiles(a.N, 4)), block, 0, stream, a);
+    return hipGetLastError();
+  }
+  for (int64_t v0 = 0; v0 < a.V; v0 += a.ds_ld) {
+    const GenPiece pc = {v0, a.V - v0 < a.ds_ld ? a.V - v0 : a.ds_ld, v0 == 0};
+    const unsigned vt = (unsigned)tiles(pc.len, kGenTile);
+    hipLaunchKernelGGL((ce_general_kernel<T, kCeDs>), dim3(vt, nt), block, 0, stream, a, pc);
+    if (a.out_dhidden)
+      hipLaunchKernelGGL((ce_general_kernel<T, kCeDhidden>), dim3(dt, nt, (unsigned)a.splits), block, 0, stream, a, pc);
+    if (a.out_dweight)
+      hipLaunchKernelGGL((ce_general_kernel<T, kCeDweight>), dim3(vt, dt), block, 0, stream, a, pc);
+  }
+  if (a.out_dhidden)
+    hipLaunchKernelGGL(ce_dhidden_kernel<sizeof(T) == 2>, dim3((unsigned)a.N), block, 0, stream, a);
+  return hipGetLastError();
+}
+
+hipError_t launch_cross_entropy(const CeArgs& a, int dtype, bool backward, hipStream_t stream) {
+  if (backward) hipLaunchKernelGGL(ce_prep_kernel<true>, dim3(1), dim3(kPrepNT), 0, stream, a);
+  else hipLaunchKernelGGL(ce_prep_kernel<false>, dim3(1), dim3(kPrepNT), 0, stream, a);
+  return dtype == ARCS_DTYPE_BF16 ? launch_general<__bf16>(a, backward, stream)
+                                  : launch_general<float>(a, backward, stream);
+}
+
+}  // namespace arcs

@@ -107,6 +107,23 @@ struct LogprobArgs {
   int32_t* out_status;       // [B] or NULL
 };
 
+// One 4-bit head product (arcs_w4_logits).
+struct W4Args {
+  const uint16_t* hidden;  // bf16
+  int64_t B, D;
+  int64_t hidden_stride;
+  const uint8_t* qweight;
+  int64_t V;
+  int64_t qweight_stride;  // bytes
+  const void* scales;
+  int64_t scale_stride;
+  const uint8_t* zeros;    // or NULL
+  int64_t zero_stride;
+  void* logits;
+  int64_t row_stride;
+};
+hipError_t launch_w4_logits(const W4Args& a, int scale_dtype, int logits_dtype, int group, hipStream_t stream);
+
 hipError_t launch_argmax(const void* logits, int dtype, int64_t B, int64_t V, int64_t stride,
                          bool vec, int32_t* out, hipStream_t stream);
 hipError_t launch_sample(const SampleArgs& a, int dtype, int64_t B, bool vec, hipStream_t stream);

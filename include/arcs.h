@@ -55,7 +55,9 @@ typedef enum arcs_status {
   ARCS_ERR_BAD_CAPACITY = -11,       /* arcs_commit_tokens: capacity 0, or capacity * B too large */
   ARCS_ERR_SCRATCH_TOO_SMALL = -12,  /* arcs_sample_noalloc: the shape needs more than its scratch */
   ARCS_ERR_BAD_BUDGET = -13,         /* arcs_sample_hybrid_nucleus: budget outside [0, 4096] */
-  ARCS_ERR_BAD_DRY = -14             /* arcs_sample_dry: breakers NULL or n_breakers outside [0, 64] */
+  ARCS_ERR_BAD_DRY = -14,            /* arcs_sample_dry: breakers NULL or n_breakers outside [0, 64] */
+  ARCS_ERR_BAD_HIDDEN = -15,         /* hidden size D outside [1, ARCS_MAX_HIDDEN] */
+  ARCS_ERR_BAD_GROUP = -16           /* arcs_w4_logits: group_size not 32, 64 or 128, or no divisor of D */
 } arcs_status;
 
 /* Per-row status codes written to out_status[b] (out_ids[b] = -1 when != 0). */
@@ -68,8 +70,9 @@ enum {
   ARCS_ROW_BAD_FLAGS = 5,            /* flags has a bit other than ARCS_ROW_TIES_WIDE */
   ARCS_ROW_HISTORY_TOO_LONG = 6,     /* penalties active, > ARCS_MAX_HISTORY distinct ids,
                                         and no long-history workspace */
-  ARCS_ROW_VOCAB_TOO_LARGE = 7       /* penalties active, V > ARCS_MAX_PENALTY_VOCAB,
+  ARCS_ROW_VOCAB_TOO_LARGE = 7,      /* penalties active, V > ARCS_MAX_PENALTY_VOCAB,
                                         and no long-history workspace */
+  ARCS_ROW_BAD_TARGET = 8            /* arcs_linear_cross_entropy: target outside [0, V) and not ignore_index */
 };
 
 /* Limits of the penalty tables kept in LDS (per row): distinct history ids
@@ -86,6 +89,9 @@ enum {
   ARCS_FAULT_TOKEN_RANGE = 1,        /* a token outside [0, V) other than -1            */
   ARCS_FAULT_RING_OVERRUN = 2        /* the ring slot still holds a step not drained yet */
 };
+
+/* Largest hidden size of arcs_w4_logits and arcs_linear_cross_entropy. */
+#define ARCS_MAX_HIDDEN 65536
 
 /* Limits of arcs_top_logprobs: entries per row, and V. */
 #define ARCS_MAX_TOP_LOGPROBS 64
@@ -415,6 +421,104 @@ int arcs_top_logprobs(const void* logits, int dtype, int64_t B, int64_t V, int64
 int arcs_commit_tokens(const int32_t* ids, int64_t B, int64_t V, int32_t* next_input, uint64_t* position,
                        int32_t* ring, uint64_t capacity, uint64_t* published, const uint64_t* drained,
                        uint32_t* fault, void* stream);
+
+/*
+ * arcs_w4_logits: the logits arcs_argmax, arcs_sample and arcs_top_logprobs
+ * read, from the last hidden states and a vocabulary head whose weights are
+ * held in 4 bits with a scale for each group of group_size of them:
+ *   logits[b, v] = sum over groups g of
+ *       scales[v, g] * sum over d in g of (q[v, d] - zeros[v, g]) * hidden[b, d]
+ * with q in 0 .. 15 and zeros 8 where `zeros` is NULL.  Products and sums are
+ * held in binary32 (weights and hidden states enter exactly) and each logit is
+ * rounded once to its type.  NaN and infinities in a hidden state or a scale
+ * reach the logits they belong to as in any such sum.
+ *   hidden         device bfloat16 [B, hidden_stride], rows 16-byte aligned
+ *   D              hidden size, 1 .. ARCS_MAX_HIDDEN, a multiple of group_size
+ *   qweight        device bytes [V, qweight_stride], rows 16-byte aligned: byte d / 2
+ *                  holds weight d in its low nibble and weight d + 1 in its high
+ *                  nibble (d even); qweight_stride >= D / 2
+ *   scales         device [V, scale_stride] of scale_dtype (ARCS_DTYPE_BF16 or
+ *                  ARCS_DTYPE_F32), scale_stride >= D / group_size elements
+ *   zeros          device bytes [V, zero_stride], 0 .. 15 each (other values are
+ *                  taken as the number they are), or NULL
+ *   group_size     32, 64 or 128
+ *   logits         device [B, row_stride] of logits_dtype, row_stride >= V
+ * No workspace.  Returns ARCS_OK or a negative arcs_status (nothing launched then):
+ * ARCS_ERR_BAD_STRIDE for any stride below its row, ARCS_ERR_MISALIGNED for
+ * `hidden` or `qweight` rows that are not 16-byte aligned or another array not
+ * aligned to its element, ARCS_ERR_BAD_BATCH for B above ARCS_W4_MAX_BATCH.
+ */
+#define ARCS_W4_MAX_BATCH 524288
+int arcs_w4_logits(const void* hidden, int64_t B, int64_t D, int64_t hidden_stride, const uint8_t* qweight,
+                   int64_t V, int64_t qweight_stride, const void* scales, int scale_dtype,
+                   int64_t scale_stride, const uint8_t* zeros, int64_t zero_stride, int group_size,
+                   void* logits, int logits_dtype, int64_t row_stride, void* stream);
+
+/*
+ * arcs_linear_cross_entropy: the log-probabilities of given tokens, or the
+ * training loss, straight from the hidden states and the vocabulary head; the
+ * [N, V] logits are never kept.  Per row n, at temperature T = temperature[n]
+ * (1 when `temperature` is NULL):
+ *   z_v = dot(hidden[n], weight[v]) / T,
+ *   out_lse[n] = ln sum_v exp(z_v),   out_loss[n] = out_lse[n] - z_target[n],
+ * so -out_loss is the target's log-probability, as arcs_top_logprobs reports
+ * it for the logits' distribution.  Rows whose target is ignore_index (which
+ * may be any value) are left out: loss and lse 0, and their hidden states are
+ * not read.  Rows whose target is outside [0, V), or whose T is NaN, <= 0 or
+ * +inf, get loss and lse NaN and a row status.  Other NaN and infinities
+ * propagate: a row with a NaN or +inf logit has a NaN loss.
+ *   hidden      device [N, hidden_stride] of dtype (ARCS_DTYPE_BF16 or
+ *               ARCS_DTYPE_F32), hidden_stride >= D, D in 1 .. ARCS_MAX_HIDDEN
+ *   weight      device [V, weight_stride] of the same dtype, weight_stride >= D
+ *   targets     device int32[N]
+ *   temperature device float[N], or NULL
+ *   out_loss    device float[N]
+ *   out_lse     device float[N] (arcs_linear_cross_entropy_backward reads it)
+ *   out_status  device int32[N]: ARCS_ROW_OK, ARCS_ROW_BAD_TARGET or
+ *               ARCS_ROW_BAD_TEMPERATURE; or NULL
+ *   workspace   device scratch of at least
+ *               arcs_linear_cross_entropy_workspace_bytes(N, V, D, dtype, 0),
+ *               256-byte aligned, not read before it is written; calls that share
+ *               one must be ordered on one stream
+ * Products and sums are held in binary32.  The same call gives the same bits.
+ * bfloat16 rows that are 16-byte aligned (both arrays, D % 8 == 0) take the
+ * matrix kernels; others a general kernel, slower by a factor.
+ * Returns ARCS_OK or a negative arcs_status (nothing launched then);
+ * ARCS_ERR_BAD_BATCH also where the call has more than 2^23 tiles of 128 x 128
+ * logits or N exceeds 2^23.
+ */
+int arcs_linear_cross_entropy(const void* hidden, int64_t hidden_stride, const void* weight,
+                              int64_t weight_stride, int dtype, int64_t N, int64_t V, int64_t D,
+                              const int32_t* targets, int32_t ignore_index, const float* temperature,
+                              float* out_loss, float* out_lse, int32_t* out_status, void* workspace,
+                              size_t workspace_bytes, void* stream);
+
+/*
+ * arcs_linear_cross_entropy_backward: the gradients of
+ * sum_n grad_loss[n] * out_loss[n] of the call above.  With p = softmax(z_n)
+ * computed again from out_lse, in pieces of the vocabulary:
+ *   dz[n, v] = (p_v - [v == target]) * grad_loss[n] / T,
+ *   out_dhidden[n] = sum_v dz[n, v] * weight[v],
+ *   out_dweight[v] = sum_n dz[n, v] * hidden[n].
+ * Rows that are ignored or refused have a zero gradient and add nothing.
+ *   lse          device float[N], out_lse of the forward call on the same inputs
+ *   grad_loss    device float[N]
+ *   out_dhidden  device [N, D] of dtype, dense, or NULL (not wanted)
+ *   out_dweight  device [V, D] of dtype, dense, or NULL (not wanted); written
+ *                whole, not added to.  One of the two must be given.
+ *   workspace    arcs_linear_cross_entropy_workspace_bytes(N, V, D, dtype, 1)
+ * Sums are held in binary32.  The matrix kernels hold dz of a piece in
+ * bfloat16, in units of the largest |grad_loss / T| of the call.  Other
+ * arguments and errors as the forward call; outputs must not overlap inputs.
+ */
+int arcs_linear_cross_entropy_backward(const void* hidden, int64_t hidden_stride, const void* weight,
+                                       int64_t weight_stride, int dtype, int64_t N, int64_t V, int64_t D,
+                                       const int32_t* targets, int32_t ignore_index, const float* temperature,
+                                       const float* lse, const float* grad_loss, void* out_dhidden,
+                                       void* out_dweight, void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace the two calls above need (0 for sizes they refuse). */
+size_t arcs_linear_cross_entropy_workspace_bytes(int64_t N, int64_t V, int64_t D, int dtype, int backward);
 
 /* Library version, major * 10000 + minor * 100 + patch. */
 int arcs_version(void);
