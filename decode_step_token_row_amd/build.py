@@ -25,7 +25,8 @@ LIB = os.path.join(PKG, "libarcs.so")
 BUILD_DIR = os.path.join(PKG, "_build")
 
 SOURCES = ["api.hip", "argmax_kernel.hip", "sample_kernel.hip", "logprobs_kernel.hip", "commit_kernel.hip",
-           "hybrid_kernel.hip", "w4_kernel.hip", "cross_entropy_kernel.hip"]
+           "hybrid_kernel.hip", "w4_kernel.hip", "cross_entropy_kernel.hip",
+           "cross_entropy_mfma.hip"]
 ARCH = os.environ.get("ARCS_OFFLOAD_ARCH", "gfx950")
 
 COMMON = [

@@ -1,0 +1,41 @@
+// Device-side pieces the linear cross entropy's kernels share.
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "cross_entropy.hpp"
+#include "device_common.hpp"
+
+namespace arcs {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x4 __attribute__((ext_vector_type(4)));
+
+constexpr float kLog2e = 1.44269504088896340736f;
+constexpr float kLn2 = 0.69314718055994530942f;
+
+__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
+__device__ __forceinline__ float finite_or_zero(float m) { return m == -__builtin_inff() ? 0.0f : m; }
+
+// The products, C[m, n] = sum_k A[m, k] B[n, k]:
+//   STATS    m: vocabulary, n: listed rows, k: D    maximum and sum per slice
+//   DS       the same                               dz / gmax of the piece
+//   DHIDDEN  m: D, n: listed rows, k: the piece     adds to the split's slab
+//   DWEIGHT  m: D, n: the piece, k: listed rows     rows of dweight
+enum CeMode { kCeStats, kCeDs, kCeDhidden, kCeDweight };
+
+struct CePiece {
+  int64_t v0, len;  // the piece of the vocabulary
+  int first;        // DHIDDEN: the slab holds nothing yet
+  int gather;       // matrix kernels: hidden states are read through the row list
+};
+
+// cross_entropy_kernel.hip
+void launch_cross_entropy_combine(const CeArgs& a, hipStream_t stream);
+void launch_cross_entropy_dhidden(const CeArgs& a, bool bf16, hipStream_t stream);
+// cross_entropy_mfma.hip
+bool cross_entropy_matrix_path(const CeArgs& a, int dtype, bool backward);
+hipError_t launch_cross_entropy_matrix(const CeArgs& a, bool backward, hipStream_t stream);
+
+}  // namespace arcs

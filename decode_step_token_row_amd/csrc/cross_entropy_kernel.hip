@@ -7,19 +7,10 @@
 #include <stdint.h>
 
 #include "cross_entropy.hpp"
-#include "device_common.hpp"
+#include "cross_entropy_device.hpp"
 #include "launch.hpp"
 
 namespace arcs {
-
-typedef float f32x16 __attribute__((ext_vector_type(16)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-
-constexpr float kLog2e = 1.44269504088896340736f;
-constexpr float kLn2 = 0.69314718055994530942f;
-
-__device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
-__device__ __forceinline__ float finite_or_zero(float m) { return m == -__builtin_inff() ? 0.0f : m; }
 
 // ---------------------------------------------------------------------------
 // The row list.  One workgroup: rows keep their order, so sums over rows do
@@ -154,13 +145,7 @@ __global__ __launch_bounds__(256) void ce_dhidden_kernel(CeArgs a) {
 // The general matrix kernel: C[m, n] = sum_k A[m, k] B[n, k] on 128 x 128
 // tiles, four waves of 64 x 64 (two by two 32x32x2 float32 products), 16 k at
 // a time through LDS.
-//   STATS    m: vocabulary, n: listed rows, k: D    maximum and sum per tile
-//   DS       the same                               dz / gmax of the piece
-//   DHIDDEN  m: D, n: listed rows, k: the piece     adds to the split's slab
-//   DWEIGHT  m: D, n: the piece, k: listed rows     rows of dweight
 // ---------------------------------------------------------------------------
-enum CeMode { kCeStats, kCeDs, kCeDhidden, kCeDweight };
-
 constexpr int kGenTile = 128, kGenK = 16, kGenLd = kGenTile + 4;
 
 // Eight consecutive elements of a row from `at` on, zeros from `len` on.
@@ -188,13 +173,8 @@ __device__ __forceinline__ void load8(const T* row, int64_t at, int64_t len, flo
   for (int e = 0; e < 8; ++e) out[e] = row != nullptr && at + e < len ? (float)row[at + e] : 0.0f;
 }
 
-struct GenPiece {
-  int64_t v0, len;  // the piece of the vocabulary
-  int first;        // DHIDDEN: the slab holds nothing yet
-};
-
 template <typename T, int MODE>
-__global__ __launch_bounds__(256) void ce_general_kernel(CeArgs a, GenPiece pc) {
+__global__ __launch_bounds__(256) void ce_general_kernel(CeArgs a, CePiece pc) {
   __shared__ float sA[kGenK * kGenLd], sB[kGenK * kGenLd];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t count = a.head->count;
@@ -364,6 +344,7 @@ namespace {
 
 constexpr int64_t kMaxTiles = int64_t(1) << 23;  // of a launch (its threads fit 32 bits)
 constexpr int64_t kPieceBytes = int64_t(1) << 28;  // dz of one piece, about
+constexpr int64_t kMaxPiece = int64_t(1) << 24;  // 64 rows of dz lie within 2^31 bytes
 
 int64_t tiles(int64_t n, int64_t t) { return (n + t - 1) / t; }
 
@@ -381,17 +362,20 @@ CePlan cross_entropy_plan(int64_t N, int64_t V, int64_t D, int dtype, bool backw
     return off;
   };
   typedef unsigned __int128 u128;
+  const bool bf16 = dtype == ARCS_DTYPE_BF16;
   p.rows = take((u128)N * sizeof(CeRow));
-  p.slices = 2 * tiles(V, kGenTile);
-  p.piece = V;
+  if (bf16) p.hc = take((u128)N * D * 2);
   p.splits = 1;
   if (!backward) {
+    p.slices = 8 * tiles(V, 256);
     p.ytarget = take((u128)N * 4);
     p.partial = take((u128)N * p.slices * sizeof(float2));
   } else {
-    int64_t piece = kPieceBytes / 4 / N / kGenTile * kGenTile;
+    // dz of a piece: bfloat16 in the matrix kernels, float32 in the general one
+    int64_t piece = kPieceBytes / 4 / N / 256 * 256;
     if (piece < 1024) piece = 1024;
-    const int64_t whole = tiles(V, kGenTile) * kGenTile;
+    if (piece > kMaxPiece) piece = kMaxPiece;
+    const int64_t whole = tiles(V, 256) * 256;
     p.piece = piece < whole ? piece : whole;
     const int64_t t = tiles(N, kGenTile) * tiles(D, kGenTile);
     int64_t splits = 512 / t, most = p.piece / 512;
@@ -406,18 +390,28 @@ CePlan cross_entropy_plan(int64_t N, int64_t V, int64_t D, int dtype, bool backw
   return p;
 }
 
+void launch_cross_entropy_combine(const CeArgs& a, hipStream_t stream) {
+  hipLaunchKernelGGL(ce_combine_kernel, dim3((unsigned)tiles(a.N, 4)), dim3(256), 0, stream, a);
+}
+
+void launch_cross_entropy_dhidden(const CeArgs& a, bool bf16, hipStream_t stream) {
+  if (bf16) hipLaunchKernelGGL(ce_dhidden_kernel<true>, dim3((unsigned)a.N), dim3(256), 0, stream, a);
+  else hipLaunchKernelGGL(ce_dhidden_kernel<false>, dim3((unsigned)a.N), dim3(256), 0, stream, a);
+}
+
 template <typename T>
-static hipError_t launch_general(const CeArgs& a, bool backward, hipStream_t stream) {
+static hipError_t launch_general(CeArgs a, bool backward, hipStream_t stream) {
   const dim3 block(256);
   const unsigned nt = (unsigned)tiles(a.N, kGenTile), dt = (unsigned)tiles(a.D, kGenTile);
   if (!backward) {
-    const GenPiece pc = {0, a.V, 1};
+    const CePiece pc = {0, a.V, 1, 0};
+    a.slices = 2 * tiles(a.V, kGenTile);
     hipLaunchKernelGGL((ce_general_kernel<T, kCeStats>), dim3((unsigned)tiles(a.V, kGenTile), nt), block, 0, stream, a, pc);
-    hipLaunchKernelGGL(ce_combine_kernel, dim3((unsigned)tiles(a.N, 4)), block, 0, stream, a);
+    launch_cross_entropy_combine(a, stream);
     return hipGetLastError();
   }
   for (int64_t v0 = 0; v0 < a.V; v0 += a.ds_ld) {
-    const GenPiece pc = {v0, a.V - v0 < a.ds_ld ? a.V - v0 : a.ds_ld, v0 == 0};
+    const CePiece pc = {v0, a.V - v0 < a.ds_ld ? a.V - v0 : a.ds_ld, v0 == 0, 0};
     const unsigned vt = (unsigned)tiles(pc.len, kGenTile);
     hipLaunchKernelGGL((ce_general_kernel<T, kCeDs>), dim3(vt, nt), block, 0, stream, a, pc);
     if (a.out_dhidden)
@@ -425,14 +419,14 @@ static hipError_t launch_general(const CeArgs& a, bool backward, hipStream_t str
     if (a.out_dweight)
       hipLaunchKernelGGL((ce_general_kernel<T, kCeDweight>), dim3(vt, dt), block, 0, stream, a, pc);
   }
-  if (a.out_dhidden)
-    hipLaunchKernelGGL(ce_dhidden_kernel<sizeof(T) == 2>, dim3((unsigned)a.N), block, 0, stream, a);
+  if (a.out_dhidden) launch_cross_entropy_dhidden(a, sizeof(T) == 2, stream);
   return hipGetLastError();
 }
 
 hipError_t launch_cross_entropy(const CeArgs& a, int dtype, bool backward, hipStream_t stream) {
   if (backward) hipLaunchKernelGGL(ce_prep_kernel<true>, dim3(1), dim3(kPrepNT), 0, stream, a);
   else hipLaunchKernelGGL(ce_prep_kernel<false>, dim3(1), dim3(kPrepNT), 0, stream, a);
+  if (cross_entropy_matrix_path(a, dtype, backward)) return launch_cross_entropy_matrix(a, backward, stream);
   return dtype == ARCS_DTYPE_BF16 ? launch_general<__bf16>(a, backward, stream)
                                   : launch_general<float>(a, backward, stream);
 }

@@ -1,0 +1,425 @@
+// Linear cross entropy on the bfloat16 matrix instruction.
+//
+// One tile kernel runs the four products of the general kernel (STATS, DS,
+// DHIDDEN, DWEIGHT) on rows that are 16-byte aligned: C[m, n] = sum_k A[m, k]
+// B[n, k], 64 k at a time.  Tiles go from memory to LDS by the buffer loads
+// that write LDS directly, S tiles deep, one barrier a tile.  An operand whose
+// rows run along k is read back 16 bytes a lane; one whose rows run along m or
+// n (the head in DHIDDEN, both operands in DWEIGHT) through the transposing
+// LDS read, so no operand is stored twice.  The load writes LDS in lane order,
+// so bank conflicts are avoided by permuting the lanes' global addresses:
+//   along k: a row's 128 bytes are 8 chunks, chunk c of row r at c ^ (r / 2 % 8);
+//   along m: a row's 32-byte chunks, chunk q of row k at q ^ 2 (k % 4).
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "cross_entropy.hpp"
+#include "cross_entropy_device.hpp"
+#include "launch.hpp"
+
+namespace arcs {
+
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef short s16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
+typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
+
+#define ARCS_LDS __attribute__((address_space(3)))
+
+constexpr int kTK = 64;                         // k of one tile
+constexpr uint32_t kNoLoad = 0x80000000u;       // an offset past every buffer: the load gives zeros
+constexpr uint32_t kBufMost = 0x7FFFFFF0u;
+
+// A buffer descriptor of `bytes` bytes from p (raw, bounds checked).
+__device__ __forceinline__ u32x4 buffer_of(const void* p, int64_t bytes) {
+  const uint64_t b = (uint64_t)p;
+  u32x4 d;
+  d[0] = (uint32_t)b;
+  d[1] = (uint32_t)(b >> 32) & 0xFFFFu;
+  d[2] = bytes < 0 ? 0u : bytes > (int64_t)kBufMost ? kBufMost : (uint32_t)bytes;
+  d[3] = 0x00020000u;
+  return d;
+}
+
+// 16 bytes a lane from descriptor + offset to LDS at `to` + 16 * lane.  The
+// wait is the caller's (vmcnt).  The wait states cover a descriptor or m0
+// written just before.
+__device__ __forceinline__ void load_to_lds(uint32_t to, uint32_t off, u32x4 from) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(to), "v"(off), "s"(from)
+               : "memory", "m0");
+}
+
+template <int N>
+__device__ __forceinline__ void wait_loads() {
+  asm volatile("s_waitcnt vmcnt(%0)" ::"n"(N) : "memory");
+}
+__device__ __forceinline__ void wait_lds() { asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory"); }
+
+__device__ __forceinline__ u32x4 uniform4(u32x4 d) {
+#pragma unroll
+  for (int e = 0; e < 4; ++e) d[e] = __builtin_amdgcn_readfirstlane(d[e]);
+  return d;
+}
+
+template <int MODE, int WM, int WN, int MT, int NT, int S>
+struct CeTile {
+  static constexpr int kThreads = WM * WN * 64, kWaves = WM * WN;
+  static constexpr int BM = WM * MT * 32, BN = WN * NT * 32;
+  static constexpr bool kLogits = MODE == kCeStats || MODE == kCeDs;
+  static constexpr bool kAOuter = !kLogits, kBOuter = MODE == kCeDweight;
+  static constexpr int kABytes = BM * kTK * 2, kBBytes = BN * kTK * 2, kStage = kABytes + kBBytes;
+  static constexpr int kALoads = BM / 8, kBLoads = BN / 8;  // of 1024 bytes each
+  static constexpr int kAPer = (kALoads + kWaves - 1) / kWaves, kBPer = (kBLoads + kWaves - 1) / kWaves;
+  static constexpr int kPer = kAPer + kBPer;
+  static constexpr int kOut = MODE == kCeDs || MODE == kCeDweight ? BM * BN * 2 : 0;
+  static constexpr int kLds = S * kStage > kOut ? S * kStage : kOut;
+};
+
+// Where a lane's 16 bytes of load `inst` lie in its tile: row and element in the row.
+template <int W>
+__device__ __forceinline__ void outer_place(int inst, int lane, int& k, int& col) {
+  constexpr int kLanes = W / 8;
+  k = inst * (64 / kLanes) + lane / kLanes;
+  const int p = lane % kLanes;
+  const int turn = W >= 128 ? (k & 3) << 1 : W == 64 ? ((k >> 1) & 1) << 1 : 0;
+  col = ((p >> 1) ^ turn) * 16 + (p & 1) * 8;
+}
+__device__ __forceinline__ void inner_place(int inst, int lane, int& r, int& k) {
+  r = inst * 8 + (lane >> 3);
+  k = ((lane & 7) ^ ((r >> 1) & 7)) * 8;
+}
+
+template <int MODE, int WM, int WN, int MT, int NT, int S>
+__global__ __launch_bounds__(WM* WN * 64) void ce_tile_kernel(CeArgs a, CePiece pc) {
+  using C = CeTile<MODE, WM, WN, MT, NT, S>;
+  constexpr int BM = C::BM, BN = C::BN;
+  __shared__ __align__(1024) char lds[C::kLds];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int64_t count = a.head->count;
+  const int64_t M = C::kLogits ? pc.len : a.D;
+  const int64_t N = MODE == kCeDweight ? pc.len : count;
+
+  // The tile of this workgroup.  Workgroups go round the eight dies in turn; a
+  // die gets neighbouring tiles, eight along m by some along n, which share
+  // their operands in its L2.
+  int64_t m0, n0;
+  int split;
+  {
+    const int mt = (int)((M + BM - 1) / BM), nt = (int)((N + BN - 1) / BN);
+    const int per = mt * nt, all = per * (MODE == kCeDhidden ? a.splits : 1);
+    const int chunk = (all + 7) / 8;
+    const int at = ((int)blockIdx.x & 7) * chunk + ((int)blockIdx.x >> 3);
+    if (((int)blockIdx.x >> 3) >= chunk || at >= all) return;
+    split = at / per;
+    const int id = at - split * per, band = id / (8 * nt), in = id - band * 8 * nt;
+    const int high = mt - band * 8 < 8 ? mt - band * 8 : 8;
+    m0 = (int64_t)(band * 8 + in % high) * BM;
+    n0 = (int64_t)(in / high) * BN;
+  }
+  int64_t k_lo = 0, k_hi = C::kLogits ? a.D : MODE == kCeDhidden ? pc.len : count;
+  if (MODE == kCeDhidden) {
+    const int64_t part = ((k_hi + a.splits - 1) / a.splits + kTK - 1) / kTK * kTK;
+    k_lo = part * split;
+    k_hi = k_lo + part < k_hi ? k_lo + part : k_hi;
+  }
+  const int nk = k_hi > k_lo ? (int)((k_hi - k_lo + kTK - 1) / kTK) : 0;
+
+  // descriptors at k_lo, and the lanes' offsets in a tile
+  const uint16_t* W = (const uint16_t*)a.weight + pc.v0 * a.weight_stride;
+  const uint16_t* H = (const uint16_t*)(pc.gather ? a.hidden : a.hc);
+  const uint16_t* Z = (const uint16_t*)a.ds;
+  const char *pa, *pb;
+  int64_t na = kBufMost, nb = kBufMost, step_a = kTK * 2, step_b = kTK * 2;
+  uint32_t oa[C::kAPer], ob[C::kBPer];
+  uint32_t ka[C::kAPer], kb[C::kBPer];  // along k: the lane's first element's k in a tile
+#pragma unroll
+  for (int t = 0; t < C::kAPer; ++t) {
+    const int inst = (wave + t * C::kWaves) % C::kALoads;
+    int r, c;
+    if (!C::kAOuter) {
+      inner_place(inst, lane, r, c);
+      const int64_t left = M - 1 - m0;
+      oa[t] = (uint32_t)((r < left ? r : left) * a.weight_stride * 2 + c * 2);
+      ka[t] = (uint32_t)c;
+    } else {
+      outer_place<BM>(inst, lane, r, c);
+      const int64_t ld = MODE == kCeDhidden ? a.weight_stride : a.D;
+      oa[t] = m0 + c < M ? (uint32_t)(r * ld * 2 + c * 2) : kNoLoad;
+      ka[t] = 0;
+    }
+  }
+#pragma unroll
+  for (int t = 0; t < C::kBPer; ++t) {
+    const int inst = (wave + t * C::kWaves) % C::kBLoads;
+    int r, c;
+    if (!C::kBOuter) {
+      inner_place(inst, lane, r, c);
+      const int64_t left = N - 1 - n0, n = r < left ? r : left;
+      if (C::kLogits) ob[t] = (uint32_t)((pc.gather ? (int64_t)a.rows[n0 + n].row * a.hidden_stride : n * a.D) * 2 + c * 2);
+      else ob[t] = (uint32_t)(n * a.ds_ld * 2 + c * 2);
+      kb[t] = (uint32_t)c;
+    } else {
+      outer_place<BN>(inst, lane, r, c);
+      ob[t] = (uint32_t)(r * a.ds_ld * 2 + c * 2);
+      kb[t] = 0;
+    }
+  }
+  if (C::kLogits) {
+    pa = (const char*)(W + m0 * a.weight_stride);
+    pb = (const char*)(pc.gather ? H : H + n0 * a.D);
+  } else if (MODE == kCeDhidden) {
+    pa = (const char*)(W + k_lo * a.weight_stride + m0);
+    na = ((pc.len - k_lo) * a.weight_stride - m0) * 2;
+    step_a = kTK * a.weight_stride * 2;
+    pb = (const char*)(Z + n0 * a.ds_ld + k_lo);
+  } else {
+    pa = (const char*)(H + m0);
+    na = (count * a.D - m0) * 2;
+    step_a = kTK * a.D * 2;
+    pb = (const char*)(Z + n0);
+    nb = (count * a.ds_ld - n0) * 2;
+    step_b = kTK * a.ds_ld * 2;
+  }
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(ARCS_LDS char*)lds;
+
+  auto issue = [&](int kt) {
+    const uint32_t to = lds0 + (uint32_t)(kt % S) * C::kStage;
+    const u32x4 da = uniform4(buffer_of(pa + kt * step_a, C::kAOuter ? na - kt * step_a : (int64_t)kBufMost));
+    const u32x4 db = uniform4(buffer_of(pb + kt * step_b, C::kBOuter ? nb - kt * step_b : (int64_t)kBufMost));
+    // logits: the columns of the last tile past D are zeros
+    const uint32_t left = C::kLogits ? (uint32_t)(a.D - (int64_t)kt * kTK < kTK ? a.D - (int64_t)kt * kTK : kTK) : kTK;
+#pragma unroll
+    for (int t = 0; t < C::kAPer; ++t)
+      load_to_lds(to + ((wave + t * C::kWaves) % C::kALoads) * 1024u, C::kLogits && ka[t] >= left ? kNoLoad : oa[t], da);
+#pragma unroll
+    for (int t = 0; t < C::kBPer; ++t)
+      load_to_lds(to + C::kABytes + ((wave + t * C::kWaves) % C::kBLoads) * 1024u,
+                  C::kLogits && kb[t] >= left ? kNoLoad : ob[t], db);
+  };
+
+  f32x16 acc[MT][NT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+#pragma unroll
+      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+
+  const int wm = (wave % WM) * MT * 32, wn = (wave / WM) * NT * 32;
+  const int fr = lane & 31, fh = lane >> 5;
+  // fragment of 32 rows from `at` at k step ks of a stage
+  auto frag_inner = [&](const char* s, int at, int ks) {
+    return *(const bf16x8*)(s + (at + fr) * 128 + (((ks * 2 + fh) ^ ((lane >> 1) & 7)) * 16));
+  };
+  auto frag_outer = [&](const char* s, int width, int at, int ks) {
+    const int k = ks * 16 + fh * 8 + ((lane & 15) >> 2);
+    const int turn = width >= 128 ? (k & 3) << 1 : width == 64 ? ((k >> 1) & 1) << 1 : 0;
+    const char* p = s + k * width * 2 + (((at >> 4) + ((lane >> 4) & 1)) ^ turn) * 32 + (lane & 3) * 8;
+    const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((ARCS_LDS s16x4*)p);
+    const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((ARCS_LDS s16x4*)(p + 4 * width * 2));
+    return __builtin_bit_cast(bf16x8, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
+  };
+
+#pragma unroll
+  for (int s = 0; s < S - 1; ++s)
+    if (s < nk) issue(s);
+  for (int kt = 0; kt < nk; ++kt) {
+    // tile kt has landed: at most the S - 2 tiles after it are on their way
+    if (kt + S - 2 < nk) wait_loads<(S - 2) * C::kPer>();
+    else wait_loads<0>();
+    wait_lds();  // this wave's reads of the stage that is filled next are done
+    __builtin_amdgcn_s_barrier();
+    if (kt + S - 1 < nk) issue(kt + S - 1);
+    const char* sa = lds + (kt % S) * C::kStage;
+    const char* sb = sa + C::kABytes;
+#pragma unroll
+    for (int ks = 0; ks < 4; ++ks) {
+      bf16x8 fa[MT], fb[NT];
+#pragma unroll
+      for (int i = 0; i < MT; ++i) fa[i] = C::kAOuter ? frag_outer(sa, BM, wm + i * 32, ks) : frag_inner(sa, wm + i * 32, ks);
+#pragma unroll
+      for (int j = 0; j < NT; ++j) fb[j] = C::kBOuter ? frag_outer(sb, BN, wn + j * 32, ks) : frag_inner(sb, wn + j * 32, ks);
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < NT; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[i], fb[j], acc[i][j], 0, 0, 0);
+    }
+  }
+
+  // A lane holds column n = lane % 32 of each 32 x 32 product and rows
+  // 8 (r / 4) + 4 (lane / 32) + r % 4: in the lane's wave, row_of + mw of the tile.
+  auto row_of = [](int i, int r) { return i * 32 + 8 * (r >> 2) + (r & 3); };
+  const int mw = wm + 4 * fh;
+  const int m_left = (int)(M - m0 < BM ? M - m0 : BM) - mw;  // rows of the lane that exist
+  if (MODE == kCeStats) {
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const int64_t n = n0 + wn + j * 32 + fr;
+      CeRow row;
+      row.target = -1;
+      row.a = 0.0f;
+      if (n < N) row = a.rows[n];
+      const int64_t to_target = (int64_t)row.target - m0 - mw;
+      const int target = to_target >= 0 && to_target < m_left ? (int)to_target : -1;
+      float m = -__builtin_inff(), yt = 0.0f;
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) {
+          const float y = acc[i][j][r] * row.a;
+          acc[i][j][r] = row_of(i, r) < m_left ? y : -__builtin_inff();
+          m = fmaxf(m, acc[i][j][r]);
+          yt = row_of(i, r) == target ? y : yt;
+        }
+      // target is one of the lane's 16 MT rows, not one between them
+      if (target >= 0 && (target & 4) == 0 && target < MT * 32) a.ytarget[n] = yt;
+      m = fmaxf(m, __shfl_xor(m, 32, kWave));
+      const float mz = finite_or_zero(m);
+      float sum = 0.0f;
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int r = 0; r < 16; ++r) sum += exp2_fast(acc[i][j][r] - mz);
+      sum += __shfl_xor(sum, 32, kWave);
+      // a slice is a wave's rows of the tile
+      if (fh == 0 && n < N) a.partial[n * a.slices + m0 / BM * WM + wave % WM] = make_float2(m, sum);
+    }
+    return;
+  }
+  if (MODE == kCeDhidden) {
+#pragma unroll
+    for (int j = 0; j < NT; ++j) {
+      const int64_t n = n0 + wn + j * 32 + fr;
+      if (n >= N) continue;
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          if (row_of(i, q * 4) >= m_left) continue;
+          f32x4* out = (f32x4*)(a.slab + ((int64_t)split * a.N + n) * a.D + m0 + mw + row_of(i, q * 4));
+          f32x4 v = {acc[i][j][q * 4], acc[i][j][q * 4 + 1], acc[i][j][q * 4 + 2], acc[i][j][q * 4 + 3]};
+          if (!pc.first) v += *out;
+          *out = v;
+        }
+    }
+    return;
+  }
+  // bfloat16 results: through LDS as [n][BM], so that a row is stored whole.
+  // 16-byte chunk c of row n at c ^ (n % 32).
+  wait_loads<0>();
+  wait_lds();
+  __builtin_amdgcn_s_barrier();
+  const float g = MODE == kCeDweight ? a.head->gmax : 0.0f;
+#pragma unroll
+  for (int j = 0; j < NT; ++j) {
+    const int nl = wn + j * 32 + fr;
+    const int64_t n = n0 + nl;
+    CeRow row;
+    row.target = -1;
+    row.a = row.c = row.lse2 = 0.0f;
+    if (MODE == kCeDs && n < N) row = a.rows[n];
+    const int64_t to_target = (int64_t)row.target - pc.v0 - m0 - mw;
+    const int target = to_target >= 0 && to_target < BM ? (int)to_target : -1;
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int q = 0; q < 4; ++q) {
+        bf16x4 out;
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float v = acc[i][j][q * 4 + e];
+          if (MODE == kCeDs) {
+            const int id = row_of(i, q * 4 + e);
+            v = exp2_fast(fmaf(v, row.a, -row.lse2));
+            v = id == target ? v - 1.0f : v;
+            v = id < m_left ? v * row.c : 0.0f;
+          } else {
+            v *= g;
+          }
+          out[e] = (__bf16)v;
+        }
+        const int ml = mw + row_of(i, q * 4);
+        *(bf16x4*)(lds + nl * (BM * 2) + (((ml >> 3) ^ (nl & 31)) * 16) + (ml & 4) * 2) = out;
+      }
+  }
+  wait_lds();
+  __builtin_amdgcn_s_barrier();
+  constexpr int kChunks = BM / 8;
+  for (int t = tid; t < BN * kChunks; t += C::kThreads) {
+    const int nl = t / kChunks, c = t % kChunks;
+    const int64_t n = n0 + nl, m = m0 + c * 8;
+    if (n >= N) continue;
+    const u32x4 v = *(const u32x4*)(lds + nl * (BM * 2) + ((c ^ (nl & 31)) * 16));
+    if (MODE == kCeDs) *(u32x4*)((uint16_t*)a.ds + n * a.ds_ld + m) = v;
+    else if (m < M) *(u32x4*)((uint16_t*)a.out_dweight + (pc.v0 + n) * a.D + m) = v;
+  }
+}
+
+// The hidden states of the listed rows, one after the other.
+__global__ __launch_bounds__(256) void ce_copy_kernel(CeArgs a) {
+  const int64_t i = blockIdx.x;
+  if (i >= a.head->count) return;
+  const u32x4* from = (const u32x4*)((const uint16_t*)a.hidden + (int64_t)a.rows[i].row * a.hidden_stride);
+  u32x4* to = (u32x4*)((uint16_t*)a.hc + i * a.D);
+  for (int64_t c = threadIdx.x; c < a.D / 8; c += 256) to[c] = from[c];
+}
+
+namespace {
+
+int64_t tiles(int64_t n, int64_t t) { return (n + t - 1) / t; }
+
+template <int MODE, int WM, int WN, int MT, int NT, int S>
+void launch_tile(const CeArgs& a, const CePiece& pc, hipStream_t stream) {
+  using C = CeTile<MODE, WM, WN, MT, NT, S>;
+  const int64_t m = C::kLogits ? pc.len : a.D, n = MODE == kCeDweight ? pc.len : a.N;
+  const int64_t all = tiles(m, C::BM) * tiles(n, C::BN) * (MODE == kCeDhidden ? a.splits : 1);
+  hipLaunchKernelGGL((ce_tile_kernel<MODE, WM, WN, MT, NT, S>), dim3((unsigned)(8 * tiles(all, 8))), dim3(C::kThreads), 0,
+                     stream, a, pc);
+}
+
+template <int MODE>
+void launch_rows(const CeArgs& a, const CePiece& pc, hipStream_t stream) {
+  if constexpr (MODE != kCeDweight) {
+    if (a.N <= 32) return launch_tile<MODE, 8, 1, 1, 1, 4>(a, pc, stream);
+    if (a.N <= 64) return launch_tile<MODE, 4, 2, 2, 1, 3>(a, pc, stream);
+    if (a.N <= 128) return launch_tile<MODE, 4, 2, 2, 2, 3>(a, pc, stream);
+  }
+  launch_tile<MODE, 2, 4, 4, 2, 2>(a, pc, stream);
+}
+
+}  // namespace
+
+bool cross_entropy_matrix_path(const CeArgs& a, int dtype, bool backward) {
+  if (dtype != ARCS_DTYPE_BF16 || a.D % 8 != 0) return false;
+  const int64_t most = int64_t(1) << 22;  // a tile's rows lie within 2^31 bytes
+  if (a.hidden_stride % 8 != 0 || a.weight_stride % 8 != 0 || a.weight_stride >= most) return false;
+  if (((uintptr_t)a.hidden | (uintptr_t)a.weight | (uintptr_t)a.out_dweight) & 15u) return false;
+  return true;
+}
+
+hipError_t launch_cross_entropy_matrix(const CeArgs& args, bool backward, hipStream_t stream) {
+  CeArgs a = args;
+  CePiece pc = {0, a.V, 1, 0};
+  // forward: rows are read where they are if one descriptor reaches them all
+  pc.gather = !backward && (unsigned __int128)a.N * (unsigned __int128)a.hidden_stride * 2 < kBufMost;
+  if (!pc.gather) hipLaunchKernelGGL(ce_copy_kernel, dim3((unsigned)a.N), dim3(256), 0, stream, a);
+  if (!backward) {
+    a.slices = tiles(a.V, 256) * (a.N <= 32 ? 8 : a.N <= 128 ? 4 : 2);
+    launch_rows<kCeStats>(a, pc, stream);
+    launch_cross_entropy_combine(a, stream);
+    return hipGetLastError();
+  }
+  for (int64_t v0 = 0; v0 < a.V; v0 += a.ds_ld) {
+    pc.v0 = v0;
+    pc.len = a.V - v0 < a.ds_ld ? a.V - v0 : a.ds_ld;
+    pc.first = v0 == 0;
+    launch_rows<kCeDs>(a, pc, stream);
+    if (a.out_dhidden) launch_rows<kCeDhidden>(a, pc, stream);
+    if (a.out_dweight) launch_rows<kCeDweight>(a, pc, stream);
+  }
+  if (a.out_dhidden) launch_cross_entropy_dhidden(a, true, stream);
+  return hipGetLastError();
+}
+
+}  // namespace arcs
