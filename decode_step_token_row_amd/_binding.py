@@ -125,8 +125,10 @@ def library() -> ctypes.CDLL:
         lib.arcs_commit_tokens.argtypes = [c_p, c_i64, c_i64, c_p, c_p, c_p, c_u64, c_p, c_p, c_p, c_p]
         lib.arcs_commit_tokens.restype = c_i
         lib.arcs_w4_logits.argtypes = [c_p, c_i64, c_i64, c_i64, c_p, c_i64, c_i64, c_p, c_i, c_i64, c_p, c_i64,
-                                       c_i, c_p, c_i, c_i64, c_p]
+                                       c_i, c_p, c_i, c_i64, c_p, ctypes.c_size_t, c_p]
         lib.arcs_w4_logits.restype = c_i
+        lib.arcs_w4_logits_workspace_bytes.argtypes = [c_i64, c_i64, c_i]
+        lib.arcs_w4_logits_workspace_bytes.restype = ctypes.c_size_t
         lib.arcs_linear_cross_entropy.argtypes = [c_p, c_i64, c_p, c_i64, c_i, c_i64, c_i64, c_i64, c_p,
                                                   ctypes.c_int32, c_p, c_p, c_p, c_p, c_p, ctypes.c_size_t, c_p]
         lib.arcs_linear_cross_entropy.restype = c_i
@@ -162,6 +164,10 @@ def workspace_bytes(B: int, V: int, dtype: int) -> int:
 
 def long_history_workspace_bytes(B: int, V: int) -> int:
     return int(library().arcs_long_history_workspace_bytes(int(B), int(V)))
+
+
+def w4_logits_workspace_bytes(B: int, D: int, group_size: int) -> int:
+    return int(library().arcs_w4_logits_workspace_bytes(int(B), int(D), int(group_size)))
 
 
 def linear_cross_entropy_workspace_bytes(N: int, V: int, D: int, dtype: int, backward: bool = False) -> int:
@@ -533,7 +539,8 @@ def _hidden_shape(hidden, what: str = "hidden"):
     return hidden.shape[0], hidden.shape[1], hidden.device
 
 
-def w4_logits(hidden, qweight, scales, group_size: int, zeros=None, out=None, out_dtype=None, stream=None):
+def w4_logits(hidden, qweight, scales, group_size: int, zeros=None, out=None, out_dtype=None, workspace=None,
+              stream=None):
     """arcs_w4_logits: [B, V] logits of a 4-bit head, ready for argmax, sample and top_logprobs.
 
     ``hidden`` bfloat16 [B, D]; ``qweight`` uint8 [V, D / 2], the even weight in
@@ -557,8 +564,10 @@ def w4_logits(hidden, qweight, scales, group_size: int, zeros=None, out=None, ou
             raise ValueError("out is not of out_dtype")
         odt = _dtype_code_of(out, "out")
         ls = _matrix(out, "out", out.dtype, B, V, dev)
+        workspace, ws_bytes = _head_workspace(workspace, w4_logits_workspace_bytes(B, D, G), dev)
         st = library().arcs_w4_logits(_ptr(hidden), B, D, hs, _ptr(qweight), V, qs, _ptr(scales), sdt, ss,
-                                      _ptr(zeros), zs, G, _ptr(out), odt, ls, _stream_ptr(stream))
+                                      _ptr(zeros), zs, G, _ptr(out), odt, ls, _ptr(workspace), ws_bytes,
+                                      _stream_ptr(stream))
     if st != OK:
         raise ArcsError(st, "arcs_w4_logits")
     return out
@@ -586,12 +595,12 @@ def _cross_entropy_inputs(hidden, weight, targets, temperature):
     return N, V, D, dev, dt, hs, ws
 
 
-def _cross_entropy_workspace(workspace, N, V, D, dt, backward, dev):
+def _head_workspace(workspace, need: int, dev):
+    """The caller's workspace, or one of the needed size (sizes the library
+    refuses need none: the call itself reports them)."""
     torch = _torch()
     if workspace is None:
-        # sizes the library refuses need none: the call itself reports them
-        need = max(256, linear_cross_entropy_workspace_bytes(N, V, D, dt, backward))
-        return torch.empty(need, dtype=torch.uint8, device=dev), need
+        return (None, 0) if need == 0 else (torch.empty(need, dtype=torch.uint8, device=dev), need)
     if workspace.device != dev or not workspace.is_contiguous():
         raise ValueError(f"workspace must be a contiguous tensor on {dev}")
     return workspace, workspace.numel() * workspace.element_size()
@@ -617,7 +626,8 @@ def linear_cross_entropy(hidden, weight, targets, temperature=None, ignore_index
         _vector(out_lse, "out_lse", torch.float32, N, dev)
         if out_status is not None:
             _vector(out_status, "out_status", torch.int32, N, dev)
-        workspace, ws_bytes = _cross_entropy_workspace(workspace, N, V, D, dt, False, dev)
+        workspace, ws_bytes = _head_workspace(
+            workspace, linear_cross_entropy_workspace_bytes(N, V, D, dt, False), dev)
         st = library().arcs_linear_cross_entropy(_ptr(hidden), hs, _ptr(weight), ws, dt, N, V, D, _ptr(targets),
                                                  int(ignore_index), _ptr(temperature), _ptr(out_loss),
                                                  _ptr(out_lse), _ptr(out_status), _ptr(workspace), ws_bytes,
@@ -646,7 +656,8 @@ def linear_cross_entropy_backward(hidden, weight, targets, lse, grad_loss, tempe
             _vector(out_dhidden, "out_dhidden", hidden.dtype, N * D, dev)
         if out_dweight is not None:
             _vector(out_dweight, "out_dweight", hidden.dtype, V * D, dev)
-        workspace, ws_bytes = _cross_entropy_workspace(workspace, N, V, D, dt, True, dev)
+        workspace, ws_bytes = _head_workspace(
+            workspace, linear_cross_entropy_workspace_bytes(N, V, D, dt, True), dev)
         st = library().arcs_linear_cross_entropy_backward(
             _ptr(hidden), hs, _ptr(weight), ws, dt, N, V, D, _ptr(targets), int(ignore_index), _ptr(temperature),
             _ptr(lse), _ptr(grad_loss), _ptr(out_dhidden), _ptr(out_dweight), _ptr(workspace), ws_bytes,

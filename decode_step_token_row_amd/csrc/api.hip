@@ -41,6 +41,8 @@ int noalloc_scratch(void** out) {
 }
 
 constexpr int64_t kMaxDim = 2147483647;
+// arcs_w4_logits: what the launch grids and 32-bit offsets in a tile hold
+constexpr int64_t kMaxW4Stride = int64_t(1) << 23, kMaxW4Batch = int64_t(1) << 19, kMaxW4Vocab = int64_t(1) << 28;
 
 int check_common(const void* logits, int dtype, int64_t B, int64_t V, int64_t row_stride,
                  const void* out_ids) {
@@ -306,24 +308,33 @@ int arcs_top_logprobs(const void* logits, int dtype, int64_t B, int64_t V, int64
 int arcs_w4_logits(const void* hidden, int64_t B, int64_t D, int64_t hidden_stride, const uint8_t* qweight,
                    int64_t V, int64_t qweight_stride, const void* scales, int scale_dtype,
                    int64_t scale_stride, const uint8_t* zeros, int64_t zero_stride, int group_size,
-                   void* logits, int logits_dtype, int64_t row_stride, void* stream) {
+                   void* logits, int logits_dtype, int64_t row_stride, void* workspace, size_t workspace_bytes,
+                   void* stream) {
   if (hidden == nullptr || qweight == nullptr || scales == nullptr || logits == nullptr) return ARCS_ERR_NULL_POINTER;
   if ((scale_dtype != ARCS_DTYPE_BF16 && scale_dtype != ARCS_DTYPE_F32) ||
       (logits_dtype != ARCS_DTYPE_BF16 && logits_dtype != ARCS_DTYPE_F32))
     return ARCS_ERR_BAD_DTYPE;
-  if (B <= 0 || B > ARCS_W4_MAX_BATCH) return ARCS_ERR_BAD_BATCH;
-  if (V <= 0 || V > kMaxDim) return ARCS_ERR_BAD_VOCAB;
+  if (B <= 0 || B > kMaxW4Batch) return ARCS_ERR_BAD_BATCH;
+  if (V <= 0 || V > kMaxW4Vocab) return ARCS_ERR_BAD_VOCAB;
+  if (B * V > int64_t(1) << 36) return ARCS_ERR_BAD_BATCH;
   if (D <= 0 || D > ARCS_MAX_HIDDEN) return ARCS_ERR_BAD_HIDDEN;
   if ((group_size != 32 && group_size != 64 && group_size != 128) || D % group_size != 0) return ARCS_ERR_BAD_GROUP;
   const int64_t groups = D / group_size;
   if (hidden_stride < D || qweight_stride < D / 2 || scale_stride < groups || row_stride < V ||
       (zeros != nullptr && zero_stride < groups))
     return ARCS_ERR_BAD_STRIDE;
+  // a tile's rows are addressed with 32 bits
+  if (qweight_stride > kMaxW4Stride || scale_stride > kMaxW4Stride || (zeros != nullptr && zero_stride > kMaxW4Stride))
+    return ARCS_ERR_BAD_STRIDE;
   if (misaligned(hidden, 16) || hidden_stride % 8 != 0 || misaligned(qweight, 16) || qweight_stride % 16 != 0 ||
       misaligned(scales, scale_dtype == ARCS_DTYPE_BF16 ? 2 : 4) ||
       misaligned(logits, logits_dtype == ARCS_DTYPE_BF16 ? 2 : 4))
     return ARCS_ERR_MISALIGNED;
-  arcs::W4Args a;
+  const size_t need = arcs::w4_workspace_bytes(B, D, group_size);
+  if (workspace_bytes < need) return ARCS_ERR_WORKSPACE_TOO_SMALL;
+  if (need > 0 && workspace == nullptr) return ARCS_ERR_NULL_POINTER;
+  if (need > 0 && misaligned(workspace, 256)) return ARCS_ERR_MISALIGNED;
+  arcs::W4Args a = {};
   a.hidden = (const uint16_t*)hidden;
   a.B = B;
   a.D = D;
@@ -337,8 +348,15 @@ int arcs_w4_logits(const void* hidden, int64_t B, int64_t D, int64_t hidden_stri
   a.zero_stride = zero_stride;
   a.logits = logits;
   a.row_stride = row_stride;
-  hipError_t e = arcs::launch_w4_logits(a, scale_dtype, logits_dtype, group_size, (hipStream_t)stream);
+  hipError_t e = arcs::launch_w4_logits(a, scale_dtype, logits_dtype, group_size, workspace, (hipStream_t)stream);
   return e == hipSuccess ? ARCS_OK : ARCS_ERR_LAUNCH;
+}
+
+size_t arcs_w4_logits_workspace_bytes(int64_t B, int64_t D, int group_size) {
+  if (B <= 0 || B > kMaxW4Batch || D <= 0 || D > ARCS_MAX_HIDDEN ||
+      (group_size != 32 && group_size != 64 && group_size != 128))
+    return 0;
+  return arcs::w4_workspace_bytes(B, D, group_size);
 }
 
 int arcs_linear_cross_entropy(const void* hidden, int64_t hidden_stride, const void* weight,

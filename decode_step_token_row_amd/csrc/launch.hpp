@@ -121,8 +121,16 @@ struct W4Args {
   int64_t zero_stride;
   void* logits;
   int64_t row_stride;
+  // set by the launch
+  int tiles, batch_tiles;
+  int whole;               // 128 k's scales, and zero points, can be loaded at once
+  int64_t padded_rows;     // of the prepared hidden states
+  char* prepared;
+  float* sums;
 };
-hipError_t launch_w4_logits(const W4Args& a, int scale_dtype, int logits_dtype, int group, hipStream_t stream);
+// Bytes of workspace (0 for batches that need none).
+size_t w4_workspace_bytes(int64_t B, int64_t D, int group);
+hipError_t launch_w4_logits(W4Args a, int scale_dtype, int logits_dtype, int group, void* workspace, hipStream_t stream);
 
 hipError_t launch_argmax(const void* logits, int dtype, int64_t B, int64_t V, int64_t stride,
                          bool vec, int32_t* out, hipStream_t stream);

@@ -4,148 +4,445 @@
 //
 // q is two weights a byte, the lower d in the low nibble.  The products run
 // on the bfloat16 matrix instruction with the batch as its rows and 16
-// vocabulary rows as its columns.  A nibble becomes the bfloat16 16 + q by an
-// AND and an OR on two weights at a time (0x4180 is 16.0 and a step of its
-// mantissa's bit 3 is 1), which is exact, and the group's sum is put right
-// with the sum of the hidden state over the group, from a product with ones:
-//   sum (q - z) h = sum (16 + q) h - (16 + z) sum h.
+// vocabulary rows as its columns, so a lane needs the scale of one row only.
+// A nibble becomes an exact bfloat16 with an offset: 16 + q by an AND and an
+// OR on two weights at a time (0x4180 is 16.0 and bit 3 of its mantissa is 1),
+// or, with zero points, 48 + q - z by an AND and an addition of the row's
+// constant (0x4200 is 32.0, bit 2 is 1).  The offset's part of a group's sum,
+// 24 or 48 times the sum of the hidden state over the group, is what the
+// product's accumulator starts from, negated:
+//   sum (q - z) h = -48 sum h + sum (48 + q - z) h.
 // Scales are applied to the group's float32 sums, so no weight is rounded.
+//
+// Batches of at most 16 rows take one launch: hidden states go through LDS, four
+// steps of 128 k at a time in two buffers, and weights from memory to registers
+// four steps ahead.  Larger batches have the hidden states prepared first, in the
+// workspace: in the nibbles' order and as the LDS holds them, with the groups'
+// sums beside them, so that a step is a plain copy to LDS that takes no registers.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
 #include "arcs.h"
 #include "device_common.hpp"
 #include "launch.hpp"
+#include "lds_load.hpp"
 
 namespace arcs {
 
-typedef __bf16 bf16x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
-constexpr int kW4Chunk = 128;  // k of one step: 16 bytes of a weight row in each of four lanes
+constexpr int64_t kW4FewRows = 16;
+constexpr int kW4Step = 128;  // k of one step: 16 bytes of a weight row in each of four lanes
 
-// Eight nibbles as bfloat16 16 + q, in the order 0 4 1 5 2 6 3 7.
-__device__ __forceinline__ bf16x8 w4_unpack(uint32_t w) {
+// Eight nibbles as bfloat16, in the order 0 4 1 5 2 6 3 7: 16 + q, or with zero
+// points (add = 0x42004200 + 4 (16 - z) in both halves) 48 + q - z.
+template <bool ZERO>
+__device__ __forceinline__ bf16x8 w4_unpack(uint32_t w, uint32_t add) {
   u32x4 d;
-  d[0] = ((w << 3) & 0x00780078u) | 0x41804180u;
-  d[1] = ((w >> 1) & 0x00780078u) | 0x41804180u;
-  d[2] = ((w >> 5) & 0x00780078u) | 0x41804180u;
-  d[3] = ((w >> 9) & 0x00780078u) | 0x41804180u;
+  if (ZERO) {
+    d[0] = ((w << 2) & 0x003C003Cu) + add;
+    d[1] = ((w >> 2) & 0x003C003Cu) + add;
+    d[2] = ((w >> 6) & 0x003C003Cu) + add;
+    d[3] = ((w >> 10) & 0x003C003Cu) + add;
+  } else {
+    d[0] = ((w << 3) & 0x00780078u) | 0x41804180u;
+    d[1] = ((w >> 1) & 0x00780078u) | 0x41804180u;
+    d[2] = ((w >> 5) & 0x00780078u) | 0x41804180u;
+    d[3] = ((w >> 9) & 0x00780078u) | 0x41804180u;
+  }
   return __builtin_bit_cast(bf16x8, d);
 }
 
 // Eight bfloat16 in the same order.
-__device__ __forceinline__ bf16x8 w4_order(u32x4 x) {
+__device__ __forceinline__ u32x4 w4_order(u32x4 x) {
   u32x4 d;
   d[0] = __builtin_amdgcn_perm(x[2], x[0], 0x05040100u);
   d[1] = __builtin_amdgcn_perm(x[2], x[0], 0x07060302u);
   d[2] = __builtin_amdgcn_perm(x[3], x[1], 0x05040100u);
   d[3] = __builtin_amdgcn_perm(x[3], x[1], 0x07060302u);
-  return __builtin_bit_cast(bf16x8, d);
+  return d;
 }
 
 // w[i] of lane group j <-> w[j] of lane group i (groups of 16 lanes).
-__device__ __forceinline__ void w4_transpose(u32x4& w) {
-  auto a = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
-  auto b = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
-  auto c = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
-  auto d = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
-  w[0] = c[0];
-  w[1] = c[1];
-  w[2] = d[0];
-  w[3] = d[1];
+__device__ __forceinline__ u32x4 w4_turn(u32x4 w) {
+  const auto a = __builtin_amdgcn_permlane32_swap(w[0], w[2], false, false);
+  const auto b = __builtin_amdgcn_permlane32_swap(w[1], w[3], false, false);
+  const auto c = __builtin_amdgcn_permlane16_swap(a[0], b[0], false, false);
+  const auto d = __builtin_amdgcn_permlane16_swap(a[1], b[1], false, false);
+  return u32x4{c[0], c[1], d[0], d[1]};
+}
+
+template <int CTRL>
+__device__ __forceinline__ float add_dpp(float x) {
+  return x + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, 0xf, 0xf, true));
 }
 
 // GROUP 128: a lane's 16 bytes are 32 consecutive k and one product takes 8 of
 // each lane group's.  GROUP 32, 64: the 16 bytes are exchanged between the four
 // lane groups first, so that a product's 32 k are consecutive and lie in one group.
-template <int RT, int GROUP, bool ZERO, bool SF32, bool OF32>
-__global__ __launch_bounds__(256) void w4_logits_kernel(W4Args a) {
-  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
-  const int r = lane & 15, j = lane >> 4;
-  const int64_t v0 = ((int64_t)blockIdx.x * 4 + wave) * (RT * 16);
-  if (v0 >= a.V) return;
-  const int64_t b0 = (int64_t)blockIdx.y * 16;
-  constexpr int kGroups = kW4Chunk / GROUP, kSteps = 4 / kGroups;
-  constexpr bool kTurn = GROUP < 128;
-  const int64_t b = b0 + r < a.B ? b0 + r : a.B - 1;
-  const uint16_t* x = a.hidden + b * a.hidden_stride;
-  const uint8_t* q[RT];
-  int64_t sc[RT], zr[RT];
-#pragma unroll
-  for (int t = 0; t < RT; ++t) {
-    const int64_t v = v0 + t * 16 + r < a.V ? v0 + t * 16 + r : a.V - 1;
-    q[t] = a.qweight + v * a.qweight_stride;
-    sc[t] = v * a.scale_stride;
-    zr[t] = v * a.zero_stride;
-  }
-  const u32x4 one4 = {0x3F803F80u, 0x3F803F80u, 0x3F803F80u, 0x3F803F80u};
-  const bf16x8 ones = __builtin_bit_cast(bf16x8, one4);
-  const u32x4 zero4 = {0, 0, 0, 0};
-  const f32x4 none = {0.0f, 0.0f, 0.0f, 0.0f};
-  f32x4 total[RT];
-#pragma unroll
-  for (int t = 0; t < RT; ++t) total[t] = none;
+template <int GROUP, bool ZERO, bool SF32>
+struct W4 {
+  static constexpr int kGroups = kW4Step / GROUP;           // of a step
+  static constexpr int kProducts = 4 / kGroups;             // of 32 k, in a group
+  static constexpr bool kTurn = GROUP < 128;
+  static constexpr int kScale = SF32 ? 4 : 2;               // bytes of a scale
+  static constexpr int kScales = (kGroups * kScale + 3) / 4;  // words of a step's scales
+  static constexpr float kOffset = ZERO ? -48.0f : -24.0f;
 
-  for (int64_t k = 0; k < a.D; k += kW4Chunk) {
-    u32x4 w[RT];
-    const bool here = !kTurn || k + j * 32 < a.D;
-#pragma unroll
-    for (int t = 0; t < RT; ++t) w[t] = here ? *(const u32x4*)(q[t] + (k >> 1) + j * 16) : zero4;
-    bf16x8 xs[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t at = k + (kTurn ? i * 32 + j * 8 : j * 32 + i * 8);
-      xs[i] = w4_order(!kTurn || k + i * 32 < a.D ? *(const u32x4*)(x + at) : zero4);
-    }
-    if (kTurn) {
-#pragma unroll
-      for (int t = 0; t < RT; ++t) w4_transpose(w[t]);
-    }
-#pragma unroll
-    for (int g = 0; g < kGroups; ++g) {
-      if (kTurn && k + g * GROUP >= a.D) break;
-      const int64_t at = k / GROUP + g;
-      f32x4 sum = none;
-#pragma unroll
-      for (int i = 0; i < kSteps; ++i) sum = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xs[g * kSteps + i], ones, sum, 0, 0, 0);
+  // Where lane group j finds the 8 k of product n of a step, in units of 8.
+  static __device__ __forceinline__ int chunk(int n, int j) { return kTurn ? n * 4 + j : j * 4 + n; }
+
+  // RT tiles of 16 weight rows: a uniform base, and a lane's row in each.
+  template <int RT>
+  struct Rows {
+    const char *qb, *sb, *zb;
+    uint32_t qo[RT], so[RT], zo[RT];
+    __device__ __forceinline__ Rows(const W4Args& a, int64_t v0, int r, int j) {
+      const int64_t base = v0 < a.V ? v0 : a.V - 1;
+      qb = (const char*)a.qweight + base * a.qweight_stride;
+      sb = (const char*)a.scales + base * a.scale_stride * kScale;
+      zb = (const char*)a.zeros + base * a.zero_stride;
 #pragma unroll
       for (int t = 0; t < RT; ++t) {
-        f32x4 acc = none;
-#pragma unroll
-        for (int i = 0; i < kSteps; ++i)
-          acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xs[g * kSteps + i], w4_unpack(w[t][g * kSteps + i]), acc, 0, 0, 0);
-        const float s = SF32 ? ((const float*)a.scales)[sc[t] + at] : bf16_to_f32(((const uint16_t*)a.scales)[sc[t] + at]);
-        const float off = 16.0f + (ZERO ? (float)a.zeros[zr[t] + at] : 8.0f);
-#pragma unroll
-        for (int e = 0; e < 4; ++e) total[t][e] = fmaf(s, fmaf(-off, sum[e], acc[e]), total[t][e]);
+        const uint32_t v = (uint32_t)(base + t * 16 + r < a.V ? t * 16 + r : a.V - 1 - base);
+        qo[t] = v * (uint32_t)a.qweight_stride + j * 16;
+        so[t] = v * (uint32_t)a.scale_stride * kScale;
+        zo[t] = v * (uint32_t)a.zero_stride;
       }
     }
+  };
+
+  // One step's weights, scales and zero points of RT tiles.
+  template <int RT>
+  struct Step {
+    u32x4 w[RT];
+    uint32_t s[RT][kScales], z[RT];
+
+    __device__ __forceinline__ void load(const W4Args& a, const Rows<RT>& rows, int step, int j) {
+      const int64_t k = (int64_t)step * kW4Step, first = k / GROUP;
+      const bool here = !kTurn || k + j * 32 < a.D;
+#pragma unroll
+      for (int t = 0; t < RT; ++t) {
+        w[t] = u32x4{0, 0, 0, 0};
+        if (here) w[t] = *(const u32x4*)(rows.qb + (k >> 1) + rows.qo[t]);
+      }
+      if (a.whole) {  // a step's scales and zero points as one load each
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+          const char* p = rows.sb + first * kScale + rows.so[t];
+          if constexpr (kScales == 4) {
+            const u32x4 x = *(const u32x4*)p;
+#pragma unroll
+            for (int g = 0; g < 4; ++g) s[t][g] = x[g];
+          } else if constexpr (kScales == 2) {
+            const uint2 x = *(const uint2*)p;
+            s[t][0] = x.x;
+            s[t][1] = x.y;
+          } else {
+            s[t][0] = kGroups * kScale == 2 ? *(const uint16_t*)p : *(const uint32_t*)p;
+          }
+          const char* q = rows.zb + first + rows.zo[t];
+          if (ZERO) z[t] = kGroups == 4 ? *(const uint32_t*)q : kGroups == 2 ? *(const uint16_t*)q : *(const uint8_t*)q;
+        }
+        return;
+      }
+#pragma unroll
+      for (int t = 0; t < RT; ++t) {
+#pragma unroll
+        for (int g = 0; g < kScales; ++g) s[t][g] = 0;
+        z[t] = 0;
+#pragma unroll
+        for (int g = 0; g < kGroups; ++g) {
+          if (k + g * GROUP >= a.D) continue;
+          const char* p = rows.sb + (first + g) * kScale + rows.so[t];
+          if (SF32) s[t][g] = *(const uint32_t*)p;
+          else s[t][g / 2] |= (uint32_t) * (const uint16_t*)p << (g % 2 * 16);
+          if (ZERO) z[t] |= (uint32_t) * (const uint8_t*)(rows.zb + first + g + rows.zo[t]) << (g * 8);
+        }
+      }
+    }
+    __device__ __forceinline__ float scale(int t, int g) const {
+      return SF32 ? __uint_as_float(s[t][g]) : g % 2 ? bf16_hi(s[t][g / 2]) : bf16_lo(s[t][g / 2]);
+    }
+    __device__ __forceinline__ uint32_t add(int t, int g) const {
+      return ZERO ? 0x42404240u - ((z[t] >> (g * 8)) & 15u) * 0x00040004u : 0u;
+    }
+  };
+
+  // A lane's 8 k of a hidden row: their order, and (in the group's first lane) the group's sum.
+  static __device__ __forceinline__ float group_sum(u32x4 v) {
+    float s = (bf16_lo(v[0]) + bf16_hi(v[0])) + (bf16_lo(v[1]) + bf16_hi(v[1]));
+    s += (bf16_lo(v[2]) + bf16_hi(v[2])) + (bf16_lo(v[3]) + bf16_hi(v[3]));
+    s = add_dpp<0xB1>(s);                   // lanes 1 apart
+    s = add_dpp<0x4E>(s);                   // 2 apart
+    if (GROUP > 32) s = add_dpp<0x141>(s);  // the other four of eight
+    if (GROUP > 64) s = add_dpp<0x140>(s);  // the other eight of sixteen
+    return kOffset * s;
   }
+};
+
+template <int MT, int RT, bool OF32>
+__device__ __forceinline__ void w4_write(const W4Args& a, const f32x4 (&total)[MT][RT], int64_t b0, int64_t v0, int r, int j) {
 #pragma unroll
   for (int t = 0; t < RT; ++t) {
     const int64_t v = v0 + t * 16 + r;
     if (v >= a.V) continue;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      const int64_t row = b0 + j * 4 + e;
-      if (row >= a.B) continue;
-      if (OF32) ((float*)a.logits)[row * a.row_stride + v] = total[t][e];
-      else ((__bf16*)a.logits)[row * a.row_stride + v] = (__bf16)total[t][e];
-    }
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        const int64_t row = b0 + m * 16 + j * 4 + e;
+        if (row >= a.B) continue;
+        if (OF32) ((float*)a.logits)[row * a.row_stride + v] = total[m][t][e];
+        else ((__bf16*)a.logits)[row * a.row_stride + v] = (__bf16)total[m][t][e];
+      }
   }
 }
 
+// ---------------------------------------------------------------------------
+// At most 16 rows: four waves of RT * 16 weight rows each.
+// ---------------------------------------------------------------------------
+constexpr int kW4Stage = 4;  // steps
+
+template <int RT, int GROUP, bool ZERO, bool SF32, bool OF32>
+__global__ __launch_bounds__(256, 2) void w4_rows_kernel(W4Args a) {
+  using K = W4<GROUP, ZERO, SF32>;
+  constexpr int SC = kW4Stage, kRows = 16, kPer = kRows * SC * 16 / 256;
+  __shared__ __align__(16) char s_x[2][SC * kRows * 256];
+  __shared__ __align__(16) float s_sum[2][SC * K::kGroups][kRows];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r = lane & 15, j = lane >> 4;
+  const int64_t v0 = ((int64_t)blockIdx.x * 4 + wave) * (RT * 16);
+  const int steps = (int)((a.D + kW4Step - 1) / kW4Step), stages = (steps + SC - 1) / SC;
+  const typename K::template Rows<RT> rows(a, v0, r, j);
+
+  // the stage's hidden states: piece p of a thread is 8 k of one row, 64 pieces a row
+  u32x4 xr[kPer];
+  auto fetch_x = [&](int stage) {
+    const int64_t k = (int64_t)stage * SC * kW4Step + lane * 8;
+#pragma unroll
+    for (int p = 0; p < kPer; ++p) {
+      const int row = wave + p * 4;
+      if (row < a.B) xr[p] = k < a.D ? *(const u32x4*)(a.hidden + row * a.hidden_stride + k) : u32x4{0, 0, 0, 0};
+    }
+  };
+  auto store_x = [&](int stage) {
+    char* x = s_x[stage & 1] + (lane >> 4) * (kRows * 256);
+#pragma unroll
+    for (int p = 0; p < kPer; ++p) {
+      const int row = wave + p * 4;
+      if (row >= a.B) continue;
+      const float s = K::group_sum(xr[p]);
+      *(u32x4*)(x + row * 256 + (((lane & 15) ^ row) * 16)) = w4_order(xr[p]);
+      if (lane % (GROUP / 8) == 0) s_sum[stage & 1][lane / (GROUP / 8)][row] = s;
+    }
+  };
+
+  typename K::template Step<RT> next[SC];
+  f32x4 total[1][RT];
+#pragma unroll
+  for (int t = 0; t < RT; ++t) total[0][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  fetch_x(0);
+#pragma unroll
+  for (int c = 0; c < SC; ++c)
+    if (c < steps) next[c].load(a, rows, c, j);
+  store_x(0);
+  __syncthreads();
+  for (int stage = 0; stage < stages; ++stage) {
+    if (stage + 1 < stages) fetch_x(stage + 1);
+    const char* x = s_x[stage & 1];
+#pragma unroll
+    for (int c = 0; c < SC; ++c) {
+      if (c > 0 && stage * SC + c >= steps) break;
+      typename K::template Step<RT> now = next[c];
+      if ((stage + 1) * SC + c < steps) next[c].load(a, rows, (stage + 1) * SC + c, j);
+#pragma unroll
+      for (int t = 0; t < RT; ++t)
+        if (K::kTurn) now.w[t] = w4_turn(now.w[t]);
+#pragma unroll
+      for (int g = 0; g < K::kGroups; ++g) {
+        const f32x4 start = *(const f32x4*)&s_sum[stage & 1][c * K::kGroups + g][j * 4];
+        bf16x8 xf[K::kProducts];
+#pragma unroll
+        for (int i = 0; i < K::kProducts; ++i)
+          xf[i] = *(const bf16x8*)(x + (c * kRows + r) * 256 + ((K::chunk(g * K::kProducts + i, j) ^ r) * 16));
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+          f32x4 acc = start;
+#pragma unroll
+          for (int i = 0; i < K::kProducts; ++i)
+            acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[i], w4_unpack<ZERO>(now.w[t][g * K::kProducts + i], now.add(t, g)),
+                                                          acc, 0, 0, 0);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) total[0][t][e] = fmaf(now.scale(t, g), acc[e], total[0][t][e]);
+        }
+      }
+    }
+    if (stage + 1 < stages) store_x(stage + 1);
+    __syncthreads();
+  }
+  w4_write<1, RT, OF32>(a, total, 0, v0, r, j);
+}
+
+// ---------------------------------------------------------------------------
+// More rows.  The prepared hidden states of one step are 4096 bytes for every 16
+// rows: row x 256 bytes, chunk c of 8 k at c ^ row; rows past B are zeros.  The
+// sums are [step][group][row].
+// ---------------------------------------------------------------------------
+template <int GROUP, bool ZERO>
+__global__ __launch_bounds__(256) void w4_prepare_kernel(W4Args a) {
+  using K = W4<GROUP, ZERO, false>;
+  const int row = threadIdx.x >> 4, c = threadIdx.x & 15;
+  const int64_t step = blockIdx.x, tile = blockIdx.y, b = tile * 16 + row, k = step * kW4Step + c * 8;
+  u32x4 v = {0, 0, 0, 0};
+  if (b < a.B && k < a.D) v = *(const u32x4*)(a.hidden + b * a.hidden_stride + k);
+  const float s = K::group_sum(v);
+  const int64_t tiles = a.padded_rows / 16;
+  *(u32x4*)(a.prepared + (step * tiles + tile) * 4096 + row * 256 + ((c ^ row) * 16)) = w4_order(v);
+  if (c % (GROUP / 8) == 0) a.sums[(step * K::kGroups + c / (GROUP / 8)) * a.padded_rows + b] = s;
+}
+
+template <int MT, int RT, int WB, int WV, int GROUP, bool ZERO, bool SF32, bool OF32>
+__global__ __launch_bounds__(WB* WV * 64, 2) void w4_batch_kernel(W4Args a) {
+  using K = W4<GROUP, ZERO, SF32>;
+  constexpr int kWaves = WB * WV, kRows = WB * MT * 16;
+  constexpr int kLoads = kRows / 4, kPer = (kLoads + kWaves - 1) / kWaves;  // of 1024 bytes
+  constexpr int kSumBytes = K::kGroups * kRows * 4, kSumLoads = (kSumBytes + 1023) / 1024;
+  constexpr int kStage = kRows * 256 + kSumLoads * 1024;
+  static_assert(kSumLoads <= kWaves && kLoads % kWaves == 0, "loads of a stage over the waves");
+  __shared__ __align__(1024) char lds[2 * kStage];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int r = lane & 15, j = lane >> 4;
+  const int wb = wave % WB, wv = wave / WB;
+  // blocks go round the eight dies in turn; a die gets neighbouring tiles, the
+  // batch's tiles of the same weights one after the other
+  const int per = (a.tiles + 7) / 8, at = ((int)blockIdx.x & 7) * per + ((int)blockIdx.x >> 3);
+  if (((int)blockIdx.x >> 3) >= per || at >= a.tiles) return;
+  const int64_t b0 = (int64_t)(at % a.batch_tiles) * kRows;
+  const int64_t v0 = ((int64_t)(at / a.batch_tiles) * WV + wv) * (RT * 16);
+  const int steps = (int)((a.D + kW4Step - 1) / kW4Step);
+  const typename K::template Rows<RT> rows(a, v0, r, j);
+
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(ARCS_LDS char*)lds;
+  const char* px = a.prepared + b0 * 256;
+  const char* ps = (const char*)(a.sums + b0);
+  const int64_t step_x = a.padded_rows * 256, step_s = (int64_t)K::kGroups * a.padded_rows * 4;
+  constexpr int kSumLanes = kRows / 4;  // lanes of one group's sums
+  const int sum_group = (wave * 64 + lane) / kSumLanes;
+  const uint32_t sum_off = sum_group < K::kGroups
+                               ? (uint32_t)(sum_group * a.padded_rows * 4 + (wave * 64 + lane) % kSumLanes * 16)
+                               : kNoLoad;
+  auto issue = [&](int step) {
+    const uint32_t to = lds0 + (uint32_t)(step & 1) * kStage;
+    const u32x4 dx = buffer_of(px + step * step_x, kRows * 256);
+#pragma unroll
+    for (int t = 0; t < kPer; ++t) {
+      const uint32_t at = (uint32_t)(wave + t * kWaves) * 1024u;
+      load_to_lds(to + at, at + lane * 16, dx);
+    }
+    if (wave < kSumLoads) load_to_lds(to + kRows * 256 + wave * 1024u, sum_off, buffer_of(ps + step * step_s, kBufMost));
+  };
+
+  f32x4 total[MT][RT];
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int t = 0; t < RT; ++t) total[m][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  typename K::template Step<RT> next;
+  issue(0);
+  next.load(a, rows, 0, j);
+  for (int step = 0; step < steps; ++step) {
+    wait_loads<0>();  // this step's hidden states are in LDS, its weights in registers
+    wait_lds();
+    __builtin_amdgcn_s_barrier();
+    typename K::template Step<RT> now = next;
+    if (step + 1 < steps) {
+      issue(step + 1);
+      next.load(a, rows, step + 1, j);
+    }
+    const char* x = lds + (step & 1) * kStage;
+    const float* sums = (const float*)(x + kRows * 256);
+#pragma unroll
+    for (int t = 0; t < RT; ++t)
+      if (K::kTurn) now.w[t] = w4_turn(now.w[t]);
+#pragma unroll
+    for (int g = 0; g < K::kGroups; ++g) {
+      f32x4 acc[MT][RT];
+#pragma unroll
+      for (int i = 0; i < K::kProducts; ++i) {
+        bf16x8 xf[MT];
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          const int row = (wb * MT + m) * 16;
+          if (i == 0) {
+            const f32x4 start = *(const f32x4*)(sums + g * kRows + row + j * 4);
+#pragma unroll
+            for (int t = 0; t < RT; ++t) acc[m][t] = start;
+          }
+          xf[m] = *(const bf16x8*)(x + (row + r) * 256 + ((K::chunk(g * K::kProducts + i, j) ^ r) * 16));
+        }
+#pragma unroll
+        for (int t = 0; t < RT; ++t) {
+          const bf16x8 wf = w4_unpack<ZERO>(now.w[t][g * K::kProducts + i], now.add(t, g));
+#pragma unroll
+          for (int m = 0; m < MT; ++m) acc[m][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[m], wf, acc[m][t], 0, 0, 0);
+        }
+      }
+#pragma unroll
+      for (int t = 0; t < RT; ++t)
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) total[m][t][e] = fmaf(now.scale(t, g), acc[m][t][e], total[m][t][e]);
+      __builtin_amdgcn_sched_barrier(0);  // one group's operands at a time in registers
+    }
+  }
+  w4_write<MT, RT, OF32>(a, total, b0 + wb * MT * 16, v0, r, j);
+}
+
+namespace {
+
+template <int RT, int GROUP, bool ZERO, bool SF32>
+void launch_w4_rows(const W4Args& a, bool f32, hipStream_t stream) {
+  const dim3 grid((unsigned)((a.V + 64 * RT - 1) / (64 * RT))), block(256);
+  if (f32) hipLaunchKernelGGL((w4_rows_kernel<RT, GROUP, ZERO, SF32, true>), grid, block, 0, stream, a);
+  else hipLaunchKernelGGL((w4_rows_kernel<RT, GROUP, ZERO, SF32, false>), grid, block, 0, stream, a);
+}
+
+template <int MT, int RT, int WB, int WV, int GROUP, bool ZERO, bool SF32>
+void launch_w4_batch(W4Args a, bool f32, hipStream_t stream) {
+  constexpr int kRows = WB * MT * 16, kCols = WV * RT * 16;
+  a.batch_tiles = (int)((a.B + kRows - 1) / kRows);
+  const int64_t tiles = (a.V + kCols - 1) / kCols * a.batch_tiles;
+  a.tiles = (int)tiles;
+  hipLaunchKernelGGL((w4_prepare_kernel<GROUP, ZERO>),
+                     dim3((unsigned)((a.D + kW4Step - 1) / kW4Step), (unsigned)(a.padded_rows / 16)), dim3(256), 0, stream, a);
+  const dim3 grid((unsigned)((tiles + 7) / 8 * 8)), block(WB * WV * 64);
+  if (f32) hipLaunchKernelGGL((w4_batch_kernel<MT, RT, WB, WV, GROUP, ZERO, SF32, true>), grid, block, 0, stream, a);
+  else hipLaunchKernelGGL((w4_batch_kernel<MT, RT, WB, WV, GROUP, ZERO, SF32, false>), grid, block, 0, stream, a);
+}
+
 template <int GROUP, bool ZERO, bool SF32>
-static void launch_w4_typed(const W4Args& a, bool f32, hipStream_t stream) {
-  constexpr int kRT = 2;
-  const dim3 grid((unsigned)((a.V + 64 * kRT - 1) / (64 * kRT)), (unsigned)((a.B + 15) / 16)), block(256);
-  if (f32) hipLaunchKernelGGL((w4_logits_kernel<kRT, GROUP, ZERO, SF32, true>), grid, block, 0, stream, a);
-  else hipLaunchKernelGGL((w4_logits_kernel<kRT, GROUP, ZERO, SF32, false>), grid, block, 0, stream, a);
+void launch_w4_typed(W4Args a, bool f32, hipStream_t stream) {
+  constexpr int64_t kGroups = kW4Step / GROUP, kBytes = kGroups * (SF32 ? 4 : 2);
+  a.whole = a.D % kW4Step == 0 && (uintptr_t)a.scales % kBytes == 0 && a.scale_stride * (SF32 ? 4 : 2) % kBytes == 0 &&
+            (!ZERO || ((uintptr_t)a.zeros % kGroups == 0 && a.zero_stride % kGroups == 0));
+  if (a.B <= kW4FewRows) {
+    if (a.V <= 65536) launch_w4_rows<1, GROUP, ZERO, SF32>(a, f32, stream);
+    else launch_w4_rows<2, GROUP, ZERO, SF32>(a, f32, stream);
+  } else if (a.B <= 32) {
+    launch_w4_batch<2, 4, 1, 4, GROUP, ZERO, SF32>(a, f32, stream);
+  } else if (a.B <= 64) {
+    launch_w4_batch<4, 4, 1, 4, GROUP, ZERO, SF32>(a, f32, stream);
+  } else {
+    launch_w4_batch<4, 4, 2, 4, GROUP, ZERO, SF32>(a, f32, stream);
+  }
 }
 
 template <int GROUP>
-static void launch_w4_group(const W4Args& a, bool sf32, bool f32, hipStream_t stream) {
+void launch_w4_group(const W4Args& a, bool sf32, bool f32, hipStream_t stream) {
   if (a.zeros) {
     if (sf32) launch_w4_typed<GROUP, true, true>(a, f32, stream);
     else launch_w4_typed<GROUP, true, false>(a, f32, stream);
@@ -155,8 +452,27 @@ static void launch_w4_group(const W4Args& a, bool sf32, bool f32, hipStream_t st
   }
 }
 
-hipError_t launch_w4_logits(const W4Args& a, int scale_dtype, int logits_dtype, int group, hipStream_t stream) {
+// Rows the workspace holds: the batch rounded up to a workgroup's.
+int64_t padded_rows(int64_t B) {
+  const int64_t to = B <= 32 ? 32 : B <= 64 ? 64 : 128;
+  return (B + to - 1) / to * to;
+}
+
+}  // namespace
+
+size_t w4_workspace_bytes(int64_t B, int64_t D, int group) {
+  if (B <= kW4FewRows) return 0;
+  const int64_t steps = (D + kW4Step - 1) / kW4Step;
+  return (size_t)(padded_rows(B) * steps * (256 + 4 * (kW4Step / group)));
+}
+
+hipError_t launch_w4_logits(W4Args a, int scale_dtype, int logits_dtype, int group, void* workspace, hipStream_t stream) {
   const bool sf32 = scale_dtype == ARCS_DTYPE_F32, f32 = logits_dtype == ARCS_DTYPE_F32;
+  if (a.B > kW4FewRows) {
+    a.padded_rows = padded_rows(a.B);
+    a.prepared = (char*)workspace;
+    a.sums = (float*)(a.prepared + a.padded_rows * ((a.D + kW4Step - 1) / kW4Step) * 256);
+  }
   if (group == 32) launch_w4_group<32>(a, sf32, f32, stream);
   else if (group == 64) launch_w4_group<64>(a, sf32, f32, stream);
   else launch_w4_group<128>(a, sf32, f32, stream);

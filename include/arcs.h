@@ -430,8 +430,8 @@ int arcs_commit_tokens(const int32_t* ids, int64_t B, int64_t V, int32_t* next_i
  *       scales[v, g] * sum over d in g of (q[v, d] - zeros[v, g]) * hidden[b, d]
  * with q in 0 .. 15 and zeros 8 where `zeros` is NULL.  Products and sums are
  * held in binary32 (weights and hidden states enter exactly) and each logit is
- * rounded once to its type.  NaN and infinities in a hidden state or a scale
- * reach the logits they belong to as in any such sum.
+ * rounded once to its type.  A NaN or an infinity in a hidden state makes its
+ * row's logits NaN or infinite, one in a scale its column's.
  *   hidden         device bfloat16 [B, hidden_stride], rows 16-byte aligned
  *   D              hidden size, 1 .. ARCS_MAX_HIDDEN, a multiple of group_size
  *   qweight        device bytes [V, qweight_stride], rows 16-byte aligned: byte d / 2
@@ -439,20 +439,29 @@ int arcs_commit_tokens(const int32_t* ids, int64_t B, int64_t V, int32_t* next_i
  *                  nibble (d even); qweight_stride >= D / 2
  *   scales         device [V, scale_stride] of scale_dtype (ARCS_DTYPE_BF16 or
  *                  ARCS_DTYPE_F32), scale_stride >= D / group_size elements
- *   zeros          device bytes [V, zero_stride], 0 .. 15 each (other values are
- *                  taken as the number they are), or NULL
+ *   zeros          device bytes [V, zero_stride], 0 .. 15 each (the upper four
+ *                  bits are ignored), or NULL
  *   group_size     32, 64 or 128
  *   logits         device [B, row_stride] of logits_dtype, row_stride >= V
- * No workspace.  Returns ARCS_OK or a negative arcs_status (nothing launched then):
- * ARCS_ERR_BAD_STRIDE for any stride below its row, ARCS_ERR_MISALIGNED for
- * `hidden` or `qweight` rows that are not 16-byte aligned or another array not
- * aligned to its element, ARCS_ERR_BAD_BATCH for B above ARCS_W4_MAX_BATCH.
+ *   workspace      device scratch of at least arcs_w4_logits_workspace_bytes(),
+ *                  256-byte aligned, not read before it is written; calls that
+ *                  share one must be ordered on one stream; may be NULL when
+ *                  none is needed
+ * Returns ARCS_OK or a negative arcs_status (nothing launched then):
+ * ARCS_ERR_BAD_STRIDE for any stride below its row, or a stride of qweight,
+ * scales or zeros above 2^23, ARCS_ERR_MISALIGNED for `hidden` or `qweight`
+ * rows that are not 16-byte aligned or another array not aligned to its
+ * element, ARCS_ERR_BAD_BATCH also for B above 2^19 or B * V above 2^36,
+ * ARCS_ERR_BAD_VOCAB also for V above 2^28.
  */
-#define ARCS_W4_MAX_BATCH 524288
 int arcs_w4_logits(const void* hidden, int64_t B, int64_t D, int64_t hidden_stride, const uint8_t* qweight,
                    int64_t V, int64_t qweight_stride, const void* scales, int scale_dtype,
                    int64_t scale_stride, const uint8_t* zeros, int64_t zero_stride, int group_size,
-                   void* logits, int logits_dtype, int64_t row_stride, void* stream);
+                   void* logits, int logits_dtype, int64_t row_stride, void* workspace,
+                   size_t workspace_bytes, void* stream);
+
+/* Bytes of workspace arcs_w4_logits needs: 0 for batches of at most 16 rows. */
+size_t arcs_w4_logits_workspace_bytes(int64_t B, int64_t D, int group_size);
 
 /*
  * arcs_linear_cross_entropy: the log-probabilities of given tokens, or the

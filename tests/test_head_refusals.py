@@ -36,25 +36,27 @@ def test_declared_and_described(arcs):
 
 
 W4 = dict(hidden=0, B=4, D=256, hs=256, q=0, V=100, qs=128, sc=0, sdt=BF16, ss=2, z=0, zs=2, g=128, out=0, odt=BF16,
-          ls=100)
+          ls=100, ws=0, more=0)
 
 
 @pytest.mark.parametrize("change,status", [
     (dict(hidden=None), NULL), (dict(q=None), NULL), (dict(sc=None), NULL), (dict(out=None), NULL),
-    (dict(sdt=2), DTYPE), (dict(odt=-1), DTYPE), (dict(B=0), BATCH), (dict(B=-1), BATCH), (dict(B=524289), BATCH),
+    (dict(sdt=2), DTYPE), (dict(odt=-1), DTYPE), (dict(B=0), BATCH), (dict(B=-1), BATCH), (dict(B=2**31), BATCH), (dict(B=2**20, V=2**17, ls=2**17), BATCH),
     (dict(V=0), VOCAB), (dict(V=2**31), VOCAB), (dict(D=0, hs=0), HIDDEN), (dict(D=65664, hs=65664, qs=32832), HIDDEN),
     (dict(g=0), GROUP), (dict(g=16), GROUP), (dict(g=256), GROUP), (dict(g=-32), GROUP), (dict(D=192, g=128), GROUP),
     (dict(D=250), GROUP), (dict(hs=255), STRIDE), (dict(qs=127), STRIDE), (dict(ss=1), STRIDE), (dict(zs=1), STRIDE),
-    (dict(ls=99), STRIDE), (dict(hidden=8), MISALIGNED), (dict(hs=260), MISALIGNED), (dict(q=4), MISALIGNED),
+    (dict(ls=99), STRIDE), (dict(qs=2**23 + 16), STRIDE), (dict(ss=2**23 + 1), STRIDE), (dict(hidden=8), MISALIGNED), (dict(hs=260), MISALIGNED), (dict(q=4), MISALIGNED),
     (dict(qs=136), MISALIGNED), (dict(sc=1), MISALIGNED), (dict(sdt=F32, sc=2), MISALIGNED), (dict(out=1), MISALIGNED),
-    (dict(odt=F32, out=2), MISALIGNED),
+    (dict(odt=F32, out=2), MISALIGNED), (dict(B=40, ws=None), NULL), (dict(B=40, ws=16), MISALIGNED),
+    (dict(B=40, more=-1), SMALL),
 ])
 def test_w4_logits(arcs, change, status):
     a = {**W4, **change}
-    at = {k: None if a[k] is None else p(a[k]) for k in ("hidden", "q", "sc", "z", "out")}
+    at = {k: None if a[k] is None else p(a[k]) for k in ("hidden", "q", "sc", "z", "out", "ws")}
+    need = arcs.w4_logits_workspace_bytes(a["B"], a["D"], a["g"])
     assert arcs.library().arcs_w4_logits(at["hidden"], a["B"], a["D"], a["hs"], at["q"], a["V"], a["qs"], at["sc"],
                                          a["sdt"], a["ss"], at["z"], a["zs"], a["g"], at["out"], a["odt"], a["ls"],
-                                         None) == status
+                                         at["ws"], need + a["more"], None) == status
 
 
 CE = dict(h=0, hs=64, w=0, ws=64, dt=BF16, N=4, V=100, D=64, t=0, T=0, loss=0, lse=0, st=0, ws_at=0, ws_bytes=None,
@@ -95,6 +97,9 @@ def test_cross_entropy_backward(arcs, change, status):
 
 
 def test_workspace_sizes(arcs):
+    w4 = arcs.w4_logits_workspace_bytes
+    assert w4(16, 4096, 128) == 0 and w4(17, 4096, 128) >= 32 * 4096 * 2 and w4(300, 96, 32) >= 384 * 96 * 2
+    assert w4(0, 128, 32) == 0 and w4(64, 128, 48) == 0 and w4(64, 0, 32) == 0
     need = arcs.linear_cross_entropy_workspace_bytes
     assert need(4096, 129280, 4096, BF16) >= 256 and need(1, 1, 1, F32, True) >= 256
     for bad in ((0, 10, 10, 0), (10, 0, 10, 0), (10, 10, 0, 0), (10, 10, 65537, 0), (10, 10, 10, 7), (2**23 + 1, 10, 10, 0)):
