@@ -123,7 +123,6 @@ struct W4Args {
   int64_t row_stride;
   // set by the launch
   int tiles, batch_tiles;
-  int whole;               // 128 k's scales, and zero points, can be loaded at once
   int64_t padded_rows;     // of the prepared hidden states
   char* prepared;
   float* sums;

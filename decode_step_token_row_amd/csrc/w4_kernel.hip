@@ -112,52 +112,49 @@ struct W4 {
     }
   };
 
-  // One step's weights, scales and zero points of RT tiles.
-  template <int RT>
-  struct Step {
-    u32x4 w[RT];
-    uint32_t s[RT][kScales], z[RT];
+  // The weights, scales and zero points of RT tiles over NS steps from one on.
+  // All of a row's 64 NS bytes are asked for at once: a line is used while it is
+  // in the cache, and a wave's loads keep NS * RT KB on their way.
+  template <int RT, int NS>
+  struct Part {
+    static constexpr int kN = NS * kGroups;                  // scales of a row
+    static constexpr int kWords = (kN * kScale + 3) / 4, kZeroWords = (kN + 3) / 4;
+    u32x4 w[NS][RT];
+    uint32_t s[RT][kWords], z[RT][kZeroWords];
 
     __device__ __forceinline__ void load(const W4Args& a, const Rows<RT>& rows, int step, int j) {
       const int64_t k = (int64_t)step * kW4Step, first = k / GROUP;
-      const bool here = !kTurn || k + j * 32 < a.D;
+      if (k + NS * kW4Step <= a.D) {
 #pragma unroll
-      for (int t = 0; t < RT; ++t) {
-        w[t] = u32x4{0, 0, 0, 0};
-        if (here) w[t] = *(const u32x4*)(rows.qb + (k >> 1) + rows.qo[t]);
-      }
-      if (a.whole) {  // a step's scales and zero points as one load each
+        for (int t = 0; t < RT; ++t)
+#pragma unroll
+          for (int c = 0; c < NS; ++c) w[c][t] = *(const u32x4*)(rows.qb + (k >> 1) + c * 64 + rows.qo[t]);
 #pragma unroll
         for (int t = 0; t < RT; ++t) {
-          const char* p = rows.sb + first * kScale + rows.so[t];
-          if constexpr (kScales == 4) {
-            const u32x4 x = *(const u32x4*)p;
-#pragma unroll
-            for (int g = 0; g < 4; ++g) s[t][g] = x[g];
-          } else if constexpr (kScales == 2) {
-            const uint2 x = *(const uint2*)p;
-            s[t][0] = x.x;
-            s[t][1] = x.y;
-          } else {
-            s[t][0] = kGroups * kScale == 2 ? *(const uint16_t*)p : *(const uint32_t*)p;
-          }
-          const char* q = rows.zb + first + rows.zo[t];
-          if (ZERO) z[t] = kGroups == 4 ? *(const uint32_t*)q : kGroups == 2 ? *(const uint16_t*)q : *(const uint8_t*)q;
+          __builtin_memcpy(s[t], rows.sb + first * kScale + rows.so[t], kN * kScale);
+          if (ZERO) __builtin_memcpy(z[t], rows.zb + first + rows.zo[t], kN);
         }
         return;
       }
+      // the row's end
 #pragma unroll
       for (int t = 0; t < RT; ++t) {
 #pragma unroll
-        for (int g = 0; g < kScales; ++g) s[t][g] = 0;
-        z[t] = 0;
+        for (int c = 0; c < NS; ++c) {
+          w[c][t] = u32x4{0, 0, 0, 0};
+          if (k + c * kW4Step + j * 32 < a.D) w[c][t] = *(const u32x4*)(rows.qb + (k >> 1) + c * 64 + rows.qo[t]);
+        }
 #pragma unroll
-        for (int g = 0; g < kGroups; ++g) {
+        for (int g = 0; g < kWords; ++g) s[t][g] = 0;
+#pragma unroll
+        for (int g = 0; g < kZeroWords; ++g) z[t][g] = 0;
+#pragma unroll
+        for (int g = 0; g < kN; ++g) {
           if (k + g * GROUP >= a.D) continue;
           const char* p = rows.sb + (first + g) * kScale + rows.so[t];
           if (SF32) s[t][g] = *(const uint32_t*)p;
           else s[t][g / 2] |= (uint32_t) * (const uint16_t*)p << (g % 2 * 16);
-          if (ZERO) z[t] |= (uint32_t) * (const uint8_t*)(rows.zb + first + g + rows.zo[t]) << (g * 8);
+          if (ZERO) z[t][g / 4] |= (uint32_t) * (const uint8_t*)(rows.zb + first + g + rows.zo[t]) << (g % 4 * 8);
         }
       }
     }
@@ -165,7 +162,7 @@ struct W4 {
       return SF32 ? __uint_as_float(s[t][g]) : g % 2 ? bf16_hi(s[t][g / 2]) : bf16_lo(s[t][g / 2]);
     }
     __device__ __forceinline__ uint32_t add(int t, int g) const {
-      return ZERO ? 0x42404240u - ((z[t] >> (g * 8)) & 15u) * 0x00040004u : 0u;
+      return ZERO ? 0x42404240u - ((z[t][g / 4] >> (g % 4 * 8)) & 15u) * 0x00040004u : 0u;
     }
   };
 
@@ -239,30 +236,31 @@ __global__ __launch_bounds__(256, 2) void w4_rows_kernel(W4Args a) {
     }
   };
 
-  typename K::template Step<RT> next[SC];
+  typename K::template Part<RT, SC> next;
   f32x4 total[1][RT];
 #pragma unroll
   for (int t = 0; t < RT; ++t) total[0][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
   fetch_x(0);
-#pragma unroll
-  for (int c = 0; c < SC; ++c)
-    if (c < steps) next[c].load(a, rows, c, j);
+  next.load(a, rows, 0, j);
   store_x(0);
   __syncthreads();
   for (int stage = 0; stage < stages; ++stage) {
-    if (stage + 1 < stages) fetch_x(stage + 1);
+    typename K::template Part<RT, SC> now = next;
+    if (stage + 1 < stages) {
+      fetch_x(stage + 1);
+      next.load(a, rows, (stage + 1) * SC, j);
+    }
     const char* x = s_x[stage & 1];
 #pragma unroll
     for (int c = 0; c < SC; ++c) {
       if (c > 0 && stage * SC + c >= steps) break;
-      typename K::template Step<RT> now = next[c];
-      if ((stage + 1) * SC + c < steps) next[c].load(a, rows, (stage + 1) * SC + c, j);
 #pragma unroll
       for (int t = 0; t < RT; ++t)
-        if (K::kTurn) now.w[t] = w4_turn(now.w[t]);
+        if (K::kTurn) now.w[c][t] = w4_turn(now.w[c][t]);
 #pragma unroll
       for (int g = 0; g < K::kGroups; ++g) {
-        const f32x4 start = *(const f32x4*)&s_sum[stage & 1][c * K::kGroups + g][j * 4];
+        const int gs = c * K::kGroups + g;
+        const f32x4 start = *(const f32x4*)&s_sum[stage & 1][gs][j * 4];
         bf16x8 xf[K::kProducts];
 #pragma unroll
         for (int i = 0; i < K::kProducts; ++i)
@@ -272,10 +270,10 @@ __global__ __launch_bounds__(256, 2) void w4_rows_kernel(W4Args a) {
           f32x4 acc = start;
 #pragma unroll
           for (int i = 0; i < K::kProducts; ++i)
-            acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[i], w4_unpack<ZERO>(now.w[t][g * K::kProducts + i], now.add(t, g)),
-                                                          acc, 0, 0, 0);
+            acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
+                xf[i], w4_unpack<ZERO>(now.w[c][t][g * K::kProducts + i], now.add(t, gs)), acc, 0, 0, 0);
 #pragma unroll
-          for (int e = 0; e < 4; ++e) total[0][t][e] = fmaf(now.scale(t, g), acc[e], total[0][t][e]);
+          for (int e = 0; e < 4; ++e) total[0][t][e] = fmaf(now.scale(t, gs), acc[e], total[0][t][e]);
         }
       }
     }
@@ -303,14 +301,17 @@ __global__ __launch_bounds__(256) void w4_prepare_kernel(W4Args a) {
   if (c % (GROUP / 8) == 0) a.sums[(step * K::kGroups + c / (GROUP / 8)) * a.padded_rows + b] = s;
 }
 
+constexpr int kW4Part = 2;  // steps between two barriers
+
 template <int MT, int RT, int WB, int WV, int GROUP, bool ZERO, bool SF32, bool OF32>
 __global__ __launch_bounds__(WB* WV * 64, 2) void w4_batch_kernel(W4Args a) {
   using K = W4<GROUP, ZERO, SF32>;
-  constexpr int kWaves = WB * WV, kRows = WB * MT * 16;
-  constexpr int kLoads = kRows / 4, kPer = (kLoads + kWaves - 1) / kWaves;  // of 1024 bytes
-  constexpr int kSumBytes = K::kGroups * kRows * 4, kSumLoads = (kSumBytes + 1023) / 1024;
-  constexpr int kStage = kRows * 256 + kSumLoads * 1024;
-  static_assert(kSumLoads <= kWaves && kLoads % kWaves == 0, "loads of a stage over the waves");
+  constexpr int NS = kW4Part, kWaves = WB * WV, kRows = WB * MT * 16;
+  constexpr int kLoads = NS * kRows / 4, kPer = kLoads / kWaves;  // of 1024 bytes
+  constexpr int kN = NS * K::kGroups;                             // groups of a part
+  constexpr int kSumLoads = (kN * kRows * 4 + 1023) / 1024;
+  constexpr int kSumAt = NS * kRows * 256, kStage = kSumAt + kSumLoads * 1024;
+  static_assert(kSumLoads <= kWaves && kLoads % kWaves == 0, "loads of a part over the waves");
   __shared__ __align__(1024) char lds[2 * kStage];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -322,27 +323,27 @@ __global__ __launch_bounds__(WB* WV * 64, 2) void w4_batch_kernel(W4Args a) {
   if (((int)blockIdx.x >> 3) >= per || at >= a.tiles) return;
   const int64_t b0 = (int64_t)(at % a.batch_tiles) * kRows;
   const int64_t v0 = ((int64_t)(at / a.batch_tiles) * WV + wv) * (RT * 16);
-  const int steps = (int)((a.D + kW4Step - 1) / kW4Step);
+  const int parts = (int)((a.D + NS * kW4Step - 1) / (NS * kW4Step));
   const typename K::template Rows<RT> rows(a, v0, r, j);
 
   const uint32_t lds0 = (uint32_t)(uintptr_t)(ARCS_LDS char*)lds;
+  const int64_t step_x = a.padded_rows * 256;
   const char* px = a.prepared + b0 * 256;
   const char* ps = (const char*)(a.sums + b0);
-  const int64_t step_x = a.padded_rows * 256, step_s = (int64_t)K::kGroups * a.padded_rows * 4;
   constexpr int kSumLanes = kRows / 4;  // lanes of one group's sums
   const int sum_group = (wave * 64 + lane) / kSumLanes;
-  const uint32_t sum_off = sum_group < K::kGroups
-                               ? (uint32_t)(sum_group * a.padded_rows * 4 + (wave * 64 + lane) % kSumLanes * 16)
-                               : kNoLoad;
-  auto issue = [&](int step) {
-    const uint32_t to = lds0 + (uint32_t)(step & 1) * kStage;
-    const u32x4 dx = buffer_of(px + step * step_x, kRows * 256);
+  const uint32_t sum_off =
+      sum_group < kN ? (uint32_t)(sum_group * a.padded_rows * 4 + (wave * 64 + lane) % kSumLanes * 16) : kNoLoad;
+  auto issue = [&](int part) {
+    const uint32_t to = lds0 + (uint32_t)(part & 1) * kStage;
 #pragma unroll
     for (int t = 0; t < kPer; ++t) {
-      const uint32_t at = (uint32_t)(wave + t * kWaves) * 1024u;
-      load_to_lds(to + at, at + lane * 16, dx);
+      const int load = wave + t * kWaves, step = load / (kRows / 4), in = load % (kRows / 4);
+      load_to_lds(to + load * 1024u, (uint32_t)(in * 1024 + lane * 16),
+                  buffer_of(px + ((int64_t)part * NS + step) * step_x, kRows * 256));
     }
-    if (wave < kSumLoads) load_to_lds(to + kRows * 256 + wave * 1024u, sum_off, buffer_of(ps + step * step_s, kBufMost));
+    if (wave < kSumLoads)
+      load_to_lds(to + kSumAt + wave * 1024u, sum_off, buffer_of(ps + (int64_t)part * kN * a.padded_rows * 4, kBufMost));
   };
 
   f32x4 total[MT][RT];
@@ -350,59 +351,66 @@ __global__ __launch_bounds__(WB* WV * 64, 2) void w4_batch_kernel(W4Args a) {
   for (int m = 0; m < MT; ++m)
 #pragma unroll
     for (int t = 0; t < RT; ++t) total[m][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  typename K::template Step<RT> next;
+  typename K::template Part<RT, NS> next;
   issue(0);
   next.load(a, rows, 0, j);
-  for (int step = 0; step < steps; ++step) {
-    wait_loads<0>();  // this step's hidden states are in LDS, its weights in registers
+  for (int part = 0; part < parts; ++part) {
+    wait_loads<0>();  // this part's hidden states are in LDS, its weights in registers
     wait_lds();
     __builtin_amdgcn_s_barrier();
-    typename K::template Step<RT> now = next;
-    if (step + 1 < steps) {
-      issue(step + 1);
-      next.load(a, rows, step + 1, j);
+    typename K::template Part<RT, NS> now = next;
+    if (part + 1 < parts) {
+      issue(part + 1);
+      next.load(a, rows, (part + 1) * NS, j);
     }
-    const char* x = lds + (step & 1) * kStage;
-    const float* sums = (const float*)(x + kRows * 256);
+    const char* x = lds + (part & 1) * kStage;
+    const float* sums = (const float*)(x + kSumAt);
 #pragma unroll
-    for (int t = 0; t < RT; ++t)
-      if (K::kTurn) now.w[t] = w4_turn(now.w[t]);
+    for (int c = 0; c < NS; ++c) {
+      u32x4 w[RT];
 #pragma unroll
-    for (int g = 0; g < K::kGroups; ++g) {
-      f32x4 acc[MT][RT];
+      for (int t = 0; t < RT; ++t) w[t] = K::kTurn ? w4_turn(now.w[c][t]) : now.w[c][t];
 #pragma unroll
-      for (int i = 0; i < K::kProducts; ++i) {
-        bf16x8 xf[MT];
+      for (int g = 0; g < K::kGroups; ++g) {
+        const int gs = c * K::kGroups + g;
+        f32x4 acc[MT][RT];
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          const int row = (wb * MT + m) * 16;
-          if (i == 0) {
-            const f32x4 start = *(const f32x4*)(sums + g * kRows + row + j * 4);
+        for (int i = 0; i < K::kProducts; ++i) {
+          bf16x8 xf[MT];
 #pragma unroll
-            for (int t = 0; t < RT; ++t) acc[m][t] = start;
+          for (int m = 0; m < MT; ++m) {
+            const int row = (wb * MT + m) * 16;
+            if (i == 0) {
+              const f32x4 start = *(const f32x4*)(sums + gs * kRows + row + j * 4);
+#pragma unroll
+              for (int t = 0; t < RT; ++t) acc[m][t] = start;
+            }
+            xf[m] = *(const bf16x8*)(x + (c * kRows + row + r) * 256 + ((K::chunk(g * K::kProducts + i, j) ^ r) * 16));
           }
-          xf[m] = *(const bf16x8*)(x + (row + r) * 256 + ((K::chunk(g * K::kProducts + i, j) ^ r) * 16));
+#pragma unroll
+          for (int t = 0; t < RT; ++t) {
+            const bf16x8 wf = w4_unpack<ZERO>(w[t][g * K::kProducts + i], now.add(t, gs));
+#pragma unroll
+            for (int m = 0; m < MT; ++m) acc[m][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[m], wf, acc[m][t], 0, 0, 0);
+          }
         }
 #pragma unroll
-        for (int t = 0; t < RT; ++t) {
-          const bf16x8 wf = w4_unpack<ZERO>(now.w[t][g * K::kProducts + i], now.add(t, g));
+        for (int t = 0; t < RT; ++t)
 #pragma unroll
-          for (int m = 0; m < MT; ++m) acc[m][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[m], wf, acc[m][t], 0, 0, 0);
-        }
+          for (int m = 0; m < MT; ++m)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) total[m][t][e] = fmaf(now.scale(t, gs), acc[m][t][e], total[m][t][e]);
+        __builtin_amdgcn_sched_barrier(0);  // one group's operands at a time in registers
       }
-#pragma unroll
-      for (int t = 0; t < RT; ++t)
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-#pragma unroll
-          for (int e = 0; e < 4; ++e) total[m][t][e] = fmaf(now.scale(t, g), acc[m][t][e], total[m][t][e]);
-      __builtin_amdgcn_sched_barrier(0);  // one group's operands at a time in registers
     }
   }
   w4_write<MT, RT, OF32>(a, total, b0 + wb * MT * 16, v0, r, j);
 }
 
 namespace {
+
+// Steps of the prepared hidden states: whole parts, zeros past D.
+int64_t w4_steps(int64_t D) { return (D + kW4Part * kW4Step - 1) / (kW4Part * kW4Step) * kW4Part; }
 
 template <int RT, int GROUP, bool ZERO, bool SF32>
 void launch_w4_rows(const W4Args& a, bool f32, hipStream_t stream) {
@@ -418,7 +426,7 @@ void launch_w4_batch(W4Args a, bool f32, hipStream_t stream) {
   const int64_t tiles = (a.V + kCols - 1) / kCols * a.batch_tiles;
   a.tiles = (int)tiles;
   hipLaunchKernelGGL((w4_prepare_kernel<GROUP, ZERO>),
-                     dim3((unsigned)((a.D + kW4Step - 1) / kW4Step), (unsigned)(a.padded_rows / 16)), dim3(256), 0, stream, a);
+                     dim3((unsigned)w4_steps(a.D), (unsigned)(a.padded_rows / 16)), dim3(256), 0, stream, a);
   const dim3 grid((unsigned)((tiles + 7) / 8 * 8)), block(WB * WV * 64);
   if (f32) hipLaunchKernelGGL((w4_batch_kernel<MT, RT, WB, WV, GROUP, ZERO, SF32, true>), grid, block, 0, stream, a);
   else hipLaunchKernelGGL((w4_batch_kernel<MT, RT, WB, WV, GROUP, ZERO, SF32, false>), grid, block, 0, stream, a);
@@ -426,18 +434,15 @@ void launch_w4_batch(W4Args a, bool f32, hipStream_t stream) {
 
 template <int GROUP, bool ZERO, bool SF32>
 void launch_w4_typed(W4Args a, bool f32, hipStream_t stream) {
-  constexpr int64_t kGroups = kW4Step / GROUP, kBytes = kGroups * (SF32 ? 4 : 2);
-  a.whole = a.D % kW4Step == 0 && (uintptr_t)a.scales % kBytes == 0 && a.scale_stride * (SF32 ? 4 : 2) % kBytes == 0 &&
-            (!ZERO || ((uintptr_t)a.zeros % kGroups == 0 && a.zero_stride % kGroups == 0));
   if (a.B <= kW4FewRows) {
     if (a.V <= 65536) launch_w4_rows<1, GROUP, ZERO, SF32>(a, f32, stream);
     else launch_w4_rows<2, GROUP, ZERO, SF32>(a, f32, stream);
   } else if (a.B <= 32) {
     launch_w4_batch<2, 4, 1, 4, GROUP, ZERO, SF32>(a, f32, stream);
   } else if (a.B <= 64) {
-    launch_w4_batch<4, 4, 1, 4, GROUP, ZERO, SF32>(a, f32, stream);
+    launch_w4_batch<4, 2, 1, 8, GROUP, ZERO, SF32>(a, f32, stream);
   } else {
-    launch_w4_batch<4, 4, 2, 4, GROUP, ZERO, SF32>(a, f32, stream);
+    launch_w4_batch<8, 2, 1, 8, GROUP, ZERO, SF32>(a, f32, stream);
   }
 }
 
@@ -462,8 +467,7 @@ int64_t padded_rows(int64_t B) {
 
 size_t w4_workspace_bytes(int64_t B, int64_t D, int group) {
   if (B <= kW4FewRows) return 0;
-  const int64_t steps = (D + kW4Step - 1) / kW4Step;
-  return (size_t)(padded_rows(B) * steps * (256 + 4 * (kW4Step / group)));
+  return (size_t)(padded_rows(B) * w4_steps(D) * (256 + 4 * (kW4Step / group)));
 }
 
 hipError_t launch_w4_logits(W4Args a, int scale_dtype, int logits_dtype, int group, void* workspace, hipStream_t stream) {
@@ -471,7 +475,7 @@ hipError_t launch_w4_logits(W4Args a, int scale_dtype, int logits_dtype, int gro
   if (a.B > kW4FewRows) {
     a.padded_rows = padded_rows(a.B);
     a.prepared = (char*)workspace;
-    a.sums = (float*)(a.prepared + a.padded_rows * ((a.D + kW4Step - 1) / kW4Step) * 256);
+    a.sums = (float*)(a.prepared + a.padded_rows * w4_steps(a.D) * 256);
   }
   if (group == 32) launch_w4_group<32>(a, sf32, f32, stream);
   else if (group == 64) launch_w4_group<64>(a, sf32, f32, stream);
