@@ -42,7 +42,7 @@ int noalloc_scratch(void** out) {
 
 constexpr int64_t kMaxDim = 2147483647;
 // arcs_w4_logits: what the launch grids and 32-bit offsets in a tile hold
-constexpr int64_t kMaxW4Stride = int64_t(1) << 23, kMaxW4Batch = int64_t(1) << 19, kMaxW4Vocab = int64_t(1) << 28;
+constexpr int64_t kMaxW4Stride = int64_t(1) << 21, kMaxW4Batch = int64_t(1) << 19, kMaxW4Vocab = int64_t(1) << 28;
 
 int check_common(const void* logits, int dtype, int64_t B, int64_t V, int64_t row_stride,
                  const void* out_ids) {

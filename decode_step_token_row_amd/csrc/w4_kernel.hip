@@ -92,77 +92,72 @@ struct W4 {
   // Where lane group j finds the 8 k of product n of a step, in units of 8.
   static __device__ __forceinline__ int chunk(int n, int j) { return kTurn ? n * 4 + j : j * 4 + n; }
 
-  // RT tiles of 16 weight rows: a uniform base, and a lane's row in each.
+  // RT tiles of 16 weight rows of a wave, through a buffer descriptor: what lies
+  // past D in a row meets hidden states that are zero there, and what lies past
+  // the last row is not read.
   template <int RT>
   struct Rows {
-    const char *qb, *sb, *zb;
-    uint32_t qo[RT], so[RT], zo[RT];
+    const char* base;
+    int64_t bytes;
+    uint32_t off[RT];
     __device__ __forceinline__ Rows(const W4Args& a, int64_t v0, int r, int j) {
-      const int64_t base = v0 < a.V ? v0 : a.V - 1;
-      qb = (const char*)a.qweight + base * a.qweight_stride;
-      sb = (const char*)a.scales + base * a.scale_stride * kScale;
-      zb = (const char*)a.zeros + base * a.zero_stride;
+      const int64_t v = v0 < a.V ? v0 : a.V - 1;
+      base = (const char*)a.qweight + v * a.qweight_stride;
+      bytes = (a.V - 1 - v) * a.qweight_stride + a.D / 2;
 #pragma unroll
-      for (int t = 0; t < RT; ++t) {
-        const uint32_t v = (uint32_t)(base + t * 16 + r < a.V ? t * 16 + r : a.V - 1 - base);
-        qo[t] = v * (uint32_t)a.qweight_stride + j * 16;
-        so[t] = v * (uint32_t)a.scale_stride * kScale;
-        zo[t] = v * (uint32_t)a.zero_stride;
-      }
+      for (int t = 0; t < RT; ++t)
+        off[t] = (uint32_t)(v + t * 16 + r < a.V ? t * 16 + r : a.V - 1 - v) * (uint32_t)a.qweight_stride + j * 16;
+    }
+    // 16 bytes a lane of each tile: k 128 step on
+    __device__ __forceinline__ void load(u32x4 (&w)[RT], int step) const {
+      const int64_t at = (int64_t)step * (kW4Step / 2);
+      const __amdgpu_buffer_rsrc_t d = __builtin_amdgcn_make_buffer_rsrc(
+          (void*)(base + at), (short)0, (int)(bytes - at < (int64_t)kBufMost ? bytes - at : (int64_t)kBufMost), 0x00020000);
+#pragma unroll
+      for (int t = 0; t < RT; ++t) w[t] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(d, off[t], 0, 0));
     }
   };
 
-  // The weights, scales and zero points of RT tiles over NS steps from one on.
-  // All of a row's 64 NS bytes are asked for at once: a line is used while it is
-  // in the cache, and a wave's loads keep NS * RT KB on their way.
-  template <int RT, int NS>
-  struct Part {
-    static constexpr int kN = NS * kGroups;                  // scales of a row
-    static constexpr int kWords = (kN * kScale + 3) / 4, kZeroWords = (kN + 3) / 4;
-    u32x4 w[NS][RT];
-    uint32_t s[RT][kWords], z[RT][kZeroWords];
-
-    __device__ __forceinline__ void load(const W4Args& a, const Rows<RT>& rows, int step, int j) {
-      const int64_t k = (int64_t)step * kW4Step, first = k / GROUP;
-      if (k + NS * kW4Step <= a.D) {
+  // The scales of a workgroup's ROWS weight rows over kN groups, and the
+  // constants of their zero points, on their way to LDS as [row][group] pairs.
+  template <int ROWS, int kN, int THREADS>
+  struct Scales {
+    static constexpr int kPer = (ROWS * kN + THREADS - 1) / THREADS;
+    const char *sb, *zb;
+    uint32_t so[kPer], zo[kPer];
+    uint32_t s[kPer], z[kPer];
+    int groups;
+    __device__ __forceinline__ Scales(const W4Args& a, int64_t v0) {
+      const int64_t v = v0 < a.V ? v0 : a.V - 1;
+      sb = (const char*)a.scales + v * a.scale_stride * kScale;
+      zb = (const char*)a.zeros + v * a.zero_stride;
+      groups = (int)(a.D / GROUP);
 #pragma unroll
-        for (int t = 0; t < RT; ++t)
-#pragma unroll
-          for (int c = 0; c < NS; ++c) w[c][t] = *(const u32x4*)(rows.qb + (k >> 1) + c * 64 + rows.qo[t]);
-#pragma unroll
-        for (int t = 0; t < RT; ++t) {
-          __builtin_memcpy(s[t], rows.sb + first * kScale + rows.so[t], kN * kScale);
-          if (ZERO) __builtin_memcpy(z[t], rows.zb + first + rows.zo[t], kN);
-        }
-        return;
+      for (int i = 0; i < kPer; ++i) {
+        const int e = threadIdx.x + i * THREADS, row = e / kN;
+        const uint32_t at = (uint32_t)(v + row < a.V ? row : a.V - 1 - v);
+        so[i] = (at * (uint32_t)a.scale_stride + e % kN) * kScale;
+        zo[i] = at * (uint32_t)a.zero_stride + e % kN;
       }
-      // the row's end
+    }
+    __device__ __forceinline__ void fetch(int part) {
 #pragma unroll
-      for (int t = 0; t < RT; ++t) {
-#pragma unroll
-        for (int c = 0; c < NS; ++c) {
-          w[c][t] = u32x4{0, 0, 0, 0};
-          if (k + c * kW4Step + j * 32 < a.D) w[c][t] = *(const u32x4*)(rows.qb + (k >> 1) + c * 64 + rows.qo[t]);
-        }
-#pragma unroll
-        for (int g = 0; g < kWords; ++g) s[t][g] = 0;
-#pragma unroll
-        for (int g = 0; g < kZeroWords; ++g) z[t][g] = 0;
-#pragma unroll
-        for (int g = 0; g < kN; ++g) {
-          if (k + g * GROUP >= a.D) continue;
-          const char* p = rows.sb + (first + g) * kScale + rows.so[t];
-          if (SF32) s[t][g] = *(const uint32_t*)p;
-          else s[t][g / 2] |= (uint32_t) * (const uint16_t*)p << (g % 2 * 16);
-          if (ZERO) z[t][g / 4] |= (uint32_t) * (const uint8_t*)(rows.zb + first + g + rows.zo[t]) << (g % 4 * 8);
+      for (int i = 0; i < kPer; ++i) {
+        const int e = threadIdx.x + i * THREADS, g = part * kN + e % kN;
+        s[i] = z[i] = 0;
+        if (e < ROWS * kN && g < groups) {
+          const char* p = sb + (int64_t)part * kN * kScale + so[i];
+          s[i] = SF32 ? *(const uint32_t*)p : (uint32_t) * (const uint16_t*)p << 16;
+          if (ZERO) z[i] = *(const uint8_t*)(zb + (int64_t)part * kN + zo[i]);
         }
       }
     }
-    __device__ __forceinline__ float scale(int t, int g) const {
-      return SF32 ? __uint_as_float(s[t][g]) : g % 2 ? bf16_hi(s[t][g / 2]) : bf16_lo(s[t][g / 2]);
-    }
-    __device__ __forceinline__ uint32_t add(int t, int g) const {
-      return ZERO ? 0x42404240u - ((z[t][g / 4] >> (g % 4 * 8)) & 15u) * 0x00040004u : 0u;
+    __device__ __forceinline__ void store(uint2* to) const {
+#pragma unroll
+      for (int i = 0; i < kPer; ++i) {
+        const int e = threadIdx.x + i * THREADS;
+        if (e < ROWS * kN) to[e] = make_uint2(s[i], 0x42404240u - (z[i] & 15u) * 0x00040004u);
+      }
     }
   };
 
@@ -201,18 +196,20 @@ __device__ __forceinline__ void w4_write(const W4Args& a, const f32x4 (&total)[M
 // ---------------------------------------------------------------------------
 constexpr int kW4Stage = 4;  // steps
 
-template <int RT, int GROUP, bool ZERO, bool SF32, bool OF32>
-__global__ __launch_bounds__(256, 2) void w4_rows_kernel(W4Args a) {
+template <int GROUP, bool ZERO, bool SF32, bool OF32>
+__global__ __launch_bounds__(256, 4) void w4_rows_kernel(W4Args a) {
   using K = W4<GROUP, ZERO, SF32>;
-  constexpr int SC = kW4Stage, kRows = 16, kPer = kRows * SC * 16 / 256;
+  constexpr int SC = kW4Stage, kRows = 16, kPer = kRows * SC * 16 / 256, kN = SC * K::kGroups;
   __shared__ __align__(16) char s_x[2][SC * kRows * 256];
-  __shared__ __align__(16) float s_sum[2][SC * K::kGroups][kRows];
+  __shared__ __align__(16) float s_sum[2][kN][kRows];
+  __shared__ __align__(16) uint2 s_scale[2][64 * kN];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 15, j = lane >> 4;
-  const int64_t v0 = ((int64_t)blockIdx.x * 4 + wave) * (RT * 16);
+  const int64_t v0 = ((int64_t)blockIdx.x * 4 + wave) * 16;
   const int steps = (int)((a.D + kW4Step - 1) / kW4Step), stages = (steps + SC - 1) / SC;
-  const typename K::template Rows<RT> rows(a, v0, r, j);
+  const typename K::template Rows<1> rows(a, v0, r, j);
+  typename K::template Scales<64, kN, 256> scales(a, (int64_t)blockIdx.x * 64);
 
   // the stage's hidden states: piece p of a thread is 8 k of one row, 64 pieces a row
   u32x4 xr[kPer];
@@ -236,51 +233,54 @@ __global__ __launch_bounds__(256, 2) void w4_rows_kernel(W4Args a) {
     }
   };
 
-  typename K::template Part<RT, SC> next;
-  f32x4 total[1][RT];
-#pragma unroll
-  for (int t = 0; t < RT; ++t) total[0][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  u32x4 next[SC][1];
+  f32x4 total[1][1] = {{{0.0f, 0.0f, 0.0f, 0.0f}}};
   fetch_x(0);
-  next.load(a, rows, 0, j);
+  scales.fetch(0);
+#pragma unroll
+  for (int c = 0; c < SC; ++c) rows.load(next[c], c < steps ? c : 0);
   store_x(0);
+  scales.store(s_scale[0]);
   __syncthreads();
   for (int stage = 0; stage < stages; ++stage) {
-    typename K::template Part<RT, SC> now = next;
+    u32x4 now[SC];
+#pragma unroll
+    for (int c = 0; c < SC; ++c) now[c] = next[c][0];
     if (stage + 1 < stages) {
       fetch_x(stage + 1);
-      next.load(a, rows, (stage + 1) * SC, j);
+      scales.fetch(stage + 1);
+      // all of a row's 256 bytes are asked for at once: a line is used while it is cached
+#pragma unroll
+      for (int c = 0; c < SC; ++c) rows.load(next[c], (stage + 1) * SC + c < steps ? (stage + 1) * SC + c : 0);
     }
     const char* x = s_x[stage & 1];
+    const uint2* scale = &s_scale[stage & 1][(wave * 16 + r) * kN];
 #pragma unroll
     for (int c = 0; c < SC; ++c) {
       if (c > 0 && stage * SC + c >= steps) break;
-#pragma unroll
-      for (int t = 0; t < RT; ++t)
-        if (K::kTurn) now.w[c][t] = w4_turn(now.w[c][t]);
+      const u32x4 w = K::kTurn ? w4_turn(now[c]) : now[c];
 #pragma unroll
       for (int g = 0; g < K::kGroups; ++g) {
         const int gs = c * K::kGroups + g;
-        const f32x4 start = *(const f32x4*)&s_sum[stage & 1][gs][j * 4];
-        bf16x8 xf[K::kProducts];
+        const uint2 sc = scale[gs];
+        f32x4 acc = *(const f32x4*)&s_sum[stage & 1][gs][j * 4];
 #pragma unroll
-        for (int i = 0; i < K::kProducts; ++i)
-          xf[i] = *(const bf16x8*)(x + (c * kRows + r) * 256 + ((K::chunk(g * K::kProducts + i, j) ^ r) * 16));
-#pragma unroll
-        for (int t = 0; t < RT; ++t) {
-          f32x4 acc = start;
-#pragma unroll
-          for (int i = 0; i < K::kProducts; ++i)
-            acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(
-                xf[i], w4_unpack<ZERO>(now.w[c][t][g * K::kProducts + i], now.add(t, gs)), acc, 0, 0, 0);
-#pragma unroll
-          for (int e = 0; e < 4; ++e) total[0][t][e] = fmaf(now.scale(t, gs), acc[e], total[0][t][e]);
+        for (int i = 0; i < K::kProducts; ++i) {
+          const bf16x8 xf = *(const bf16x8*)(x + (c * kRows + r) * 256 + ((K::chunk(g * K::kProducts + i, j) ^ r) * 16));
+          acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf, w4_unpack<ZERO>(w[g * K::kProducts + i], sc.y), acc, 0, 0, 0);
         }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) total[0][0][e] = fmaf(__uint_as_float(sc.x), acc[e], total[0][0][e]);
+        asm volatile("" : "+v"(total[0][0]));  // the sums are not left for later
       }
     }
-    if (stage + 1 < stages) store_x(stage + 1);
+    if (stage + 1 < stages) {
+      store_x(stage + 1);
+      scales.store(s_scale[(stage + 1) & 1]);
+    }
     __syncthreads();
   }
-  w4_write<1, RT, OF32>(a, total, 0, v0, r, j);
+  w4_write<1, 1, OF32>(a, total, 0, v0, r, j);
 }
 
 // ---------------------------------------------------------------------------
@@ -301,18 +301,21 @@ __global__ __launch_bounds__(256) void w4_prepare_kernel(W4Args a) {
   if (c % (GROUP / 8) == 0) a.sums[(step * K::kGroups + c / (GROUP / 8)) * a.padded_rows + b] = s;
 }
 
-constexpr int kW4Part = 2;  // steps between two barriers
+// Steps between two barriers: a row's 128 bytes, as far as LDS reaches.
+constexpr int w4_part(int rows, int group) { return rows == 128 && group == 32 ? 1 : 2; }
 
 template <int MT, int RT, int WB, int WV, int GROUP, bool ZERO, bool SF32, bool OF32>
-__global__ __launch_bounds__(WB* WV * 64, 2) void w4_batch_kernel(W4Args a) {
+__global__ __launch_bounds__(WB* WV * 64, MT == 8 ? 2 : 4) void w4_batch_kernel(W4Args a) {
   using K = W4<GROUP, ZERO, SF32>;
-  constexpr int NS = kW4Part, kWaves = WB * WV, kRows = WB * MT * 16;
+  constexpr int NS = w4_part(WB * MT * 16, GROUP), kThreads = WB * WV * 64, kCols = WV * RT * 16;
+  constexpr int kWaves = WB * WV, kRows = WB * MT * 16;
   constexpr int kLoads = NS * kRows / 4, kPer = kLoads / kWaves;  // of 1024 bytes
   constexpr int kN = NS * K::kGroups;                             // groups of a part
   constexpr int kSumLoads = (kN * kRows * 4 + 1023) / 1024;
   constexpr int kSumAt = NS * kRows * 256, kStage = kSumAt + kSumLoads * 1024;
   static_assert(kSumLoads <= kWaves && kLoads % kWaves == 0, "loads of a part over the waves");
   __shared__ __align__(1024) char lds[2 * kStage];
+  __shared__ __align__(16) uint2 s_scale[2][kCols * kN];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int r = lane & 15, j = lane >> 4;
@@ -322,9 +325,10 @@ __global__ __launch_bounds__(WB* WV * 64, 2) void w4_batch_kernel(W4Args a) {
   const int per = (a.tiles + 7) / 8, at = ((int)blockIdx.x & 7) * per + ((int)blockIdx.x >> 3);
   if (((int)blockIdx.x >> 3) >= per || at >= a.tiles) return;
   const int64_t b0 = (int64_t)(at % a.batch_tiles) * kRows;
-  const int64_t v0 = ((int64_t)(at / a.batch_tiles) * WV + wv) * (RT * 16);
+  const int64_t vb = (int64_t)(at / a.batch_tiles) * kCols, v0 = vb + wv * (RT * 16);
   const int parts = (int)((a.D + NS * kW4Step - 1) / (NS * kW4Step));
   const typename K::template Rows<RT> rows(a, v0, r, j);
+  typename K::template Scales<kCols, kN, kThreads> scales(a, vb);
 
   const uint32_t lds0 = (uint32_t)(uintptr_t)(ARCS_LDS char*)lds;
   const int64_t step_x = a.padded_rows * 256;
@@ -351,28 +355,38 @@ __global__ __launch_bounds__(WB* WV * 64, 2) void w4_batch_kernel(W4Args a) {
   for (int m = 0; m < MT; ++m)
 #pragma unroll
     for (int t = 0; t < RT; ++t) total[m][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-  typename K::template Part<RT, NS> next;
+  u32x4 next[NS][RT];
+  scales.fetch(0);
   issue(0);
-  next.load(a, rows, 0, j);
+#pragma unroll
+  for (int c = 0; c < NS; ++c) rows.load(next[c], c);
+  scales.store(s_scale[0]);
   for (int part = 0; part < parts; ++part) {
-    wait_loads<0>();  // this part's hidden states are in LDS, its weights in registers
+    // This part's hidden states are in LDS: only its weights, NS * RT loads issued
+    // after them, may be on their way.
+    wait_loads<NS * RT>();
     wait_lds();
     __builtin_amdgcn_s_barrier();
-    typename K::template Part<RT, NS> now = next;
     if (part + 1 < parts) {
+      scales.fetch(part + 1);
       issue(part + 1);
-      next.load(a, rows, (part + 1) * NS, j);
     }
+    const int ahead = part + 1 < parts ? (part + 1) * NS : 0;  // the last part's loads are not used
     const char* x = lds + (part & 1) * kStage;
+    const uint2* scale = &s_scale[part & 1][(wv * RT * 16 + r) * kN];
     const float* sums = (const float*)(x + kSumAt);
 #pragma unroll
     for (int c = 0; c < NS; ++c) {
       u32x4 w[RT];
 #pragma unroll
-      for (int t = 0; t < RT; ++t) w[t] = K::kTurn ? w4_turn(now.w[c][t]) : now.w[c][t];
+      for (int t = 0; t < RT; ++t) w[t] = K::kTurn ? w4_turn(next[c][t]) : next[c][t];
+      rows.load(next[c], ahead + c);
 #pragma unroll
       for (int g = 0; g < K::kGroups; ++g) {
         const int gs = c * K::kGroups + g;
+        uint2 sc[RT];
+#pragma unroll
+        for (int t = 0; t < RT; ++t) sc[t] = scale[t * 16 * kN + gs];
         f32x4 acc[MT][RT];
 #pragma unroll
         for (int i = 0; i < K::kProducts; ++i) {
@@ -389,7 +403,7 @@ __global__ __launch_bounds__(WB* WV * 64, 2) void w4_batch_kernel(W4Args a) {
           }
 #pragma unroll
           for (int t = 0; t < RT; ++t) {
-            const bf16x8 wf = w4_unpack<ZERO>(w[t][g * K::kProducts + i], now.add(t, gs));
+            const bf16x8 wf = w4_unpack<ZERO>(w[t][g * K::kProducts + i], sc[t].y);
 #pragma unroll
             for (int m = 0; m < MT; ++m) acc[m][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[m], wf, acc[m][t], 0, 0, 0);
           }
@@ -399,24 +413,29 @@ __global__ __launch_bounds__(WB* WV * 64, 2) void w4_batch_kernel(W4Args a) {
 #pragma unroll
           for (int m = 0; m < MT; ++m)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) total[m][t][e] = fmaf(now.scale(t, gs), acc[m][t][e], total[m][t][e]);
-        __builtin_amdgcn_sched_barrier(0);  // one group's operands at a time in registers
+            for (int e = 0; e < 4; ++e) total[m][t][e] = fmaf(__uint_as_float(sc[t].x), acc[m][t][e], total[m][t][e]);
+        // one group at a time in registers: its sums are not left for later
+#pragma unroll
+        for (int t = 0; t < RT; ++t)
+#pragma unroll
+          for (int m = 0; m < MT; ++m) asm volatile("" : "+v"(total[m][t]));
       }
     }
+    if (part + 1 < parts) scales.store(s_scale[(part + 1) & 1]);
   }
   w4_write<MT, RT, OF32>(a, total, b0 + wb * MT * 16, v0, r, j);
 }
 
 namespace {
 
-// Steps of the prepared hidden states: whole parts, zeros past D.
-int64_t w4_steps(int64_t D) { return (D + kW4Part * kW4Step - 1) / (kW4Part * kW4Step) * kW4Part; }
+// Steps of the prepared hidden states: whole parts of two, zeros past D.
+int64_t w4_steps(int64_t D) { return (D + 2 * kW4Step - 1) / (2 * kW4Step) * 2; }
 
-template <int RT, int GROUP, bool ZERO, bool SF32>
+template <int GROUP, bool ZERO, bool SF32>
 void launch_w4_rows(const W4Args& a, bool f32, hipStream_t stream) {
-  const dim3 grid((unsigned)((a.V + 64 * RT - 1) / (64 * RT))), block(256);
-  if (f32) hipLaunchKernelGGL((w4_rows_kernel<RT, GROUP, ZERO, SF32, true>), grid, block, 0, stream, a);
-  else hipLaunchKernelGGL((w4_rows_kernel<RT, GROUP, ZERO, SF32, false>), grid, block, 0, stream, a);
+  const dim3 grid((unsigned)((a.V + 63) / 64)), block(256);
+  if (f32) hipLaunchKernelGGL((w4_rows_kernel<GROUP, ZERO, SF32, true>), grid, block, 0, stream, a);
+  else hipLaunchKernelGGL((w4_rows_kernel<GROUP, ZERO, SF32, false>), grid, block, 0, stream, a);
 }
 
 template <int MT, int RT, int WB, int WV, int GROUP, bool ZERO, bool SF32>
@@ -435,10 +454,9 @@ void launch_w4_batch(W4Args a, bool f32, hipStream_t stream) {
 template <int GROUP, bool ZERO, bool SF32>
 void launch_w4_typed(W4Args a, bool f32, hipStream_t stream) {
   if (a.B <= kW4FewRows) {
-    if (a.V <= 65536) launch_w4_rows<1, GROUP, ZERO, SF32>(a, f32, stream);
-    else launch_w4_rows<2, GROUP, ZERO, SF32>(a, f32, stream);
+    launch_w4_rows<GROUP, ZERO, SF32>(a, f32, stream);
   } else if (a.B <= 32) {
-    launch_w4_batch<2, 4, 1, 4, GROUP, ZERO, SF32>(a, f32, stream);
+    launch_w4_batch<2, 2, 1, 8, GROUP, ZERO, SF32>(a, f32, stream);
   } else if (a.B <= 64) {
     launch_w4_batch<4, 2, 1, 8, GROUP, ZERO, SF32>(a, f32, stream);
   } else {

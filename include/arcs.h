@@ -449,7 +449,7 @@ int arcs_commit_tokens(const int32_t* ids, int64_t B, int64_t V, int32_t* next_i
  *                  none is needed
  * Returns ARCS_OK or a negative arcs_status (nothing launched then):
  * ARCS_ERR_BAD_STRIDE for any stride below its row, or a stride of qweight,
- * scales or zeros above 2^23, ARCS_ERR_MISALIGNED for `hidden` or `qweight`
+ * scales or zeros above 2^21, ARCS_ERR_MISALIGNED for `hidden` or `qweight`
  * rows that are not 16-byte aligned or another array not aligned to its
  * element, ARCS_ERR_BAD_BATCH also for B above 2^19 or B * V above 2^36,
  * ARCS_ERR_BAD_VOCAB also for V above 2^28.

@@ -45,7 +45,7 @@ W4 = dict(hidden=0, B=4, D=256, hs=256, q=0, V=100, qs=128, sc=0, sdt=BF16, ss=2
     (dict(V=0), VOCAB), (dict(V=2**31), VOCAB), (dict(D=0, hs=0), HIDDEN), (dict(D=65664, hs=65664, qs=32832), HIDDEN),
     (dict(g=0), GROUP), (dict(g=16), GROUP), (dict(g=256), GROUP), (dict(g=-32), GROUP), (dict(D=192, g=128), GROUP),
     (dict(D=250), GROUP), (dict(hs=255), STRIDE), (dict(qs=127), STRIDE), (dict(ss=1), STRIDE), (dict(zs=1), STRIDE),
-    (dict(ls=99), STRIDE), (dict(qs=2**23 + 16), STRIDE), (dict(ss=2**23 + 1), STRIDE), (dict(hidden=8), MISALIGNED), (dict(hs=260), MISALIGNED), (dict(q=4), MISALIGNED),
+    (dict(ls=99), STRIDE), (dict(qs=2**21 + 16), STRIDE), (dict(ss=2**21 + 1), STRIDE), (dict(hidden=8), MISALIGNED), (dict(hs=260), MISALIGNED), (dict(q=4), MISALIGNED),
     (dict(qs=136), MISALIGNED), (dict(sc=1), MISALIGNED), (dict(sdt=F32, sc=2), MISALIGNED), (dict(out=1), MISALIGNED),
     (dict(odt=F32, out=2), MISALIGNED), (dict(B=40, ws=None), NULL), (dict(B=40, ws=16), MISALIGNED),
     (dict(B=40, more=-1), SMALL),
