@@ -89,8 +89,9 @@ struct W4 {
   static constexpr int kScales = (kGroups * kScale + 3) / 4;  // words of a step's scales
   static constexpr float kOffset = ZERO ? -48.0f : -24.0f;
 
-  // Where lane group j finds the 8 k of product n of a step, in units of 8.
-  static __device__ __forceinline__ int chunk(int n, int j) { return kTurn ? n * 4 + j : j * 4 + n; }
+  // Chunk c of 8 k of a step is lane group j's in product n; the LDS slot of (n, j) is 4 n + j
+  // in a row of 16 chunks, then turned by the row, so that no two lanes of a read share a bank.
+  static __device__ __forceinline__ int slot(int c) { return kTurn ? c : (c & 3) * 4 + (c >> 2); }
 
   // RT tiles of 16 weight rows of a wave, through a buffer descriptor: what lies
   // past D in a row meets hidden states that are zero there, and what lies past
@@ -119,10 +120,12 @@ struct W4 {
   };
 
   // The scales of a workgroup's ROWS weight rows over kN groups, and the
-  // constants of their zero points, on their way to LDS as [row][group] pairs.
+  // constants of their zero points, on their way to LDS as [group][row] pairs.
+  // fetch only loads (a conversion beside a load would wait for it there).
   template <int ROWS, int kN, int THREADS>
   struct Scales {
-    static constexpr int kPer = (ROWS * kN + THREADS - 1) / THREADS;
+    static_assert(ROWS * kN % THREADS == 0, "scales of a part over the threads");
+    static constexpr int kPer = ROWS * kN / THREADS;
     const char *sb, *zb;
     uint32_t so[kPer], zo[kPer];
     uint32_t s[kPer], z[kPer];
@@ -134,29 +137,28 @@ struct W4 {
       groups = (int)(a.D / GROUP);
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
-        const int e = threadIdx.x + i * THREADS, row = e / kN;
+        const int row = (threadIdx.x + i * THREADS) / kN;
         const uint32_t at = (uint32_t)(v + row < a.V ? row : a.V - 1 - v);
-        so[i] = (at * (uint32_t)a.scale_stride + e % kN) * kScale;
-        zo[i] = at * (uint32_t)a.zero_stride + e % kN;
+        so[i] = at * (uint32_t)a.scale_stride * kScale;
+        zo[i] = at * (uint32_t)a.zero_stride;
       }
     }
     __device__ __forceinline__ void fetch(int part) {
+      int g = part * kN + threadIdx.x % kN;  // THREADS is a multiple of kN
+      g = g < groups ? g : groups - 1;
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
-        const int e = threadIdx.x + i * THREADS, g = part * kN + e % kN;
-        s[i] = z[i] = 0;
-        if (e < ROWS * kN && g < groups) {
-          const char* p = sb + (int64_t)part * kN * kScale + so[i];
-          s[i] = SF32 ? *(const uint32_t*)p : (uint32_t) * (const uint16_t*)p << 16;
-          if (ZERO) z[i] = *(const uint8_t*)(zb + (int64_t)part * kN + zo[i]);
-        }
+        const char* p = sb + (so[i] + (uint32_t)g * kScale);
+        s[i] = SF32 ? *(const uint32_t*)p : *(const uint16_t*)p;
+        if (ZERO) z[i] = *(const uint8_t*)(zb + (zo[i] + (uint32_t)g));
       }
     }
     __device__ __forceinline__ void store(uint2* to) const {
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
         const int e = threadIdx.x + i * THREADS;
-        if (e < ROWS * kN) to[e] = make_uint2(s[i], 0x42404240u - (z[i] & 15u) * 0x00040004u);
+        to[e % kN * ROWS + e / kN] =
+            make_uint2(SF32 ? s[i] : s[i] << 16, ZERO ? 0x42404240u - (z[i] & 15u) * 0x00040004u : 0u);
       }
     }
   };
@@ -218,7 +220,7 @@ __global__ __launch_bounds__(256, 4) void w4_rows_kernel(W4Args a) {
 #pragma unroll
     for (int p = 0; p < kPer; ++p) {
       const int row = wave + p * 4;
-      if (row < a.B) xr[p] = k < a.D ? *(const u32x4*)(a.hidden + row * a.hidden_stride + k) : u32x4{0, 0, 0, 0};
+      if (row < a.B) xr[p] = *(const u32x4*)(a.hidden + row * a.hidden_stride + (k < a.D ? k : 0));
     }
   };
   auto store_x = [&](int stage) {
@@ -227,8 +229,9 @@ __global__ __launch_bounds__(256, 4) void w4_rows_kernel(W4Args a) {
     for (int p = 0; p < kPer; ++p) {
       const int row = wave + p * 4;
       if (row >= a.B) continue;
+      if ((int64_t)stage * SC * kW4Step + lane * 8 >= a.D) xr[p] = u32x4{0, 0, 0, 0};
       const float s = K::group_sum(xr[p]);
-      *(u32x4*)(x + row * 256 + (((lane & 15) ^ row) * 16)) = w4_order(xr[p]);
+      *(u32x4*)(x + row * 256 + ((K::slot(lane & 15) ^ row) * 16)) = w4_order(xr[p]);
       if (lane % (GROUP / 8) == 0) s_sum[stage & 1][lane / (GROUP / 8)][row] = s;
     }
   };
@@ -254,7 +257,7 @@ __global__ __launch_bounds__(256, 4) void w4_rows_kernel(W4Args a) {
       for (int c = 0; c < SC; ++c) rows.load(next[c], (stage + 1) * SC + c < steps ? (stage + 1) * SC + c : 0);
     }
     const char* x = s_x[stage & 1];
-    const uint2* scale = &s_scale[stage & 1][(wave * 16 + r) * kN];
+    const uint2* scale = &s_scale[stage & 1][wave * 16 + r];
 #pragma unroll
     for (int c = 0; c < SC; ++c) {
       if (c > 0 && stage * SC + c >= steps) break;
@@ -262,11 +265,12 @@ __global__ __launch_bounds__(256, 4) void w4_rows_kernel(W4Args a) {
 #pragma unroll
       for (int g = 0; g < K::kGroups; ++g) {
         const int gs = c * K::kGroups + g;
-        const uint2 sc = scale[gs];
+        if (K::kTurn && (int64_t)(stage * SC + c) * kW4Step + g * GROUP >= a.D) break;  // no such group
+        const uint2 sc = scale[gs * 64];
         f32x4 acc = *(const f32x4*)&s_sum[stage & 1][gs][j * 4];
 #pragma unroll
         for (int i = 0; i < K::kProducts; ++i) {
-          const bf16x8 xf = *(const bf16x8*)(x + (c * kRows + r) * 256 + ((K::chunk(g * K::kProducts + i, j) ^ r) * 16));
+          const bf16x8 xf = *(const bf16x8*)(x + (c * kRows + r) * 256 + ((((g * K::kProducts + i) * 4 + j) ^ r) * 16));
           acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf, w4_unpack<ZERO>(w[g * K::kProducts + i], sc.y), acc, 0, 0, 0);
         }
 #pragma unroll
@@ -285,7 +289,7 @@ __global__ __launch_bounds__(256, 4) void w4_rows_kernel(W4Args a) {
 
 // ---------------------------------------------------------------------------
 // More rows.  The prepared hidden states of one step are 4096 bytes for every 16
-// rows: row x 256 bytes, chunk c of 8 k at c ^ row; rows past B are zeros.  The
+// rows: row x 256 bytes, chunk c of 8 k at slot(c) ^ row; rows past B are zeros.  The
 // sums are [step][group][row].
 // ---------------------------------------------------------------------------
 template <int GROUP, bool ZERO>
@@ -297,7 +301,7 @@ __global__ __launch_bounds__(256) void w4_prepare_kernel(W4Args a) {
   if (b < a.B && k < a.D) v = *(const u32x4*)(a.hidden + b * a.hidden_stride + k);
   const float s = K::group_sum(v);
   const int64_t tiles = a.padded_rows / 16;
-  *(u32x4*)(a.prepared + (step * tiles + tile) * 4096 + row * 256 + ((c ^ row) * 16)) = w4_order(v);
+  *(u32x4*)(a.prepared + (step * tiles + tile) * 4096 + row * 256 + ((K::slot(c) ^ row) * 16)) = w4_order(v);
   if (c % (GROUP / 8) == 0) a.sums[(step * K::kGroups + c / (GROUP / 8)) * a.padded_rows + b] = s;
 }
 
@@ -305,7 +309,7 @@ __global__ __launch_bounds__(256) void w4_prepare_kernel(W4Args a) {
 constexpr int w4_part(int rows, int group) { return rows == 128 && group == 32 ? 1 : 2; }
 
 template <int MT, int RT, int WB, int WV, int GROUP, bool ZERO, bool SF32, bool OF32>
-__global__ __launch_bounds__(WB* WV * 64, MT == 8 ? 2 : 4) void w4_batch_kernel(W4Args a) {
+__global__ __launch_bounds__(WB* WV * 64, MT == 2 ? 3 : 2) void w4_batch_kernel(W4Args a) {
   using K = W4<GROUP, ZERO, SF32>;
   constexpr int NS = w4_part(WB * MT * 16, GROUP), kThreads = WB * WV * 64, kCols = WV * RT * 16;
   constexpr int kWaves = WB * WV, kRows = WB * MT * 16;
@@ -343,8 +347,8 @@ __global__ __launch_bounds__(WB* WV * 64, MT == 8 ? 2 : 4) void w4_batch_kernel(
 #pragma unroll
     for (int t = 0; t < kPer; ++t) {
       const int load = wave + t * kWaves, step = load / (kRows / 4), in = load % (kRows / 4);
-      load_to_lds(to + load * 1024u, (uint32_t)(in * 1024 + lane * 16),
-                  buffer_of(px + ((int64_t)part * NS + step) * step_x, kRows * 256));
+      load_to_lds(to + load * 1024u, (uint32_t)lane * 16,
+                  buffer_of(px + ((int64_t)part * NS + step) * step_x + in * 1024, 1024));
     }
     if (wave < kSumLoads)
       load_to_lds(to + kSumAt + wave * 1024u, sum_off, buffer_of(ps + (int64_t)part * kN * a.padded_rows * 4, kBufMost));
@@ -373,7 +377,7 @@ __global__ __launch_bounds__(WB* WV * 64, MT == 8 ? 2 : 4) void w4_batch_kernel(
     }
     const int ahead = part + 1 < parts ? (part + 1) * NS : 0;  // the last part's loads are not used
     const char* x = lds + (part & 1) * kStage;
-    const uint2* scale = &s_scale[part & 1][(wv * RT * 16 + r) * kN];
+    const uint2* scale = &s_scale[part & 1][wv * RT * 16 + r];
     const float* sums = (const float*)(x + kSumAt);
 #pragma unroll
     for (int c = 0; c < NS; ++c) {
@@ -384,9 +388,10 @@ __global__ __launch_bounds__(WB* WV * 64, MT == 8 ? 2 : 4) void w4_batch_kernel(
 #pragma unroll
       for (int g = 0; g < K::kGroups; ++g) {
         const int gs = c * K::kGroups + g;
+        if ((int64_t)(part * NS + c) * kW4Step + g * GROUP >= a.D) break;  // no such group
         uint2 sc[RT];
 #pragma unroll
-        for (int t = 0; t < RT; ++t) sc[t] = scale[t * 16 * kN + gs];
+        for (int t = 0; t < RT; ++t) sc[t] = scale[gs * kCols + t * 16];
         f32x4 acc[MT][RT];
 #pragma unroll
         for (int i = 0; i < K::kProducts; ++i) {
@@ -399,7 +404,7 @@ __global__ __launch_bounds__(WB* WV * 64, MT == 8 ? 2 : 4) void w4_batch_kernel(
 #pragma unroll
               for (int t = 0; t < RT; ++t) acc[m][t] = start;
             }
-            xf[m] = *(const bf16x8*)(x + (c * kRows + row + r) * 256 + ((K::chunk(g * K::kProducts + i, j) ^ r) * 16));
+            xf[m] = *(const bf16x8*)(x + (c * kRows + row + r) * 256 + ((((g * K::kProducts + i) * 4 + j) ^ r) * 16));
           }
 #pragma unroll
           for (int t = 0; t < RT; ++t) {
@@ -456,9 +461,9 @@ void launch_w4_typed(W4Args a, bool f32, hipStream_t stream) {
   if (a.B <= kW4FewRows) {
     launch_w4_rows<GROUP, ZERO, SF32>(a, f32, stream);
   } else if (a.B <= 32) {
-    launch_w4_batch<2, 2, 1, 8, GROUP, ZERO, SF32>(a, f32, stream);
+    launch_w4_batch<2, 2, 1, 4, GROUP, ZERO, SF32>(a, f32, stream);
   } else if (a.B <= 64) {
-    launch_w4_batch<4, 2, 1, 8, GROUP, ZERO, SF32>(a, f32, stream);
+    launch_w4_batch<4, 4, 1, 4, GROUP, ZERO, SF32>(a, f32, stream);
   } else {
     launch_w4_batch<8, 2, 1, 8, GROUP, ZERO, SF32>(a, f32, stream);
   }
