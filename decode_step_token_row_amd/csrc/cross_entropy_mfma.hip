@@ -174,43 +174,80 @@ __global__ __launch_bounds__(WM* WN * 64) void ce_tile_kernel(CeArgs a, CePiece 
 
   const int wm = (wave % WM) * MT * 32, wn = (wave / WM) * NT * 32;
   const int fr = lane & 31, fh = lane >> 5;
-  // fragment of 32 rows from `at` at k step ks of a stage
-  auto frag_inner = [&](const char* s, int at, int ks) {
-    return *(const bf16x8*)(s + (at + fr) * 128 + (((ks * 2 + fh) ^ ((lane >> 1) & 7)) * 16));
-  };
-  auto frag_outer = [&](const char* s, int width, int at, int ks) {
-    const int k = ks * 16 + fh * 8 + ((lane & 15) >> 2);
-    const int turn = width >= 128 ? (k & 3) << 1 : width == 64 ? ((k >> 1) & 1) << 1 : 0;
-    const char* p = s + k * width * 2 + (((at >> 4) + ((lane >> 4) & 1)) ^ turn) * 32 + (lane & 3) * 8;
-    const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((ARCS_LDS s16x4*)p);
-    const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((ARCS_LDS s16x4*)(p + 4 * width * 2));
+  // A lane's fragments in a stage, as LDS addresses: along k one place for each
+  // k step (tiles of 32 rows are 4096 bytes apart), along m one for each tile
+  // (k steps are 16 rows apart).
+  uint32_t pa_lds[4], pb_lds[4];
+#pragma unroll
+  for (int t = 0; t < 4; ++t) {
+    const uint32_t inner = fr * 128 + (((t * 2 + fh) ^ ((lane >> 1) & 7)) * 16);
+    auto outer = [&](int width, int at) {
+      const int k = fh * 8 + ((lane & 15) >> 2);
+      const int turn = width >= 128 ? (k & 3) << 1 : width == 64 ? ((k >> 1) & 1) << 1 : 0;
+      return (uint32_t)(k * width * 2 + (((at >> 4) + ((lane >> 4) & 1)) ^ turn) * 32 + (lane & 3) * 8);
+    };
+    pa_lds[t] = lds0 + (C::kAOuter ? outer(BM, wm + t * 32) : wm * 128 + inner);
+    pb_lds[t] = lds0 + C::kABytes + (C::kBOuter ? outer(BN, wn + t * 32) : wn * 128 + inner);
+  }
+  auto frag_inner = [](uint32_t at) { return *(const ARCS_LDS bf16x8*)(uintptr_t)at; };
+  auto frag_outer = [](uint32_t at, int width) {
+    const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((ARCS_LDS s16x4*)(uintptr_t)at);
+    const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((ARCS_LDS s16x4*)(uintptr_t)(at + 8 * width));
     return __builtin_bit_cast(bf16x8, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
   };
 
+  // Fragments of step ks + 1 are read while step ks multiplies.  The last step of
+  // a tile reads from the next one: there the workgroup meets, once a tile, the
+  // next tile has landed and this one's buffer is filled again.
+  bf16x8 fa[2][MT], fb[2][NT];
+  auto read = [&](int kt, int ks) {
+    const uint32_t at = (uint32_t)(kt % S) * C::kStage;
 #pragma unroll
-  for (int s = 0; s < S - 1; ++s)
-    if (s < nk) issue(s);
-  for (int kt = 0; kt < nk; ++kt) {
-    // tile kt has landed: at most the S - 2 tiles after it are on their way
-    if (kt + S - 2 < nk) wait_loads<(S - 2) * C::kPer>();
+    for (int i = 0; i < MT; ++i)
+      fa[ks & 1][i] = C::kAOuter ? frag_outer(pa_lds[i] + at + ks * 32 * BM, BM) : frag_inner(pa_lds[ks] + at + i * 4096);
+#pragma unroll
+    for (int j = 0; j < NT; ++j)
+      fb[ks & 1][j] = C::kBOuter ? frag_outer(pb_lds[j] + at + ks * 32 * BN, BN) : frag_inner(pb_lds[ks] + at + j * 4096);
+  };
+  auto multiply = [&](int ks) {
+#pragma unroll
+    for (int i = 0; i < MT; ++i)
+#pragma unroll
+      for (int j = 0; j < NT; ++j)
+        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[ks & 1][i], fb[ks & 1][j], acc[i][j], 0, 0, 0);
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  if (nk > 0) {
+#pragma unroll
+    for (int s = 0; s < S; ++s)
+      if (s < nk) issue(s);
+    if (nk >= S) wait_loads<(S - 1) * C::kPer>();
     else wait_loads<0>();
-    wait_lds();  // this wave's reads of the stage that is filled next are done
     __builtin_amdgcn_s_barrier();
-    if (kt + S - 1 < nk) issue(kt + S - 1);
-    const char* sa = lds + (kt % S) * C::kStage;
-    const char* sb = sa + C::kABytes;
+    read(0, 0);
+  }
+  for (int kt = 0; kt < nk - 1; ++kt) {
 #pragma unroll
-    for (int ks = 0; ks < 4; ++ks) {
-      bf16x8 fa[MT], fb[NT];
-#pragma unroll
-      for (int i = 0; i < MT; ++i) fa[i] = C::kAOuter ? frag_outer(sa, BM, wm + i * 32, ks) : frag_inner(sa, wm + i * 32, ks);
-#pragma unroll
-      for (int j = 0; j < NT; ++j) fb[j] = C::kBOuter ? frag_outer(sb, BN, wn + j * 32, ks) : frag_inner(sb, wn + j * 32, ks);
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int j = 0; j < NT; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[i], fb[j], acc[i][j], 0, 0, 0);
+    for (int ks = 0; ks < 3; ++ks) {
+      read(kt, ks + 1);
+      multiply(ks);
     }
+    // tile kt + 1 has landed: at most the S - 2 tiles after it are on their way
+    if (kt + S - 1 < nk) wait_loads<(S - 2) * C::kPer>();
+    else wait_loads<0>();
+    wait_lds();  // this wave's reads of tile kt are done
+    __builtin_amdgcn_s_barrier();
+    if (kt + S < nk) issue(kt + S);
+    read(kt + 1, 0);
+    multiply(3);
+  }
+  if (nk > 0) {
+#pragma unroll
+    for (int ks = 0; ks < 3; ++ks) {
+      read(nk - 1, ks + 1);
+      multiply(ks);
+    }
+    multiply(3);
   }
 
   // A lane holds column n = lane % 32 of each 32 x 32 product and rows
