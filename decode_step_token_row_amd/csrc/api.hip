@@ -179,6 +179,7 @@ arcs::CeArgs cross_entropy_args(const void* hidden, int64_t hidden_stride, const
   a.ds_ld = p.piece;
   a.slab = (float*)(w + p.slab);
   a.splits = p.splits;
+  a.workers = p.workers;
   a.hc = w + p.hc;
   return a;
 }

@@ -63,8 +63,9 @@ struct CeArgs {
   float* ytarget;   // forward: [N] y of the target
   void* ds;         // backward: [N][ds_ld] dz / gmax of one piece of the vocabulary
   int64_t ds_ld;    // (also the piece's length)
-  float* slab;      // backward: [splits][N][D] partial sums of dhidden / gmax
-  int splits;
+  float* slab;      // backward: partial sums of dhidden / gmax: [splits][N][D], or parts of tiles (matrix kernels)
+  int splits;       // general kernel: of k in dhidden
+  int workers;      // matrix kernels: workgroups that share dhidden's tiles
   void* hc;         // backward, matrix kernels: [N][D] hidden states of the listed rows
 };
 
@@ -72,10 +73,13 @@ struct CeArgs {
 struct CePlan {
   size_t rows, place, partial, ytarget, ds, slab, hc, total;
   int64_t slices, piece;
-  int splits;
+  int splits, workers;
   bool fits;  // the sizes fit size_t and the launch grids
 };
 CePlan cross_entropy_plan(int64_t N, int64_t V, int64_t D, int dtype, bool backward);
+
+// Matrix kernels: rows of a tile's n side, by the call's rows.
+inline int ce_rows_of_tile(int64_t N) { return N <= 32 ? 32 : N <= 64 ? 64 : N <= 128 ? 128 : 256; }
 
 hipError_t launch_cross_entropy(const CeArgs& a, int dtype, bool backward, hipStream_t stream);
 

@@ -383,7 +383,16 @@ CePlan cross_entropy_plan(int64_t N, int64_t V, int64_t D, int dtype, bool backw
     p.splits = (int)(splits < 1 ? 1 : splits);
     p.place = take((u128)N * 4);
     p.ds = take((u128)N * p.piece * 4);
-    p.slab = take((u128)p.splits * N * D * 4);
+    u128 slab = (u128)p.splits * N * D * 4;
+    if (bf16) {
+      const int64_t rows = ce_rows_of_tile(N);
+      // one workgroup for each compute unit, unless that leaves them less than 512 of k
+      const int64_t t = tiles(N, rows) * tiles(D, 256), most = t * tiles(p.piece, 512);
+      p.workers = most < 256 ? (int)tiles(most, 8) * 8 : 256;
+      const u128 parts = (u128)(p.workers + t) * rows * 256 * 4;
+      if (parts > slab) slab = parts;
+    }
+    p.slab = take(slab);
   }
   if (at > (u128)INT64_MAX) p.fits = false;
   p.total = (size_t)at;

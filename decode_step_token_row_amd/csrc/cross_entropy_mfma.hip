@@ -41,6 +41,17 @@ struct CeTile {
   static constexpr int kLds = S * kStage > kOut ? S * kStage : kOut;
 };
 
+// Tile `id` of mt x nt: bands of eight along m, in a band m first.
+__device__ __forceinline__ void ce_tile_place(int id, int mt, int nt, int64_t& m, int64_t& n) {
+  const int band = id / (8 * nt), in = id - band * 8 * nt, high = mt - band * 8 < 8 ? mt - band * 8 : 8;
+  m = band * 8 + in % high;
+  n = in / high;
+}
+__device__ __forceinline__ int ce_tile_index(int m, int n, int mt, int nt) {
+  const int band = m / 8, high = mt - band * 8 < 8 ? mt - band * 8 : 8;
+  return band * 8 * nt + n * high + m - band * 8;
+}
+
 // Where a lane's 16 bytes of load `inst` lie in its tile: row and element in the row.
 template <int W>
 __device__ __forceinline__ void outer_place(int inst, int lane, int& k, int& col) {
@@ -66,28 +77,36 @@ __global__ __launch_bounds__(WM* WN * 64) void ce_tile_kernel(CeArgs a, CePiece 
   const int64_t M = C::kLogits ? pc.len : a.D;
   const int64_t N = MODE == kCeDweight ? pc.len : count;
 
-  // The tile of this workgroup.  Workgroups go round the eight dies in turn; a
+  // The tiles of this workgroup.  Workgroups go round the eight dies in turn; a
   // die gets neighbouring tiles, eight along m by some along n, which share
-  // their operands in its L2.
-  int64_t m0, n0;
-  int split;
-  {
-    const int mt = (int)((M + BM - 1) / BM), nt = (int)((N + BN - 1) / BN);
-    const int per = mt * nt, all = per * (MODE == kCeDhidden ? a.splits : 1);
+  // their operands in its L2.  DHIDDEN has few tiles of a long k: there
+  // a.workers workgroups share them out evenly, worker w the tiles from
+  // w T / workers on, the first and last of them in part.
+  const int mt = (int)((M + BM - 1) / BM), nt = (int)((N + BN - 1) / BN), all = mt * nt;
+  int job, job_end, worker = 0;
+  if (MODE == kCeDhidden) {
+    worker = ((int)blockIdx.x & 7) * (a.workers / 8) + ((int)blockIdx.x >> 3);
+    job = (int)((int64_t)worker * all / a.workers);
+    job_end = (int)(((int64_t)(worker + 1) * all + a.workers - 1) / a.workers);
+  } else {
     const int chunk = (all + 7) / 8;
-    const int at = ((int)blockIdx.x & 7) * chunk + ((int)blockIdx.x >> 3);
-    if (((int)blockIdx.x >> 3) >= chunk || at >= all) return;
-    split = at / per;
-    const int id = at - split * per, band = id / (8 * nt), in = id - band * 8 * nt;
-    const int high = mt - band * 8 < 8 ? mt - band * 8 : 8;
-    m0 = (int64_t)(band * 8 + in % high) * BM;
-    n0 = (int64_t)(in / high) * BN;
+    job = ((int)blockIdx.x & 7) * chunk + ((int)blockIdx.x >> 3);
+    if (((int)blockIdx.x >> 3) >= chunk || job >= all) return;
+    job_end = job + 1;
   }
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(ARCS_LDS char*)lds;
+  for (; job < job_end; ++job) {
+  int64_t m0, n0;
+  ce_tile_place(job, mt, nt, m0, n0);
+  m0 *= BM;
+  n0 *= BN;
   int64_t k_lo = 0, k_hi = C::kLogits ? a.D : MODE == kCeDhidden ? pc.len : count;
   if (MODE == kCeDhidden) {
-    const int64_t part = ((k_hi + a.splits - 1) / a.splits + kTK - 1) / kTK * kTK;
-    k_lo = part * split;
-    k_hi = k_lo + part < k_hi ? k_lo + part : k_hi;
+    // where worker w begins, in tiles' k: a fraction of the workers, the same in every piece
+    const int64_t tiles_k = (pc.len + kTK - 1) / kTK;
+    const int64_t from = (int64_t)worker * all - (int64_t)job * a.workers, to = from + all;
+    if (from > 0) k_lo = from * tiles_k / a.workers * kTK;
+    if (to < a.workers) k_hi = to * tiles_k / a.workers * kTK;
   }
   const int nk = k_hi > k_lo ? (int)((k_hi - k_lo + kTK - 1) / kTK) : 0;
 
@@ -147,21 +166,36 @@ __global__ __launch_bounds__(WM* WN * 64) void ce_tile_kernel(CeArgs a, CePiece 
     nb = (count * a.ds_ld - n0) * 2;
     step_b = kTK * a.ds_ld * 2;
   }
-  const uint32_t lds0 = (uint32_t)(uintptr_t)(ARCS_LDS char*)lds;
 
-  auto issue = [&](int kt) {
-    const uint32_t to = lds0 + (uint32_t)(kt % S) * C::kStage;
-    const u32x4 da = uniform4(buffer_of(pa + kt * step_a, C::kAOuter ? na - kt * step_a : (int64_t)kBufMost));
-    const u32x4 db = uniform4(buffer_of(pb + kt * step_b, C::kBOuter ? nb - kt * step_b : (int64_t)kBufMost));
+  // Load t of tile kt, of the kPer a wave has; tiles past the last read nothing
+  // (zeros go to a buffer that is free), so that the waits always count the same.
+  struct Source {
+    u32x4 a, b;
+    uint32_t to, left;
+  };
+  auto source = [&](int kt) {
+    Source s;
+    const int64_t k = (int64_t)kt * kTK;
+    s.a = uniform4(buffer_of(pa + kt * step_a, kt >= nk ? 0 : C::kAOuter ? na - kt * step_a : (int64_t)kBufMost));
+    s.b = uniform4(buffer_of(pb + kt * step_b, kt >= nk ? 0 : C::kBOuter ? nb - kt * step_b : (int64_t)kBufMost));
+    s.to = lds0 + (uint32_t)(kt % S) * C::kStage;
     // logits: the columns of the last tile past D are zeros
-    const uint32_t left = C::kLogits ? (uint32_t)(a.D - (int64_t)kt * kTK < kTK ? a.D - (int64_t)kt * kTK : kTK) : kTK;
-#pragma unroll
-    for (int t = 0; t < C::kAPer; ++t)
-      load_to_lds(to + ((wave + t * C::kWaves) % C::kALoads) * 1024u, C::kLogits && ka[t] >= left ? kNoLoad : oa[t], da);
-#pragma unroll
-    for (int t = 0; t < C::kBPer; ++t)
-      load_to_lds(to + C::kABytes + ((wave + t * C::kWaves) % C::kBLoads) * 1024u,
-                  C::kLogits && kb[t] >= left ? kNoLoad : ob[t], db);
+    s.left = (uint32_t)(a.D - k < kTK ? a.D - k : kTK);
+    return s;
+  };
+  auto issue_one = [&](const Source& s, int t) {
+    if (t < C::kAPer) {
+      const uint32_t off = C::kLogits && ka[t] >= s.left ? kNoLoad : oa[t];
+      const uint32_t to = s.to + ((wave + t * C::kWaves) % C::kALoads) * 1024u;
+      if (t == 0) load_to_lds<true>(to, off, s.a);
+      else load_to_lds<false>(to, off, s.a);
+    } else {
+      t -= C::kAPer;
+      const uint32_t off = C::kLogits && kb[t] >= s.left ? kNoLoad : ob[t];
+      const uint32_t to = s.to + C::kABytes + ((wave + t * C::kWaves) % C::kBLoads) * 1024u;
+      if (t == 0) load_to_lds<true>(to, off, s.b);
+      else load_to_lds<false>(to, off, s.b);
+    }
   };
 
   f32x16 acc[MT][NT];
@@ -219,36 +253,40 @@ __global__ __launch_bounds__(WM* WN * 64) void ce_tile_kernel(CeArgs a, CePiece 
   };
   if (nk > 0) {
 #pragma unroll
-    for (int s = 0; s < S; ++s)
-      if (s < nk) issue(s);
-    if (nk >= S) wait_loads<(S - 1) * C::kPer>();
-    else wait_loads<0>();
+    for (int t = 0; t < S; ++t) {
+      const Source from = source(t);
+#pragma unroll
+      for (int l = 0; l < C::kPer; ++l) issue_one(from, l);
+    }
+    wait_loads<(S - 1) * C::kPer>();
     __builtin_amdgcn_s_barrier();
     read(0, 0);
   }
-  for (int kt = 0; kt < nk - 1; ++kt) {
+  for (int kt = 0; kt < nk; ++kt) {
 #pragma unroll
     for (int ks = 0; ks < 3; ++ks) {
       read(kt, ks + 1);
       multiply(ks);
     }
-    // tile kt + 1 has landed: at most the S - 2 tiles after it are on their way
-    if (kt + S - 1 < nk) wait_loads<(S - 2) * C::kPer>();
-    else wait_loads<0>();
-    wait_lds();  // this wave's reads of tile kt are done
+    const Source from = source(kt + S);
+    wait_loads<(S - 2) * C::kPer>();  // tile kt + 1 has landed
+    wait_lds();                       // this wave's reads of tile kt are done
     __builtin_amdgcn_s_barrier();
-    if (kt + S < nk) issue(kt + S);
     read(kt + 1, 0);
-    multiply(3);
-  }
-  if (nk > 0) {
+    // the loads go between the products, which run on while one is issued
+    constexpr int kProducts = MT * NT, kEach = (C::kPer + kProducts - 1) / kProducts;
 #pragma unroll
-    for (int ks = 0; ks < 3; ++ks) {
-      read(nk - 1, ks + 1);
-      multiply(ks);
+    for (int p = 0; p < kProducts; ++p) {
+      acc[p / NT][p % NT] =
+          __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[1][p / NT], fb[1][p % NT], acc[p / NT][p % NT], 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int l = p * kEach; l < (p + 1) * kEach && l < C::kPer; ++l) issue_one(from, l);
+      __builtin_amdgcn_sched_barrier(0);
     }
-    multiply(3);
   }
+
+  wait_loads<0>();  // no load into LDS outlives its tile
 
   // A lane holds column n = lane % 32 of each 32 x 32 product and rows
   // 8 (r / 4) + 4 (lane / 32) + r % 4: in the lane's wave, row_of + mw of the tile.
@@ -288,29 +326,31 @@ __global__ __launch_bounds__(WM* WN * 64) void ce_tile_kernel(CeArgs a, CePiece 
       // a slice is a wave's rows of the tile
       if (fh == 0 && n < N) a.partial[n * a.slices + m0 / BM * WM + wave % WM] = make_float2(m, sum);
     }
-    return;
+    continue;
   }
   if (MODE == kCeDhidden) {
+    // part worker + job of the slab, [BN][BM]: each pair of them is met once
+    float* part = a.slab + (int64_t)(worker + job) * (BM * BN);
 #pragma unroll
     for (int j = 0; j < NT; ++j) {
-      const int64_t n = n0 + wn + j * 32 + fr;
-      if (n >= N) continue;
+      const int nl = wn + j * 32 + fr;
+      if (n0 + nl >= N) continue;
 #pragma unroll
       for (int i = 0; i < MT; ++i)
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
           if (row_of(i, q * 4) >= m_left) continue;
-          f32x4* out = (f32x4*)(a.slab + ((int64_t)split * a.N + n) * a.D + m0 + mw + row_of(i, q * 4));
+          f32x4* out = (f32x4*)(part + nl * BM + mw + row_of(i, q * 4));
           f32x4 v = {acc[i][j][q * 4], acc[i][j][q * 4 + 1], acc[i][j][q * 4 + 2], acc[i][j][q * 4 + 3]};
           if (!pc.first) v += *out;
           *out = v;
         }
     }
-    return;
+    __builtin_amdgcn_s_barrier();  // LDS is free for the next tile
+    continue;
   }
   // bfloat16 results: through LDS as [n][BM], so that a row is stored whole.
   // 16-byte chunk c of row n at c ^ (n % 32).
-  wait_loads<0>();
   wait_lds();
   __builtin_amdgcn_s_barrier();
   const float g = MODE == kCeDweight ? a.head->gmax : 0.0f;
@@ -357,6 +397,30 @@ __global__ __launch_bounds__(WM* WN * 64) void ce_tile_kernel(CeArgs a, CePiece 
     if (MODE == kCeDs) *(u32x4*)((uint16_t*)a.ds + n * a.ds_ld + m) = v;
     else if (m < M) *(u32x4*)((uint16_t*)a.out_dweight + (pc.v0 + n) * a.D + m) = v;
   }
+  }
+}
+
+// dhidden rows: the parts of each tile added up in the workers' order; zeros for
+// rows that are not listed.
+__global__ __launch_bounds__(256) void ce_dhidden_parts_kernel(CeArgs a, int BN) {
+  constexpr int BM = 256;
+  const int64_t n = blockIdx.x;
+  const int i = a.place[n];
+  __bf16* out = (__bf16*)a.out_dhidden + n * a.D;
+  const int mt = (int)((a.D + BM - 1) / BM), nt = (a.head->count + BN - 1) / BN, all = mt * nt;
+  const float g = a.head->gmax;
+  for (int m = 0; m < mt; ++m) {
+    const int d = m * BM + (int)threadIdx.x;
+    if (d >= a.D) continue;
+    float v = 0.0f;
+    if (i >= 0) {
+      const int job = ce_tile_index(m, i / BN, mt, nt);
+      const int lo = (int)((int64_t)job * a.workers / all), hi = (int)(((int64_t)(job + 1) * a.workers + all - 1) / all);
+      for (int w = lo; w < hi; ++w) v += a.slab[((int64_t)(w + job) * BN + i % BN) * BM + (int)threadIdx.x];
+      v *= g;
+    }
+    out[d] = (__bf16)v;
+  }
 }
 
 // The hidden states of the listed rows, one after the other.
@@ -376,7 +440,7 @@ template <int MODE, int WM, int WN, int MT, int NT, int S>
 void launch_tile(const CeArgs& a, const CePiece& pc, hipStream_t stream) {
   using C = CeTile<MODE, WM, WN, MT, NT, S>;
   const int64_t m = C::kLogits ? pc.len : a.D, n = MODE == kCeDweight ? pc.len : a.N;
-  const int64_t all = tiles(m, C::BM) * tiles(n, C::BN) * (MODE == kCeDhidden ? a.splits : 1);
+  const int64_t all = MODE == kCeDhidden ? a.workers : tiles(m, C::BM) * tiles(n, C::BN);
   hipLaunchKernelGGL((ce_tile_kernel<MODE, WM, WN, MT, NT, S>), dim3((unsigned)(8 * tiles(all, 8))), dim3(C::kThreads), 0,
                      stream, a, pc);
 }
@@ -384,9 +448,10 @@ void launch_tile(const CeArgs& a, const CePiece& pc, hipStream_t stream) {
 template <int MODE>
 void launch_rows(const CeArgs& a, const CePiece& pc, hipStream_t stream) {
   if constexpr (MODE != kCeDweight) {
-    if (a.N <= 32) return launch_tile<MODE, 8, 1, 1, 1, 4>(a, pc, stream);
-    if (a.N <= 64) return launch_tile<MODE, 4, 2, 2, 1, 3>(a, pc, stream);
-    if (a.N <= 128) return launch_tile<MODE, 4, 2, 2, 2, 3>(a, pc, stream);
+    const int rows = ce_rows_of_tile(a.N);
+    if (rows == 32) return launch_tile<MODE, 8, 1, 1, 1, 4>(a, pc, stream);
+    if (rows == 64) return launch_tile<MODE, 4, 2, 2, 1, 3>(a, pc, stream);
+    if (rows == 128) return launch_tile<MODE, 4, 2, 2, 2, 3>(a, pc, stream);
   }
   launch_tile<MODE, 2, 4, 4, 2, 2>(a, pc, stream);
 }
@@ -408,7 +473,8 @@ hipError_t launch_cross_entropy_matrix(const CeArgs& args, bool backward, hipStr
   pc.gather = !backward && (unsigned __int128)a.N * (unsigned __int128)a.hidden_stride * 2 < kBufMost;
   if (!pc.gather) hipLaunchKernelGGL(ce_copy_kernel, dim3((unsigned)a.N), dim3(256), 0, stream, a);
   if (!backward) {
-    a.slices = tiles(a.V, 256) * (a.N <= 32 ? 8 : a.N <= 128 ? 4 : 2);
+    const int rows = ce_rows_of_tile(a.N);
+    a.slices = tiles(a.V, 256) * (rows == 32 ? 8 : rows == 256 ? 2 : 4);
     launch_rows<kCeStats>(a, pc, stream);
     launch_cross_entropy_combine(a, stream);
     return hipGetLastError();
@@ -421,7 +487,8 @@ hipError_t launch_cross_entropy_matrix(const CeArgs& args, bool backward, hipStr
     if (a.out_dhidden) launch_rows<kCeDhidden>(a, pc, stream);
     if (a.out_dweight) launch_rows<kCeDweight>(a, pc, stream);
   }
-  if (a.out_dhidden) launch_cross_entropy_dhidden(a, true, stream);
+  if (a.out_dhidden)
+    hipLaunchKernelGGL(ce_dhidden_parts_kernel, dim3((unsigned)a.N), dim3(256), 0, stream, a, ce_rows_of_tile(a.N));
   return hipGetLastError();
 }
 

@@ -30,11 +30,16 @@ __device__ __forceinline__ u32x4 buffer_of(const void* p, int64_t bytes) {
 }
 
 // 16 bytes a lane from descriptor + offset to LDS at `to` + 16 * lane.  The
-// wait is the caller's (vmcnt).  The wait states cover a descriptor or m0
-// written just before.
+// wait is the caller's (vmcnt).  m0 takes one wait state, a descriptor that a
+// vector instruction has just written five: the first load of a descriptor has them.
+template <bool FIRST = true>
 __device__ __forceinline__ void load_to_lds(uint32_t to, uint32_t off, u32x4 from) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(to), "v"(off), "s"(from)
-               : "memory", "m0");
+  if (FIRST)
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(to), "v"(off), "s"(from)
+                 : "memory", "m0");
+  else
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(to), "v"(off), "s"(from)
+                 : "memory", "m0");
 }
 
 template <int N>
