@@ -37,8 +37,10 @@ struct CeTile {
   static constexpr int kALoads = BM / 8, kBLoads = BN / 8;  // of 1024 bytes each
   static constexpr int kAPer = (kALoads + kWaves - 1) / kWaves, kBPer = (kBLoads + kWaves - 1) / kWaves;
   static constexpr int kPer = kAPer + kBPer;
-  static constexpr int kOut = MODE == kCeDs || MODE == kCeDweight ? BM * BN * 2 : 0;
-  static constexpr int kLds = S * kStage > kOut ? S * kStage : kOut;
+  // bfloat16 results go out through 32 rows of kOutM columns a wave
+  static constexpr bool kOut = MODE == kCeDs || MODE == kCeDweight;
+  static constexpr int kOutM = MT % 2 == 0 && S * kStage + kWaves * 32 * 64 * 2 <= 163840 ? 64 : 32;
+  static constexpr int kOutBytes = 32 * kOutM * 2, kLds = S * kStage + (kOut ? kWaves * kOutBytes : 0);
 };
 
 // Tile `id` of mt x nt: bands of eight along m, in a band m first.
@@ -76,6 +78,7 @@ __global__ __launch_bounds__(WM* WN * 64) void ce_tile_kernel(CeArgs a, CePiece 
   const int64_t count = a.head->count;
   const int64_t M = C::kLogits ? pc.len : a.D;
   const int64_t N = MODE == kCeDweight ? pc.len : count;
+  const uint32_t lds0 = (uint32_t)(uintptr_t)(ARCS_LDS char*)lds;
 
   // The tiles of this workgroup.  Workgroups go round the eight dies in turn; a
   // die gets neighbouring tiles, eight along m by some along n, which share
@@ -83,88 +86,95 @@ __global__ __launch_bounds__(WM* WN * 64) void ce_tile_kernel(CeArgs a, CePiece 
   // a.workers workgroups share them out evenly, worker w the tiles from
   // w T / workers on, the first and last of them in part.
   const int mt = (int)((M + BM - 1) / BM), nt = (int)((N + BN - 1) / BN), all = mt * nt;
-  int job, job_end, worker = 0;
+  int job, job_end, job_step = 1, worker = 0;
   if (MODE == kCeDhidden) {
     worker = ((int)blockIdx.x & 7) * (a.workers / 8) + ((int)blockIdx.x >> 3);
     job = (int)((int64_t)worker * all / a.workers);
     job_end = (int)(((int64_t)(worker + 1) * all + a.workers - 1) / a.workers);
   } else {
-    const int chunk = (all + 7) / 8;
-    job = ((int)blockIdx.x & 7) * chunk + ((int)blockIdx.x >> 3);
-    if (((int)blockIdx.x >> 3) >= chunk || job >= all) return;
-    job_end = job + 1;
+    const int chunk = (all + 7) / 8, first = ((int)blockIdx.x & 7) * chunk;
+    job = first + ((int)blockIdx.x >> 3);
+    job_end = first + chunk < all ? first + chunk : all;
+    job_step = (int)gridDim.x / 8;
   }
-  const uint32_t lds0 = (uint32_t)(uintptr_t)(ARCS_LDS char*)lds;
-  for (; job < job_end; ++job) {
-  int64_t m0, n0;
-  ce_tile_place(job, mt, nt, m0, n0);
-  m0 *= BM;
-  n0 *= BN;
-  int64_t k_lo = 0, k_hi = C::kLogits ? a.D : MODE == kCeDhidden ? pc.len : count;
-  if (MODE == kCeDhidden) {
-    // where worker w begins, in tiles' k: a fraction of the workers, the same in every piece
-    const int64_t tiles_k = (pc.len + kTK - 1) / kTK;
-    const int64_t from = (int64_t)worker * all - (int64_t)job * a.workers, to = from + all;
-    if (from > 0) k_lo = from * tiles_k / a.workers * kTK;
-    if (to < a.workers) k_hi = to * tiles_k / a.workers * kTK;
-  }
-  const int nk = k_hi > k_lo ? (int)((k_hi - k_lo + kTK - 1) / kTK) : 0;
+  if (job >= job_end) return;
 
-  // descriptors at k_lo, and the lanes' offsets in a tile
+  // The tile that is loaded: descriptors at its first k, and the lanes' offsets.
+  int64_t m0, n0;
+  int nk;
+  const char *pa, *pb;
+  int64_t na, nb;
+  uint32_t oa[C::kAPer], ob[C::kBPer];
   const uint16_t* W = (const uint16_t*)a.weight + pc.v0 * a.weight_stride;
   const uint16_t* H = (const uint16_t*)(pc.gather ? a.hidden : a.hc);
   const uint16_t* Z = (const uint16_t*)a.ds;
-  const char *pa, *pb;
-  int64_t na = kBufMost, nb = kBufMost, step_a = kTK * 2, step_b = kTK * 2;
-  uint32_t oa[C::kAPer], ob[C::kBPer];
-  uint32_t ka[C::kAPer], kb[C::kBPer];  // along k: the lane's first element's k in a tile
-#pragma unroll
-  for (int t = 0; t < C::kAPer; ++t) {
-    const int inst = (wave + t * C::kWaves) % C::kALoads;
-    int r, c;
-    if (!C::kAOuter) {
-      inner_place(inst, lane, r, c);
-      const int64_t left = M - 1 - m0;
-      oa[t] = (uint32_t)((r < left ? r : left) * a.weight_stride * 2 + c * 2);
-      ka[t] = (uint32_t)c;
-    } else {
-      outer_place<BM>(inst, lane, r, c);
-      const int64_t ld = MODE == kCeDhidden ? a.weight_stride : a.D;
-      oa[t] = m0 + c < M ? (uint32_t)(r * ld * 2 + c * 2) : kNoLoad;
-      ka[t] = 0;
+  const int64_t step_a = C::kLogits ? kTK * 2 : MODE == kCeDhidden ? kTK * a.weight_stride * 2 : kTK * a.D * 2;
+  const int64_t step_b = MODE == kCeDweight ? kTK * a.ds_ld * 2 : kTK * 2;
+  auto place = [&](int job) {
+    ce_tile_place(job, mt, nt, m0, n0);
+    m0 *= BM;
+    n0 *= BN;
+    int64_t k_lo = 0, k_hi = C::kLogits ? a.D : MODE == kCeDhidden ? pc.len : count;
+    if (MODE == kCeDhidden) {
+      // where worker w begins, in tiles' k: a fraction of the workers, the same in every piece
+      const int64_t tiles_k = (pc.len + kTK - 1) / kTK;
+      const int64_t from = (int64_t)worker * all - (int64_t)job * a.workers, to = from + all;
+      if (from > 0) k_lo = from * tiles_k / a.workers * kTK;
+      if (to < a.workers) k_hi = to * tiles_k / a.workers * kTK;
     }
-  }
+    nk = k_hi > k_lo ? (int)((k_hi - k_lo + kTK - 1) / kTK) : 0;
+    na = nb = kBufMost;
 #pragma unroll
-  for (int t = 0; t < C::kBPer; ++t) {
-    const int inst = (wave + t * C::kWaves) % C::kBLoads;
-    int r, c;
-    if (!C::kBOuter) {
-      inner_place(inst, lane, r, c);
-      const int64_t left = N - 1 - n0, n = r < left ? r : left;
-      if (C::kLogits) ob[t] = (uint32_t)((pc.gather ? (int64_t)a.rows[n0 + n].row * a.hidden_stride : n * a.D) * 2 + c * 2);
-      else ob[t] = (uint32_t)(n * a.ds_ld * 2 + c * 2);
-      kb[t] = (uint32_t)c;
-    } else {
-      outer_place<BN>(inst, lane, r, c);
-      ob[t] = (uint32_t)(r * a.ds_ld * 2 + c * 2);
-      kb[t] = 0;
+    for (int t = 0; t < C::kAPer; ++t) {
+      const int inst = (wave + t * C::kWaves) % C::kALoads;
+      int r, c;
+      if (!C::kAOuter) {
+        inner_place(inst, lane, r, c);
+        const int64_t left = M - 1 - m0;
+        oa[t] = (uint32_t)((r < left ? r : left) * a.weight_stride * 2 + c * 2);
+      } else {
+        outer_place<BM>(inst, lane, r, c);
+        const int64_t ld = MODE == kCeDhidden ? a.weight_stride : a.D;
+        oa[t] = m0 + c < M ? (uint32_t)(r * ld * 2 + c * 2) : kNoLoad;
+      }
     }
-  }
-  if (C::kLogits) {
-    pa = (const char*)(W + m0 * a.weight_stride);
-    pb = (const char*)(pc.gather ? H : H + n0 * a.D);
-  } else if (MODE == kCeDhidden) {
-    pa = (const char*)(W + k_lo * a.weight_stride + m0);
-    na = ((pc.len - k_lo) * a.weight_stride - m0) * 2;
-    step_a = kTK * a.weight_stride * 2;
-    pb = (const char*)(Z + n0 * a.ds_ld + k_lo);
-  } else {
-    pa = (const char*)(H + m0);
-    na = (count * a.D - m0) * 2;
-    step_a = kTK * a.D * 2;
-    pb = (const char*)(Z + n0);
-    nb = (count * a.ds_ld - n0) * 2;
-    step_b = kTK * a.ds_ld * 2;
+#pragma unroll
+    for (int t = 0; t < C::kBPer; ++t) {
+      const int inst = (wave + t * C::kWaves) % C::kBLoads;
+      int r, c;
+      if (!C::kBOuter) {
+        inner_place(inst, lane, r, c);
+        const int64_t left = N - 1 - n0, n = r < left ? r : left;
+        if (C::kLogits) ob[t] = (uint32_t)((pc.gather ? (int64_t)a.rows[n0 + n].row * a.hidden_stride : n * a.D) * 2 + c * 2);
+        else ob[t] = (uint32_t)(n * a.ds_ld * 2 + c * 2);
+      } else {
+        outer_place<BN>(inst, lane, r, c);
+        ob[t] = (uint32_t)(r * a.ds_ld * 2 + c * 2);
+      }
+    }
+    if (C::kLogits) {
+      pa = (const char*)(W + m0 * a.weight_stride);
+      pb = (const char*)(pc.gather ? H : H + n0 * a.D);
+    } else if (MODE == kCeDhidden) {
+      pa = (const char*)(W + k_lo * a.weight_stride + m0);
+      na = ((pc.len - k_lo) * a.weight_stride - m0) * 2;
+      pb = (const char*)(Z + n0 * a.ds_ld + k_lo);
+    } else {
+      pa = (const char*)(H + m0);
+      na = (count * a.D - m0) * 2;
+      pb = (const char*)(Z + n0);
+      nb = (count * a.ds_ld - n0) * 2;
+    }
+  };
+  // along k: the lane's first element's k in a tile, the same for each second load
+  uint32_t ka[2], kb[2];
+#pragma unroll
+  for (int t = 0; t < 2; ++t) {
+    int r, c;
+    inner_place((wave + t * C::kWaves) % C::kALoads, lane, r, c);
+    ka[t] = (uint32_t)c;
+    inner_place((wave + t * C::kWaves) % C::kBLoads, lane, r, c);
+    kb[t] = (uint32_t)c;
   }
 
   // Load t of tile kt, of the kPer a wave has; tiles past the last read nothing
@@ -185,26 +195,26 @@ __global__ __launch_bounds__(WM* WN * 64) void ce_tile_kernel(CeArgs a, CePiece 
   };
   auto issue_one = [&](const Source& s, int t) {
     if (t < C::kAPer) {
-      const uint32_t off = C::kLogits && ka[t] >= s.left ? kNoLoad : oa[t];
+      const uint32_t off = C::kLogits && ka[t & 1] >= s.left ? kNoLoad : oa[t];
       const uint32_t to = s.to + ((wave + t * C::kWaves) % C::kALoads) * 1024u;
       if (t == 0) load_to_lds<true>(to, off, s.a);
       else load_to_lds<false>(to, off, s.a);
     } else {
       t -= C::kAPer;
-      const uint32_t off = C::kLogits && kb[t] >= s.left ? kNoLoad : ob[t];
+      const uint32_t off = C::kLogits && kb[t & 1] >= s.left ? kNoLoad : ob[t];
       const uint32_t to = s.to + C::kABytes + ((wave + t * C::kWaves) % C::kBLoads) * 1024u;
       if (t == 0) load_to_lds<true>(to, off, s.b);
       else load_to_lds<false>(to, off, s.b);
     }
   };
-
-  f32x16 acc[MT][NT];
+  auto issue_first = [&]() {
 #pragma unroll
-  for (int i = 0; i < MT; ++i)
+    for (int t = 0; t < S; ++t) {
+      const Source from = source(t);
 #pragma unroll
-    for (int j = 0; j < NT; ++j)
-#pragma unroll
-      for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+      for (int l = 0; l < C::kPer; ++l) issue_one(from, l);
+    }
+  };
 
   const int wm = (wave % WM) * MT * 32, wn = (wave / WM) * NT * 32;
   const int fr = lane & 31, fh = lane >> 5;
@@ -233,6 +243,7 @@ __global__ __launch_bounds__(WM* WN * 64) void ce_tile_kernel(CeArgs a, CePiece 
   // Fragments of step ks + 1 are read while step ks multiplies.  The last step of
   // a tile reads from the next one: there the workgroup meets, once a tile, the
   // next tile has landed and this one's buffer is filled again.
+  f32x16 acc[MT][NT];
   bf16x8 fa[2][MT], fb[2][NT];
   auto read = [&](int kt, int ks) {
     const uint32_t at = (uint32_t)(kt % S) * C::kStage;
@@ -251,152 +262,177 @@ __global__ __launch_bounds__(WM* WN * 64) void ce_tile_kernel(CeArgs a, CePiece 
         acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[ks & 1][i], fb[ks & 1][j], acc[i][j], 0, 0, 0);
     __builtin_amdgcn_sched_barrier(0);
   };
-  if (nk > 0) {
-#pragma unroll
-    for (int t = 0; t < S; ++t) {
-      const Source from = source(t);
-#pragma unroll
-      for (int l = 0; l < C::kPer; ++l) issue_one(from, l);
-    }
-    wait_loads<(S - 1) * C::kPer>();
-    __builtin_amdgcn_s_barrier();
-    read(0, 0);
-  }
-  for (int kt = 0; kt < nk; ++kt) {
-#pragma unroll
-    for (int ks = 0; ks < 3; ++ks) {
-      read(kt, ks + 1);
-      multiply(ks);
-    }
-    const Source from = source(kt + S);
-    wait_loads<(S - 2) * C::kPer>();  // tile kt + 1 has landed
-    wait_lds();                       // this wave's reads of tile kt are done
-    __builtin_amdgcn_s_barrier();
-    read(kt + 1, 0);
-    // the loads go between the products, which run on while one is issued
-    constexpr int kProducts = MT * NT, kEach = (C::kPer + kProducts - 1) / kProducts;
-#pragma unroll
-    for (int p = 0; p < kProducts; ++p) {
-      acc[p / NT][p % NT] =
-          __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[1][p / NT], fb[1][p % NT], acc[p / NT][p % NT], 0, 0, 0);
-      __builtin_amdgcn_sched_barrier(0);
-#pragma unroll
-      for (int l = p * kEach; l < (p + 1) * kEach && l < C::kPer; ++l) issue_one(from, l);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-  }
 
-  wait_loads<0>();  // no load into LDS outlives its tile
-
-  // A lane holds column n = lane % 32 of each 32 x 32 product and rows
-  // 8 (r / 4) + 4 (lane / 32) + r % 4: in the lane's wave, row_of + mw of the tile.
-  auto row_of = [](int i, int r) { return i * 32 + 8 * (r >> 2) + (r & 3); };
-  const int mw = wm + 4 * fh;
-  const int m_left = (int)(M - m0 < BM ? M - m0 : BM) - mw;  // rows of the lane that exist
-  if (MODE == kCeStats) {
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      const int64_t n = n0 + wn + j * 32 + fr;
-      CeRow row;
-      row.target = -1;
-      row.a = 0.0f;
-      if (n < N) row = a.rows[n];
-      const int64_t to_target = (int64_t)row.target - m0 - mw;
-      const int target = to_target >= 0 && to_target < m_left ? (int)to_target : -1;
-      float m = -__builtin_inff(), yt = 0.0f;
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) {
-          const float y = acc[i][j][r] * row.a;
-          acc[i][j][r] = row_of(i, r) < m_left ? y : -__builtin_inff();
-          m = fmaxf(m, acc[i][j][r]);
-          yt = row_of(i, r) == target ? y : yt;
-        }
-      // target is one of the lane's 16 MT rows, not one between them
-      if (target >= 0 && (target & 4) == 0 && target < MT * 32) a.ytarget[n] = yt;
-      m = fmaxf(m, __shfl_xor(m, 32, kWave));
-      const float mz = finite_or_zero(m);
-      float sum = 0.0f;
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int r = 0; r < 16; ++r) sum += exp2_fast(acc[i][j][r] - mz);
-      sum += __shfl_xor(sum, 32, kWave);
-      // a slice is a wave's rows of the tile
-      if (fh == 0 && n < N) a.partial[n * a.slices + m0 / BM * WM + wave % WM] = make_float2(m, sum);
-    }
-    continue;
-  }
-  if (MODE == kCeDhidden) {
-    // part worker + job of the slab, [BN][BM]: each pair of them is met once
-    float* part = a.slab + (int64_t)(worker + job) * (BM * BN);
-#pragma unroll
-    for (int j = 0; j < NT; ++j) {
-      const int nl = wn + j * 32 + fr;
-      if (n0 + nl >= N) continue;
-#pragma unroll
-      for (int i = 0; i < MT; ++i)
-#pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          if (row_of(i, q * 4) >= m_left) continue;
-          f32x4* out = (f32x4*)(part + nl * BM + mw + row_of(i, q * 4));
-          f32x4 v = {acc[i][j][q * 4], acc[i][j][q * 4 + 1], acc[i][j][q * 4 + 2], acc[i][j][q * 4 + 3]};
-          if (!pc.first) v += *out;
-          *out = v;
-        }
-    }
-    __builtin_amdgcn_s_barrier();  // LDS is free for the next tile
-    continue;
-  }
-  // bfloat16 results: through LDS as [n][BM], so that a row is stored whole.
-  // 16-byte chunk c of row n at c ^ (n % 32).
-  wait_lds();
-  __builtin_amdgcn_s_barrier();
-  const float g = MODE == kCeDweight ? a.head->gmax : 0.0f;
-#pragma unroll
-  for (int j = 0; j < NT; ++j) {
-    const int nl = wn + j * 32 + fr;
-    const int64_t n = n0 + nl;
-    CeRow row;
-    row.target = -1;
-    row.a = row.c = row.lse2 = 0.0f;
-    if (MODE == kCeDs && n < N) row = a.rows[n];
-    const int64_t to_target = (int64_t)row.target - pc.v0 - m0 - mw;
-    const int target = to_target >= 0 && to_target < BM ? (int)to_target : -1;
+  place(job);
+  issue_first();
+  while (true) {
 #pragma unroll
     for (int i = 0; i < MT; ++i)
 #pragma unroll
-      for (int q = 0; q < 4; ++q) {
-        bf16x4 out;
+      for (int j = 0; j < NT; ++j)
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float v = acc[i][j][q * 4 + e];
-          if (MODE == kCeDs) {
-            const int id = row_of(i, q * 4 + e);
-            v = exp2_fast(fmaf(v, row.a, -row.lse2));
-            v = id == target ? v - 1.0f : v;
-            v = id < m_left ? v * row.c : 0.0f;
-          } else {
-            v *= g;
-          }
-          out[e] = (__bf16)v;
-        }
-        const int ml = mw + row_of(i, q * 4);
-        *(bf16x4*)(lds + nl * (BM * 2) + (((ml >> 3) ^ (nl & 31)) * 16) + (ml & 4) * 2) = out;
+        for (int r = 0; r < 16; ++r) acc[i][j][r] = 0.0f;
+    wait_loads<(S - 1) * C::kPer>();
+    __builtin_amdgcn_s_barrier();
+    read(0, 0);
+    for (int kt = 0; kt < nk; ++kt) {
+#pragma unroll
+      for (int ks = 0; ks < 3; ++ks) {
+        read(kt, ks + 1);
+        multiply(ks);
       }
-  }
-  wait_lds();
-  __builtin_amdgcn_s_barrier();
-  constexpr int kChunks = BM / 8;
-  for (int t = tid; t < BN * kChunks; t += C::kThreads) {
-    const int nl = t / kChunks, c = t % kChunks;
-    const int64_t n = n0 + nl, m = m0 + c * 8;
-    if (n >= N) continue;
-    const u32x4 v = *(const u32x4*)(lds + nl * (BM * 2) + ((c ^ (nl & 31)) * 16));
-    if (MODE == kCeDs) *(u32x4*)((uint16_t*)a.ds + n * a.ds_ld + m) = v;
-    else if (m < M) *(u32x4*)((uint16_t*)a.out_dweight + (pc.v0 + n) * a.D + m) = v;
-  }
+      const Source from = source(kt + S);
+      wait_loads<(S - 2) * C::kPer>();  // tile kt + 1 has landed
+      wait_lds();                       // this wave's reads of tile kt are done
+      __builtin_amdgcn_s_barrier();
+      read(kt + 1, 0);
+      // the loads go between the products, which run on while one is issued
+      constexpr int kProducts = MT * NT, kEach = (C::kPer + kProducts - 1) / kProducts;
+#pragma unroll
+      for (int p = 0; p < kProducts; ++p) {
+        acc[p / NT][p % NT] =
+            __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[1][p / NT], fb[1][p % NT], acc[p / NT][p % NT], 0, 0, 0);
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int l = p * kEach; l < (p + 1) * kEach && l < C::kPer; ++l) issue_one(from, l);
+        __builtin_amdgcn_sched_barrier(0);
+      }
+    }
+    wait_loads<0>();  // no load into LDS outlives its tile
+    wait_lds();
+    __builtin_amdgcn_s_barrier();
+
+    // The next tile's first loads fly while this one's results go out.
+    const int64_t em0 = m0, en0 = n0;
+    const int done = job;
+    job += job_step;
+    const bool more = job < job_end;
+    if (more) {
+      place(job);
+      issue_first();
+    }
+
+    // A lane holds column n = lane % 32 of each 32 x 32 product and rows
+    // 8 (r / 4) + 4 (lane / 32) + r % 4: in the lane's wave, row_of + mw of the tile.
+    auto row_of = [](int i, int r) { return i * 32 + 8 * (r >> 2) + (r & 3); };
+    const int mw = wm + 4 * fh;
+    const int m_left = (int)(M - em0 < BM ? M - em0 : BM) - mw;  // rows of the lane that exist
+    if (MODE == kCeStats) {
+      const bool ragged = M - em0 < BM;
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        const int64_t n = en0 + wn + j * 32 + fr;
+        CeRow row;
+        row.target = -1;
+        row.a = 1.0f;
+        if (n < N) row = a.rows[n];
+        if (ragged) {
+#pragma unroll
+          for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int r = 0; r < 16; ++r)
+              if (row_of(i, r) >= m_left) acc[i][j][r] = -__builtin_inff();
+        }
+        float m = acc[0][j][0];
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) m = fmaxf(m, acc[i][j][r]);
+        m = fmaxf(m, __shfl_xor(m, 32, kWave)) * row.a;  // y = dot * a, a > 0
+        const float mz = finite_or_zero(m);
+        float sum = 0.0f;
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int r = 0; r < 16; ++r) sum += exp2_fast(fmaf(acc[i][j][r], row.a, -mz));
+        sum += __shfl_xor(sum, 32, kWave);
+        // a slice is a wave's rows of the tile
+        if (fh == 0 && n < N) a.partial[n * a.slices + em0 / BM * WM + wave % WM] = make_float2(m, sum);
+        // few tiles hold a row's target
+        const int64_t to_target = (int64_t)row.target - em0 - mw;
+        const bool mine = to_target >= 0 && to_target < MT * 32 && (to_target & 4) == 0;
+        if (__any(mine)) {
+          float t = 0.0f;
+#pragma unroll
+          for (int i = 0; i < MT; ++i)
+#pragma unroll
+            for (int r = 0; r < 16; ++r) t = row_of(i, r) == (int)to_target ? acc[i][j][r] : t;
+          if (mine) a.ytarget[n] = t * row.a;
+        }
+      }
+    }
+    if (MODE == kCeDhidden) {
+      // part worker + job of the slab, [BN][BM]: each pair of them is met once
+      float* part = a.slab + (int64_t)(worker + done) * (BM * BN);
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        const int nl = wn + j * 32 + fr;
+        if (en0 + nl >= N) continue;
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            if (row_of(i, q * 4) >= m_left) continue;
+            f32x4* out = (f32x4*)(part + nl * BM + mw + row_of(i, q * 4));
+            f32x4 v = {acc[i][j][q * 4], acc[i][j][q * 4 + 1], acc[i][j][q * 4 + 2], acc[i][j][q * 4 + 3]};
+            if (!pc.first) v += *out;
+            *out = v;
+          }
+      }
+    }
+    if (C::kOut) {
+      // bfloat16 results: 32 rows n of kOutM columns at a time through the wave's own
+      // part of LDS, so that whole lines are stored.  16-byte chunk c of row n at c ^ n.
+      constexpr int kOutM = C::kOutM, kChunks = kOutM / 8, kTiles = kOutM / 32;
+      char* own = lds + S * C::kStage + wave * C::kOutBytes;
+      const float g = MODE == kCeDweight ? a.head->gmax : 0.0f;
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        CeRow row;
+        row.target = -1;
+        row.a = row.c = row.lse2 = 0.0f;
+        if (MODE == kCeDs && en0 + wn + j * 32 + fr < N) row = a.rows[en0 + wn + j * 32 + fr];
+        const int64_t to_target = (int64_t)row.target - pc.v0 - em0 - mw;
+        const int target = to_target >= 0 && to_target < MT * 32 ? (int)to_target : -1;
+#pragma unroll
+        for (int i0 = 0; i0 < MT; i0 += kTiles) {
+#pragma unroll
+          for (int i = i0; i < i0 + kTiles; ++i)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+              bf16x4 out;
+#pragma unroll
+              for (int e = 0; e < 4; ++e) {
+                float v = acc[i][j][q * 4 + e];
+                if (MODE == kCeDs) {
+                  const int id = row_of(i, q * 4 + e);
+                  v = exp2_fast(fmaf(v, row.a, -row.lse2));
+                  v = id == target ? v - 1.0f : v;
+                  v = id < m_left ? v * row.c : 0.0f;
+                } else {
+                  v *= g;
+                }
+                out[e] = (__bf16)v;
+              }
+              const int ml = row_of(i - i0, q * 4) + 4 * fh;
+              *(bf16x4*)(own + fr * (kOutM * 2) + (((ml >> 3) ^ (fr & (kChunks - 1))) * 16) + (ml & 4) * 2) = out;
+            }
+          wait_lds();
+          const int64_t ms = em0 + wm + i0 * 32;
+#pragma unroll
+          for (int t = 0; t < 32 * kChunks / 64; ++t) {
+            const int nl = (t * 64 + lane) / kChunks, c = (t * 64 + lane) % kChunks;
+            const int64_t n = en0 + wn + j * 32 + nl, m = ms + c * 8;
+            const u32x4 v = *(const u32x4*)(own + nl * (kOutM * 2) + ((c ^ (nl & (kChunks - 1))) * 16));
+            if (n >= N) continue;
+            if (MODE == kCeDs) *(u32x4*)((uint16_t*)a.ds + n * a.ds_ld + m) = v;
+            else if (m < M) *(u32x4*)((uint16_t*)a.out_dweight + (pc.v0 + n) * a.D + m) = v;
+          }
+          wait_lds();  // read before the next columns are written
+        }
+      }
+    }
+    if (!more) break;
   }
 }
 
@@ -405,22 +441,24 @@ __global__ __launch_bounds__(WM* WN * 64) void ce_tile_kernel(CeArgs a, CePiece 
 __global__ __launch_bounds__(256) void ce_dhidden_parts_kernel(CeArgs a, int BN) {
   constexpr int BM = 256;
   const int64_t n = blockIdx.x;
+  const int m = blockIdx.y * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;  // a wave takes one tile's columns
+  const int64_t d = m * BM + lane * 4;
+  if (d >= a.D) return;
   const int i = a.place[n];
-  __bf16* out = (__bf16*)a.out_dhidden + n * a.D;
   const int mt = (int)((a.D + BM - 1) / BM), nt = (a.head->count + BN - 1) / BN, all = mt * nt;
-  const float g = a.head->gmax;
-  for (int m = 0; m < mt; ++m) {
-    const int d = m * BM + (int)threadIdx.x;
-    if (d >= a.D) continue;
-    float v = 0.0f;
-    if (i >= 0) {
-      const int job = ce_tile_index(m, i / BN, mt, nt);
-      const int lo = (int)((int64_t)job * a.workers / all), hi = (int)(((int64_t)(job + 1) * a.workers + all - 1) / all);
-      for (int w = lo; w < hi; ++w) v += a.slab[((int64_t)(w + job) * BN + i % BN) * BM + (int)threadIdx.x];
-      v *= g;
-    }
-    out[d] = (__bf16)v;
+  f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
+  if (i >= 0) {
+    const int job = ce_tile_index(m, i / BN, mt, nt);
+    const int lo = (int)((int64_t)job * a.workers / all), hi = (int)(((int64_t)(job + 1) * a.workers + all - 1) / all);
+    const float* p = a.slab + ((int64_t)job * BN + i % BN) * BM + lane * 4;
+#pragma unroll 4
+    for (int w = lo; w < hi; ++w) v += *(const f32x4*)(p + (int64_t)w * (BN * BM));
+    v *= a.head->gmax;
   }
+  bf16x4 out;
+#pragma unroll
+  for (int e = 0; e < 4; ++e) out[e] = (__bf16)v[e];
+  *(bf16x4*)((__bf16*)a.out_dhidden + n * a.D + d) = out;
 }
 
 // The hidden states of the listed rows, one after the other.
@@ -440,9 +478,10 @@ template <int MODE, int WM, int WN, int MT, int NT, int S>
 void launch_tile(const CeArgs& a, const CePiece& pc, hipStream_t stream) {
   using C = CeTile<MODE, WM, WN, MT, NT, S>;
   const int64_t m = C::kLogits ? pc.len : a.D, n = MODE == kCeDweight ? pc.len : a.N;
-  const int64_t all = MODE == kCeDhidden ? a.workers : tiles(m, C::BM) * tiles(n, C::BN);
-  hipLaunchKernelGGL((ce_tile_kernel<MODE, WM, WN, MT, NT, S>), dim3((unsigned)(8 * tiles(all, 8))), dim3(C::kThreads), 0,
-                     stream, a, pc);
+  // one workgroup for each compute unit (LDS holds no second), at most
+  const int64_t all = tiles(m, C::BM) * tiles(n, C::BN);
+  const int64_t blocks = MODE == kCeDhidden ? a.workers : all < 256 ? tiles(all, 8) * 8 : 256;
+  hipLaunchKernelGGL((ce_tile_kernel<MODE, WM, WN, MT, NT, S>), dim3((unsigned)blocks), dim3(C::kThreads), 0, stream, a, pc);
 }
 
 template <int MODE>
@@ -462,7 +501,7 @@ bool cross_entropy_matrix_path(const CeArgs& a, int dtype, bool backward) {
   if (dtype != ARCS_DTYPE_BF16 || a.D % 8 != 0) return false;
   const int64_t most = int64_t(1) << 22;  // a tile's rows lie within 2^31 bytes
   if (a.hidden_stride % 8 != 0 || a.weight_stride % 8 != 0 || a.weight_stride >= most) return false;
-  if (((uintptr_t)a.hidden | (uintptr_t)a.weight | (uintptr_t)a.out_dweight) & 15u) return false;
+  if (((uintptr_t)a.hidden | (uintptr_t)a.weight | (uintptr_t)a.out_dweight | (uintptr_t)a.out_dhidden) & 15u) return false;
   return true;
 }
 
@@ -488,7 +527,8 @@ hipError_t launch_cross_entropy_matrix(const CeArgs& args, bool backward, hipStr
     if (a.out_dweight) launch_rows<kCeDweight>(a, pc, stream);
   }
   if (a.out_dhidden)
-    hipLaunchKernelGGL(ce_dhidden_parts_kernel, dim3((unsigned)a.N), dim3(256), 0, stream, a, ce_rows_of_tile(a.N));
+    hipLaunchKernelGGL(ce_dhidden_parts_kernel, dim3((unsigned)a.N, (unsigned)tiles(a.D, 1024)), dim3(256), 0, stream, a,
+                       ce_rows_of_tile(a.N));
   return hipGetLastError();
 }
 
