@@ -503,6 +503,9 @@ def sample_debug(logits, params, hist_ids=None, hist_offsets=None, seed: int = 0
 # --------------------------------------------------------------------------
 # the vocabulary head: 4-bit logits and the linear cross entropy
 # --------------------------------------------------------------------------
+_NO_CONTEXT = contextlib.nullcontext()
+
+
 def _work_on(device, stream):
     """The device and stream a head call runs on: the given stream, which has to
     be one of the tensors' device, or that device's current stream.  What the
@@ -514,7 +517,7 @@ def _work_on(device, stream):
         return torch.cuda.stream(stream)
     if torch.cuda.current_device() != device.index:
         return torch.cuda.device(device)
-    return contextlib.nullcontext()
+    return _NO_CONTEXT
 
 
 def _matrix(t, name: str, dtype, rows: int, cols: int, device):

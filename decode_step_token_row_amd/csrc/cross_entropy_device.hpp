@@ -29,10 +29,22 @@ struct CePiece {
   int64_t v0, len;  // the piece of the vocabulary
   int first;        // DHIDDEN: the slab holds nothing yet
   int gather;       // matrix kernels: hidden states are read through the row list
+  int direct;       // STATS of few rows: no row list, every row is computed
 };
 
+// 0: the row counts, -1: it is masked, otherwise its status code.
+__device__ __forceinline__ int ce_row_kind(const CeArgs& a, int64_t n, int32_t& target, float& T) {
+  target = a.targets[n];
+  T = a.temperature ? a.temperature[n] : 1.0f;
+  if (target == a.ignore_index) return -1;
+  if (target < 0 || (int64_t)target >= a.V) return ARCS_ROW_BAD_TARGET;
+  if (!(T > 0.0f) || T == __builtin_inff()) return ARCS_ROW_BAD_TEMPERATURE;
+  return 0;
+}
+
 // cross_entropy_kernel.hip
-void launch_cross_entropy_combine(const CeArgs& a, hipStream_t stream);
+void launch_cross_entropy_prep(const CeArgs& a, bool backward, hipStream_t stream);
+void launch_cross_entropy_combine(const CeArgs& a, bool direct, hipStream_t stream);
 void launch_cross_entropy_dhidden(const CeArgs& a, bool bf16, hipStream_t stream);
 // cross_entropy_mfma.hip
 bool cross_entropy_matrix_path(const CeArgs& a, int dtype, bool backward);

@@ -23,22 +23,13 @@ __global__ __launch_bounds__(kPrepNT) void ce_prep_kernel(CeArgs a) {
   __shared__ int s_count[kPrepNT / kWave];
   __shared__ float s_max[kPrepNT / kWave];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  // 0: listed, 1: masked, otherwise a row status code
-  auto kind = [&](int64_t n, int32_t& t, float& T) {
-    t = a.targets[n];
-    T = a.temperature ? a.temperature[n] : 1.0f;
-    if (t == a.ignore_index) return -1;
-    if (t < 0 || (int64_t)t >= a.V) return (int)ARCS_ROW_BAD_TARGET;
-    if (!(T > 0.0f) || T == __builtin_inff()) return (int)ARCS_ROW_BAD_TEMPERATURE;
-    return 0;
-  };
   float gmax = 1.0f;
   if (BACKWARD) {
     float m = 0.0f;
     for (int64_t n = tid; n < a.N; n += kPrepNT) {
       int32_t t;
       float T;
-      if (kind(n, t, T) != 0) continue;
+      if (ce_row_kind(a, n, t, T) != 0) continue;
       const float g = fabsf(a.grad_loss[n] / T);
       if (g < __builtin_inff() && g > m) m = g;
     }
@@ -53,7 +44,7 @@ __global__ __launch_bounds__(kPrepNT) void ce_prep_kernel(CeArgs a) {
     const int64_t n = n0 + tid;
     int32_t t = 0;
     float T = 1.0f;
-    const int k = n < a.N ? kind(n, t, T) : 1;
+    const int k = n < a.N ? ce_row_kind(a, n, t, T) : 1;
     const uint64_t mask = __ballot(k == 0);
     __syncthreads();  // the last round's counts have been read
     if (lane == 0) s_count[wave] = __popcll(mask);
@@ -95,26 +86,45 @@ __global__ __launch_bounds__(kPrepNT) void ce_prep_kernel(CeArgs a) {
 }
 
 // ---------------------------------------------------------------------------
-// Forward: the slices of a row joined, one wave per listed row.
+// Forward: the slices of a row joined, one workgroup per row (listed, or direct).
 // ---------------------------------------------------------------------------
-__global__ __launch_bounds__(256) void ce_combine_kernel(CeArgs a) {
-  const int64_t i = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 6);
-  const int lane = threadIdx.x & 63;
-  if (i >= a.head->count) return;
-  const float2* p = a.partial + i * a.slices;
-  float m = -__builtin_inff();
-  for (int64_t s = lane; s < a.slices; s += kWave) m = fmaxf(m, p[s].x);
-  for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o, kWave));
-  const float m0 = finite_or_zero(m);
-  float sum = 0.0f;
-  for (int64_t s = lane; s < a.slices; s += kWave) {
-    const float2 q = p[s];
-    sum = fmaf(q.y, exp2_fast(q.x - m0), sum);
+__global__ __launch_bounds__(256) void ce_combine_kernel(CeArgs a, int direct) {
+  __shared__ float2 s_part[4];
+  const int64_t i = blockIdx.x;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  int64_t n = i;
+  if (direct) {
+    int32_t target;
+    float T;
+    const int k = ce_row_kind(a, i, target, T);
+    if (tid == 0 && a.out_status) a.out_status[i] = k < 0 ? 0 : k;
+    if (k != 0) {
+      if (tid == 0) a.out_loss[i] = a.out_lse[i] = k < 0 ? 0.0f : __builtin_nanf("");
+      return;
+    }
+  } else {
+    if (i >= a.head->count) return;
+    n = a.rows[i].row;
   }
-  for (int o = 32; o > 0; o >>= 1) sum += __shfl_xor(sum, o, kWave);
-  if (lane == 0) {
+  // each lane's slices, then the lanes', then the waves' (the first wave goes over the four)
+  const float2* p = a.partial + i * a.slices;
+  float m = -__builtin_inff(), sum = 0.0f;
+  auto join = [&](float m2, float s2) {
+    const float top = fmaxf(m, m2), z = finite_or_zero(top);
+    sum = fmaf(sum, exp2_fast(m - z), s2 * exp2_fast(m2 - z));
+    m = top;
+  };
+#pragma unroll 4
+  for (int64_t s = tid; s < a.slices; s += 256) {
+    const float2 q = p[s];
+    join(q.x, q.y);
+  }
+  for (int o = 32; o > 0; o >>= 1) join(__shfl_xor(m, o, kWave), __shfl_xor(sum, o, kWave));
+  if (lane == 0) s_part[wave] = make_float2(m, sum);
+  __syncthreads();
+  if (tid == 0) {
+    for (int w = 1; w < 4; ++w) join(s_part[w].x, s_part[w].y);
     const float l2 = m + log2f(sum);
-    const int32_t n = a.rows[i].row;
     a.out_lse[n] = l2 * kLn2;
     a.out_loss[n] = (l2 - a.ytarget[i]) * kLn2;
   }
@@ -399,8 +409,13 @@ CePlan cross_entropy_plan(int64_t N, int64_t V, int64_t D, int dtype, bool backw
   return p;
 }
 
-void launch_cross_entropy_combine(const CeArgs& a, hipStream_t stream) {
-  hipLaunchKernelGGL(ce_combine_kernel, dim3((unsigned)tiles(a.N, 4)), dim3(256), 0, stream, a);
+void launch_cross_entropy_prep(const CeArgs& a, bool backward, hipStream_t stream) {
+  if (backward) hipLaunchKernelGGL(ce_prep_kernel<true>, dim3(1), dim3(kPrepNT), 0, stream, a);
+  else hipLaunchKernelGGL(ce_prep_kernel<false>, dim3(1), dim3(kPrepNT), 0, stream, a);
+}
+
+void launch_cross_entropy_combine(const CeArgs& a, bool direct, hipStream_t stream) {
+  hipLaunchKernelGGL(ce_combine_kernel, dim3((unsigned)a.N), dim3(256), 0, stream, a, direct ? 1 : 0);
 }
 
 void launch_cross_entropy_dhidden(const CeArgs& a, bool bf16, hipStream_t stream) {
@@ -413,14 +428,14 @@ static hipError_t launch_general(CeArgs a, bool backward, hipStream_t stream) {
   const dim3 block(256);
   const unsigned nt = (unsigned)tiles(a.N, kGenTile), dt = (unsigned)tiles(a.D, kGenTile);
   if (!backward) {
-    const CePiece pc = {0, a.V, 1, 0};
+    const CePiece pc = {0, a.V, 1, 0, 0};
     a.slices = 2 * tiles(a.V, kGenTile);
     hipLaunchKernelGGL((ce_general_kernel<T, kCeStats>), dim3((unsigned)tiles(a.V, kGenTile), nt), block, 0, stream, a, pc);
-    launch_cross_entropy_combine(a, stream);
+    launch_cross_entropy_combine(a, false, stream);
     return hipGetLastError();
   }
   for (int64_t v0 = 0; v0 < a.V; v0 += a.ds_ld) {
-    const CePiece pc = {v0, a.V - v0 < a.ds_ld ? a.V - v0 : a.ds_ld, v0 == 0, 0};
+    const CePiece pc = {v0, a.V - v0 < a.ds_ld ? a.V - v0 : a.ds_ld, v0 == 0, 0, 0};
     const unsigned vt = (unsigned)tiles(pc.len, kGenTile);
     hipLaunchKernelGGL((ce_general_kernel<T, kCeDs>), dim3(vt, nt), block, 0, stream, a, pc);
     if (a.out_dhidden)
@@ -433,9 +448,8 @@ static hipError_t launch_general(CeArgs a, bool backward, hipStream_t stream) {
 }
 
 hipError_t launch_cross_entropy(const CeArgs& a, int dtype, bool backward, hipStream_t stream) {
-  if (backward) hipLaunchKernelGGL(ce_prep_kernel<true>, dim3(1), dim3(kPrepNT), 0, stream, a);
-  else hipLaunchKernelGGL(ce_prep_kernel<false>, dim3(1), dim3(kPrepNT), 0, stream, a);
   if (cross_entropy_matrix_path(a, dtype, backward)) return launch_cross_entropy_matrix(a, backward, stream);
+  launch_cross_entropy_prep(a, backward, stream);
   return dtype == ARCS_DTYPE_BF16 ? launch_general<__bf16>(a, backward, stream)
                                   : launch_general<float>(a, backward, stream);
 }

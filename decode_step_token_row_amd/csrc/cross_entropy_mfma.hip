@@ -75,7 +75,8 @@ __global__ __launch_bounds__(WM* WN * 64) void ce_tile_kernel(CeArgs a, CePiece 
   __shared__ __align__(1024) char lds[C::kLds];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-  const int64_t count = a.head->count;
+  const bool direct = MODE == kCeStats && pc.direct;
+  const int64_t count = direct ? a.N : a.head->count;
   const int64_t M = C::kLogits ? pc.len : a.D;
   const int64_t N = MODE == kCeDweight ? pc.len : count;
   const uint32_t lds0 = (uint32_t)(uintptr_t)(ARCS_LDS char*)lds;
@@ -145,7 +146,7 @@ __global__ __launch_bounds__(WM* WN * 64) void ce_tile_kernel(CeArgs a, CePiece 
       if (!C::kBOuter) {
         inner_place(inst, lane, r, c);
         const int64_t left = N - 1 - n0, n = r < left ? r : left;
-        if (C::kLogits) ob[t] = (uint32_t)((pc.gather ? (int64_t)a.rows[n0 + n].row * a.hidden_stride : n * a.D) * 2 + c * 2);
+        if (C::kLogits) ob[t] = (uint32_t)((direct ? (n0 + n) * a.hidden_stride : pc.gather ? (int64_t)a.rows[n0 + n].row * a.hidden_stride : n * a.D) * 2 + c * 2);
         else ob[t] = (uint32_t)(n * a.ds_ld * 2 + c * 2);
       } else {
         outer_place<BN>(inst, lane, r, c);
@@ -325,7 +326,13 @@ __global__ __launch_bounds__(WM* WN * 64) void ce_tile_kernel(CeArgs a, CePiece 
         CeRow row;
         row.target = -1;
         row.a = 1.0f;
-        if (n < N) row = a.rows[n];
+        if (n < N && !direct) row = a.rows[n];
+        if (n < N && direct) {
+          float T;
+          const int kind = ce_row_kind(a, n, row.target, T);
+          row.a = kLog2e / (kind == 0 ? T : 1.0f);
+          if (kind != 0) row.target = -1;
+        }
         if (ragged) {
 #pragma unroll
           for (int i = 0; i < MT; ++i)
@@ -507,15 +514,18 @@ bool cross_entropy_matrix_path(const CeArgs& a, int dtype, bool backward) {
 
 hipError_t launch_cross_entropy_matrix(const CeArgs& args, bool backward, hipStream_t stream) {
   CeArgs a = args;
-  CePiece pc = {0, a.V, 1, 0};
+  CePiece pc = {0, a.V, 1, 0, 0};
   // forward: rows are read where they are if one descriptor reaches them all
   pc.gather = !backward && (unsigned __int128)a.N * (unsigned __int128)a.hidden_stride * 2 < kBufMost;
+  // a tile's worth of rows or less: a list would save no product
+  pc.direct = pc.gather && a.N <= 256;
+  if (!pc.direct) launch_cross_entropy_prep(a, backward, stream);
   if (!pc.gather) hipLaunchKernelGGL(ce_copy_kernel, dim3((unsigned)a.N), dim3(256), 0, stream, a);
   if (!backward) {
     const int rows = ce_rows_of_tile(a.N);
     a.slices = tiles(a.V, 256) * (rows == 32 ? 8 : rows == 256 ? 2 : 4);
     launch_rows<kCeStats>(a, pc, stream);
-    launch_cross_entropy_combine(a, stream);
+    launch_cross_entropy_combine(a, pc.direct, stream);
     return hipGetLastError();
   }
   for (int64_t v0 = 0; v0 < a.V; v0 += a.ds_ld) {
