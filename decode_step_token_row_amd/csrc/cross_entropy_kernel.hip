@@ -161,31 +161,29 @@ constexpr int kGenTile = 128, kGenK = 16, kGenLd = kGenTile + 4;
 // Eight consecutive elements of a row from `at` on, zeros from `len` on.
 template <typename T>
 __device__ __forceinline__ void load8(const T* row, int64_t at, int64_t len, float out[8]) {
-  if (row != nullptr && at + 8 <= len && (((uintptr_t)(row + at)) & 15u) == 0) {
-    if (sizeof(T) == 2) {
-      const u32x4 x = *(const u32x4*)(row + at);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        out[2 * e] = bf16_lo(x[e]);
-        out[2 * e + 1] = bf16_hi(x[e]);
-      }
-    } else {
-      const f32x4 x = *(const f32x4*)(row + at), y = *(const f32x4*)(row + at + 4);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        out[e] = x[e];
-        out[4 + e] = y[e];
-      }
-    }
-    return;
-  }
 #pragma unroll
   for (int e = 0; e < 8; ++e) out[e] = row != nullptr && at + e < len ? (float)row[at + e] : 0.0f;
 }
 
-template <typename T, int MODE>
-__global__ __launch_bounds__(256) void ce_general_kernel(CeArgs a, CePiece pc) {
-  __shared__ float sA[kGenK * kGenLd], sB[kGenK * kGenLd];
+// The same of float32 rows whose fours are aligned and whole, without a branch:
+// what lies outside is loaded from `safe` and dropped where it is stored, so
+// that no wait stands beside the loads.
+struct Eight {
+  f32x4 lo, hi;
+  bool has_lo, has_hi;
+};
+__device__ __forceinline__ Eight load8_aligned(const float* row, int64_t at, int64_t len, const float* safe) {
+  Eight v;
+  v.has_lo = row != nullptr && at + 4 <= len;
+  v.has_hi = row != nullptr && at + 8 <= len;
+  v.lo = *(const f32x4*)(v.has_lo ? row + at : safe);
+  v.hi = *(const f32x4*)(v.has_hi ? row + at + 4 : safe);
+  return v;
+}
+
+template <typename T, int MODE, bool ALIGNED>
+__global__ __launch_bounds__(256, 3) void ce_general_kernel(CeArgs a, CePiece pc) {
+  __shared__ float sA[2][kGenK * kGenLd], sB[2][kGenK * kGenLd];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   const int64_t count = a.head->count;
   constexpr bool kLogits = MODE == kCeStats || MODE == kCeDs;
@@ -208,31 +206,24 @@ __global__ __launch_bounds__(256) void ce_general_kernel(CeArgs a, CePiece pc) {
   // this thread's eight elements of a tile: along k of one m, or along m of one k
   const int in_r = tid >> 1, in_k = (tid & 1) * 8;
   const int out_k = tid >> 4, out_m = (tid & 15) * 8;
-  auto load_a = [&](int64_t k0, float v[8]) {
-    if (!kAOuter) {
-      const int64_t m = m0 + in_r;
-      load8<T>(m < M ? W + m * a.weight_stride : nullptr, k0 + in_k, k_hi, v);
-    } else {
-      const int64_t k = k0 + out_k;
-      const T* row = nullptr;
-      if (k < k_hi)
-        row = MODE == kCeDhidden ? W + k * a.weight_stride : H + (int64_t)a.rows[k].row * a.hidden_stride;
-      load8<T>(row, m0 + out_m, M, v);
-    }
-  };
   const int64_t bn = n0 + in_r;
   const T* hrow = kLogits && bn < N ? H + (int64_t)a.rows[bn].row * a.hidden_stride : nullptr;
-  auto load_b = [&](int64_t k0, float v[8]) {
-    if (kLogits) {
-      load8<T>(hrow, k0 + in_k, k_hi, v);
-    } else if (!kBOuter) {
-      load8<float>(bn < N ? S + bn * a.ds_ld : nullptr, k0 + in_k, k_hi, v);
-    } else {
-      const int64_t k = k0 + out_k;
-      load8<float>(k < k_hi ? S + k * a.ds_ld : nullptr, n0 + out_m, N, v);
-    }
+  // row, place in it and its length of this thread's eight elements at k0
+  auto a_row = [&](int64_t k0, int64_t& at, int64_t& len) -> const T* {
+    at = kAOuter ? m0 + out_m : k0 + in_k;
+    len = kAOuter ? M : k_hi;
+    if (!kAOuter) return m0 + in_r < M ? W + (m0 + in_r) * a.weight_stride : nullptr;
+    const int64_t k = k0 + out_k;
+    if (k >= k_hi) return nullptr;
+    return MODE == kCeDhidden ? W + k * a.weight_stride : H + (int64_t)a.rows[k].row * a.hidden_stride;
   };
-  auto store = [&](float* s, bool outer, const float v[8]) {
+  auto s_row = [&](int64_t k0, int64_t& at, int64_t& len) -> const float* {  // dz: zeros from the piece's end on
+    at = kBOuter ? n0 + out_m : k0 + in_k;
+    len = a.ds_ld;
+    const int64_t r = kBOuter ? k0 + out_k : bn;
+    return r < (kBOuter ? k_hi : N) ? S + r * a.ds_ld : nullptr;
+  };
+  auto put = [&](float* s, bool outer, const float v[8]) {
     if (outer) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) s[out_k * kGenLd + out_m + e] = v[e];
@@ -240,6 +231,35 @@ __global__ __launch_bounds__(256) void ce_general_kernel(CeArgs a, CePiece pc) {
 #pragma unroll
       for (int e = 0; e < 8; ++e) s[(in_k + e) * kGenLd + in_r] = v[e];
     }
+  };
+  float va[8], vb[8];
+  Eight ea, eb;
+  auto load = [&](int64_t k0) {
+    int64_t at, len;
+    const T* ra = a_row(k0, at, len);
+    if constexpr (ALIGNED) ea = load8_aligned(ra, at, len, W);
+    else load8<T>(ra, at, len, va);
+    if constexpr (kLogits) {
+      if constexpr (ALIGNED) eb = load8_aligned(hrow, k0 + in_k, k_hi, W);
+      else load8<T>(hrow, k0 + in_k, k_hi, vb);
+    } else {
+      const float* rs = s_row(k0, at, len);
+      if constexpr (ALIGNED) eb = load8_aligned(rs, at, len, S);
+      else load8<float>(rs, at, len, vb);
+    }
+  };
+  auto store = [&](int to) {
+    if (ALIGNED) {
+#pragma unroll
+      for (int e = 0; e < 4; ++e) {
+        va[e] = ea.has_lo ? ea.lo[e] : 0.0f;
+        va[4 + e] = ea.has_hi ? ea.hi[e] : 0.0f;
+        vb[e] = eb.has_lo ? eb.lo[e] : 0.0f;
+        vb[4 + e] = eb.has_hi ? eb.hi[e] : 0.0f;
+      }
+    }
+    put(sA[to], kAOuter, va);
+    put(sB[to], kBOuter, vb);
   };
 
   f32x16 acc[2][2];
@@ -252,32 +272,29 @@ __global__ __launch_bounds__(256) void ce_general_kernel(CeArgs a, CePiece pc) {
   const int wm = (wave & 1) * 64, wn = (wave >> 1) * 64;
   const int fr = lane & 31, fk = lane >> 5;
 
-  float va[8], vb[8];
   if (k_lo < k_hi) {
-    load_a(k_lo, va);
-    load_b(k_lo, vb);
+    load(k_lo);
+    store(0);
   }
-  for (int64_t k0 = k_lo; k0 < k_hi; k0 += kGenK) {
-    store(sA, kAOuter, va);
-    store(sB, kBOuter, vb);
-    __syncthreads();
-    if (k0 + kGenK < k_hi) {
-      load_a(k0 + kGenK, va);
-      load_b(k0 + kGenK, vb);
-    }
+  __syncthreads();
+  int at = 0;
+  for (int64_t k0 = k_lo; k0 < k_hi; k0 += kGenK, at ^= 1) {
+    const bool more = k0 + kGenK < k_hi;
+    if (more) load(k0 + kGenK);
 #pragma unroll
     for (int kk = 0; kk < kGenK; kk += 2) {
       float fa[2], fb[2];
 #pragma unroll
       for (int i = 0; i < 2; ++i) {
-        fa[i] = sA[(kk + fk) * kGenLd + wm + i * 32 + fr];
-        fb[i] = sB[(kk + fk) * kGenLd + wn + i * 32 + fr];
+        fa[i] = sA[at][(kk + fk) * kGenLd + wm + i * 32 + fr];
+        fb[i] = sB[at][(kk + fk) * kGenLd + wn + i * 32 + fr];
       }
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int j = 0; j < 2; ++j) acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x2f32(fa[i], fb[j], acc[i][j], 0, 0, 0);
     }
+    if (more) store(at ^ 1);
     __syncthreads();
   }
 
@@ -323,10 +340,9 @@ __global__ __launch_bounds__(256) void ce_general_kernel(CeArgs a, CePiece pc) {
 #pragma unroll
           for (int r = 0; r < 16; ++r) {
             const int64_t v = row_of(i, r);
-            if (v >= M) continue;
             float p = exp2_fast(fmaf(acc[i][j][r], row.a, -row.lse2));
             if (pc.v0 + v == row.target) p -= 1.0f;
-            out[v] = p * row.c;
+            out[v] = v < M ? p * row.c : 0.0f;  // ds_ld is a multiple of the tile
           }
       }
     } else if (n < N) {
@@ -423,25 +439,25 @@ void launch_cross_entropy_dhidden(const CeArgs& a, bool bf16, hipStream_t stream
   else hipLaunchKernelGGL(ce_dhidden_kernel<false>, dim3((unsigned)a.N), dim3(256), 0, stream, a);
 }
 
-template <typename T>
+template <typename T, bool ALIGNED>
 static hipError_t launch_general(CeArgs a, bool backward, hipStream_t stream) {
   const dim3 block(256);
   const unsigned nt = (unsigned)tiles(a.N, kGenTile), dt = (unsigned)tiles(a.D, kGenTile);
   if (!backward) {
     const CePiece pc = {0, a.V, 1, 0, 0};
     a.slices = 2 * tiles(a.V, kGenTile);
-    hipLaunchKernelGGL((ce_general_kernel<T, kCeStats>), dim3((unsigned)tiles(a.V, kGenTile), nt), block, 0, stream, a, pc);
+    hipLaunchKernelGGL((ce_general_kernel<T, kCeStats, ALIGNED>), dim3((unsigned)tiles(a.V, kGenTile), nt), block, 0, stream, a, pc);
     launch_cross_entropy_combine(a, false, stream);
     return hipGetLastError();
   }
   for (int64_t v0 = 0; v0 < a.V; v0 += a.ds_ld) {
     const CePiece pc = {v0, a.V - v0 < a.ds_ld ? a.V - v0 : a.ds_ld, v0 == 0, 0, 0};
     const unsigned vt = (unsigned)tiles(pc.len, kGenTile);
-    hipLaunchKernelGGL((ce_general_kernel<T, kCeDs>), dim3(vt, nt), block, 0, stream, a, pc);
+    hipLaunchKernelGGL((ce_general_kernel<T, kCeDs, ALIGNED>), dim3(vt, nt), block, 0, stream, a, pc);
     if (a.out_dhidden)
-      hipLaunchKernelGGL((ce_general_kernel<T, kCeDhidden>), dim3(dt, nt, (unsigned)a.splits), block, 0, stream, a, pc);
+      hipLaunchKernelGGL((ce_general_kernel<T, kCeDhidden, ALIGNED>), dim3(dt, nt, (unsigned)a.splits), block, 0, stream, a, pc);
     if (a.out_dweight)
-      hipLaunchKernelGGL((ce_general_kernel<T, kCeDweight>), dim3(vt, dt), block, 0, stream, a, pc);
+      hipLaunchKernelGGL((ce_general_kernel<T, kCeDweight, ALIGNED>), dim3(vt, dt), block, 0, stream, a, pc);
   }
   if (a.out_dhidden) launch_cross_entropy_dhidden(a, sizeof(T) == 2, stream);
   return hipGetLastError();
@@ -450,8 +466,10 @@ static hipError_t launch_general(CeArgs a, bool backward, hipStream_t stream) {
 hipError_t launch_cross_entropy(const CeArgs& a, int dtype, bool backward, hipStream_t stream) {
   if (cross_entropy_matrix_path(a, dtype, backward)) return launch_cross_entropy_matrix(a, backward, stream);
   launch_cross_entropy_prep(a, backward, stream);
-  return dtype == ARCS_DTYPE_BF16 ? launch_general<__bf16>(a, backward, stream)
-                                  : launch_general<float>(a, backward, stream);
+  if (dtype == ARCS_DTYPE_BF16) return launch_general<__bf16, false>(a, backward, stream);
+  const bool aligned = a.D % 4 == 0 && a.hidden_stride % 4 == 0 && a.weight_stride % 4 == 0 &&
+                       (((uintptr_t)a.hidden | (uintptr_t)a.weight) & 15u) == 0;
+  return aligned ? launch_general<float, true>(a, backward, stream) : launch_general<float, false>(a, backward, stream);
 }
 
 }  // namespace arcs

@@ -485,9 +485,10 @@ template <int MODE, int WM, int WN, int MT, int NT, int S>
 void launch_tile(const CeArgs& a, const CePiece& pc, hipStream_t stream) {
   using C = CeTile<MODE, WM, WN, MT, NT, S>;
   const int64_t m = C::kLogits ? pc.len : a.D, n = MODE == kCeDweight ? pc.len : a.N;
-  // one workgroup for each compute unit (LDS holds no second), at most
+  // as many workgroups as the compute units hold (by LDS), at most
+  constexpr int64_t kMost = 256 * (163840 / C::kLds);
   const int64_t all = tiles(m, C::BM) * tiles(n, C::BN);
-  const int64_t blocks = MODE == kCeDhidden ? a.workers : all < 256 ? tiles(all, 8) * 8 : 256;
+  const int64_t blocks = MODE == kCeDhidden ? a.workers : all < kMost ? tiles(all, 8) * 8 : kMost;
   hipLaunchKernelGGL((ce_tile_kernel<MODE, WM, WN, MT, NT, S>), dim3((unsigned)blocks), dim3(C::kThreads), 0, stream, a, pc);
 }
 
@@ -495,6 +496,9 @@ template <int MODE>
 void launch_rows(const CeArgs& a, const CePiece& pc, hipStream_t stream) {
   if constexpr (MODE != kCeDweight) {
     const int rows = ce_rows_of_tile(a.N);
+    // 128 of the vocabulary a tile where 256 would leave compute units without one
+    if constexpr (MODE != kCeDhidden)
+      if (rows == 32 && tiles(pc.len, 256) < 256) return launch_tile<MODE, 4, 1, 1, 1, 4>(a, pc, stream);
     if (rows == 32) return launch_tile<MODE, 8, 1, 1, 1, 4>(a, pc, stream);
     if (rows == 64) return launch_tile<MODE, 4, 2, 2, 1, 3>(a, pc, stream);
     if (rows == 128) return launch_tile<MODE, 4, 2, 2, 2, 3>(a, pc, stream);
@@ -523,7 +527,8 @@ hipError_t launch_cross_entropy_matrix(const CeArgs& args, bool backward, hipStr
   if (!pc.gather) hipLaunchKernelGGL(ce_copy_kernel, dim3((unsigned)a.N), dim3(256), 0, stream, a);
   if (!backward) {
     const int rows = ce_rows_of_tile(a.N);
-    a.slices = tiles(a.V, 256) * (rows == 32 ? 8 : rows == 256 ? 2 : 4);
+    a.slices = rows == 32 ? tiles(a.V, tiles(a.V, 256) < 256 ? 128 : 256) * (tiles(a.V, 256) < 256 ? 4 : 8)
+                          : tiles(a.V, 256) * (rows == 256 ? 2 : 4);
     launch_rows<kCeStats>(a, pc, stream);
     launch_cross_entropy_combine(a, pc.direct, stream);
     return hipGetLastError();
