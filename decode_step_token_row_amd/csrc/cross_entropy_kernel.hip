@@ -135,20 +135,19 @@ __global__ __launch_bounds__(256) void ce_combine_kernel(CeArgs a, int direct) {
 // ---------------------------------------------------------------------------
 template <bool BF16>
 __global__ __launch_bounds__(256) void ce_dhidden_kernel(CeArgs a) {
-  const int64_t n = blockIdx.x;
+  const int64_t n = blockIdx.x, d = (int64_t)blockIdx.y * 256 + threadIdx.x;
+  if (d >= a.D) return;
   const int i = a.place[n];
-  const float g = a.head->gmax;
-  const int64_t step = a.N * a.D;
-  for (int64_t d = threadIdx.x; d < a.D; d += 256) {
-    float v = 0.0f;
-    if (i >= 0) {
-      const float* p = a.slab + (int64_t)i * a.D + d;
-      for (int s = 0; s < a.splits; ++s) v += p[s * step];
-      v *= g;
-    }
-    if (BF16) ((__bf16*)a.out_dhidden)[n * a.D + d] = (__bf16)v;
-    else ((float*)a.out_dhidden)[n * a.D + d] = v;
+  float v = 0.0f;
+  if (i >= 0) {
+    const float* p = a.slab + (int64_t)i * a.D + d;
+    const int64_t step = a.N * a.D;
+#pragma unroll 8
+    for (int s = 0; s < a.splits; ++s) v += p[s * step];
+    v *= a.head->gmax;
   }
+  if (BF16) ((__bf16*)a.out_dhidden)[n * a.D + d] = (__bf16)v;
+  else ((float*)a.out_dhidden)[n * a.D + d] = v;
 }
 
 // ---------------------------------------------------------------------------
@@ -435,8 +434,9 @@ void launch_cross_entropy_combine(const CeArgs& a, bool direct, hipStream_t stre
 }
 
 void launch_cross_entropy_dhidden(const CeArgs& a, bool bf16, hipStream_t stream) {
-  if (bf16) hipLaunchKernelGGL(ce_dhidden_kernel<true>, dim3((unsigned)a.N), dim3(256), 0, stream, a);
-  else hipLaunchKernelGGL(ce_dhidden_kernel<false>, dim3((unsigned)a.N), dim3(256), 0, stream, a);
+  const dim3 grid((unsigned)a.N, (unsigned)tiles(a.D, 256));
+  if (bf16) hipLaunchKernelGGL(ce_dhidden_kernel<true>, grid, dim3(256), 0, stream, a);
+  else hipLaunchKernelGGL(ce_dhidden_kernel<false>, grid, dim3(256), 0, stream, a);
 }
 
 template <typename T, bool ALIGNED>

@@ -265,7 +265,6 @@ __global__ __launch_bounds__(256, 4) void w4_rows_kernel(W4Args a) {
 #pragma unroll
       for (int g = 0; g < K::kGroups; ++g) {
         const int gs = c * K::kGroups + g;
-        if (K::kTurn && (int64_t)(stage * SC + c) * kW4Step + g * GROUP >= a.D) break;  // no such group
         const uint2 sc = scale[gs * 64];
         f32x4 acc = *(const f32x4*)&s_sum[stage & 1][gs][j * 4];
 #pragma unroll
@@ -379,52 +378,56 @@ __global__ __launch_bounds__(WB* WV * 64, MT == 2 ? 3 : 2) void w4_batch_kernel(
     const char* x = lds + (part & 1) * kStage;
     const uint2* scale = &s_scale[part & 1][wv * RT * 16 + r];
     const float* sums = (const float*)(x + kSumAt);
+    // Products p = 0 .. 4 NS - 1 of 32 k each; the hidden states of the next one are
+    // read while one runs.  Groups past D meet zeros (and the last group's scale).
+    constexpr int kAll = 4 * NS;
+    bf16x8 xf[2][MT];
+    auto read_x = [&](int p) {
 #pragma unroll
-    for (int c = 0; c < NS; ++c) {
-      u32x4 w[RT];
+      for (int m = 0; m < MT; ++m)
+        xf[p & 1][m] = *(const bf16x8*)(x + ((p >> 2) * kRows + (wb * MT + m) * 16 + r) * 256 + ((((p & 3) * 4 + j) ^ r) * 16));
+    };
+    u32x4 w[RT];
+    uint2 sc[RT];
+    f32x4 acc[MT][RT];
+    read_x(0);
 #pragma unroll
-      for (int t = 0; t < RT; ++t) w[t] = K::kTurn ? w4_turn(next[c][t]) : next[c][t];
-      rows.load(next[c], ahead + c);
+    for (int p = 0; p < kAll; ++p) {
+      const int c = p / 4, gs = p / K::kProducts, i = p % K::kProducts;
+      if (p % 4 == 0) {
 #pragma unroll
-      for (int g = 0; g < K::kGroups; ++g) {
-        const int gs = c * K::kGroups + g;
-        if ((int64_t)(part * NS + c) * kW4Step + g * GROUP >= a.D) break;  // no such group
-        uint2 sc[RT];
+        for (int t = 0; t < RT; ++t) w[t] = K::kTurn ? w4_turn(next[c][t]) : next[c][t];
+        rows.load(next[c], ahead + c);
+      }
+      if (i == 0) {
 #pragma unroll
         for (int t = 0; t < RT; ++t) sc[t] = scale[gs * kCols + t * 16];
-        f32x4 acc[MT][RT];
 #pragma unroll
-        for (int i = 0; i < K::kProducts; ++i) {
-          bf16x8 xf[MT];
+        for (int m = 0; m < MT; ++m) {
+          const f32x4 start = *(const f32x4*)(sums + gs * kRows + (wb * MT + m) * 16 + j * 4);
+#pragma unroll
+          for (int t = 0; t < RT; ++t) acc[m][t] = start;
+        }
+      }
+      if (p + 1 < kAll) read_x(p + 1);
+#pragma unroll
+      for (int t = 0; t < RT; ++t) {
+        const bf16x8 wf = w4_unpack<ZERO>(w[t][p % 4], sc[t].y);
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+          acc[m][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[p & 1][m], wf, acc[m][t], 0, 0, 0);
+      }
+      if (i == K::kProducts - 1) {
+#pragma unroll
+        for (int t = 0; t < RT; ++t)
 #pragma unroll
           for (int m = 0; m < MT; ++m) {
-            const int row = (wb * MT + m) * 16;
-            if (i == 0) {
-              const f32x4 start = *(const f32x4*)(sums + gs * kRows + row + j * 4);
-#pragma unroll
-              for (int t = 0; t < RT; ++t) acc[m][t] = start;
-            }
-            xf[m] = *(const bf16x8*)(x + (c * kRows + row + r) * 256 + ((((g * K::kProducts + i) * 4 + j) ^ r) * 16));
-          }
-#pragma unroll
-          for (int t = 0; t < RT; ++t) {
-            const bf16x8 wf = w4_unpack<ZERO>(w[t][g * K::kProducts + i], sc[t].y);
-#pragma unroll
-            for (int m = 0; m < MT; ++m) acc[m][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[m], wf, acc[m][t], 0, 0, 0);
-          }
-        }
-#pragma unroll
-        for (int t = 0; t < RT; ++t)
-#pragma unroll
-          for (int m = 0; m < MT; ++m)
 #pragma unroll
             for (int e = 0; e < 4; ++e) total[m][t][e] = fmaf(__uint_as_float(sc[t].x), acc[m][t][e], total[m][t][e]);
-        // one group at a time in registers: its sums are not left for later
-#pragma unroll
-        for (int t = 0; t < RT; ++t)
-#pragma unroll
-          for (int m = 0; m < MT; ++m) asm volatile("" : "+v"(total[m][t]));
+            asm volatile("" : "+v"(total[m][t]));  // one group at a time in registers: its sums are not left for later
+          }
       }
+      __builtin_amdgcn_sched_barrier(0);
     }
     if (part + 1 < parts) scales.store(s_scale[(part + 1) & 1]);
   }
