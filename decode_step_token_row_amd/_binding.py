@@ -585,7 +585,7 @@ def _dtype_code_of(t, name: str) -> int:
     raise TypeError(f"{name} must be bfloat16 or float32, got {t.dtype}")
 
 
-def _cross_entropy_inputs(hidden, weight, targets, temperature):
+def _cross_entropy_inputs(hidden, weight, targets, temperature, ignore_index):
     torch = _torch()
     N, D, dev = _hidden_shape(hidden)
     dt = _dtype_code_of(hidden, "hidden")
@@ -595,6 +595,8 @@ def _cross_entropy_inputs(hidden, weight, targets, temperature):
     _vector(targets, "targets", torch.int32, N, dev)
     if temperature is not None:
         _vector(temperature, "temperature", torch.float32, N, dev)
+    if not -2**31 <= ignore_index < 2**31:
+        raise ValueError("ignore_index must fit int32")
     return N, V, D, dev, dt, hs, ws
 
 
@@ -619,7 +621,7 @@ def linear_cross_entropy(hidden, weight, targets, temperature=None, ignore_index
     are computed by that call.
     """
     torch = _torch()
-    N, V, D, dev, dt, hs, ws = _cross_entropy_inputs(hidden, weight, targets, temperature)
+    N, V, D, dev, dt, hs, ws = _cross_entropy_inputs(hidden, weight, targets, temperature, ignore_index)
     with _work_on(dev, stream):
         if out_loss is None:
             out_loss = torch.empty(N, dtype=torch.float32, device=dev)
@@ -647,7 +649,7 @@ def linear_cross_entropy_backward(hidden, weight, targets, lse, grad_loss, tempe
     sum(grad_loss * loss), in the inputs' type; None in place of one not wanted.
     ``lse`` is the forward call's, ``grad_loss`` float32 [N]."""
     torch = _torch()
-    N, V, D, dev, dt, hs, ws = _cross_entropy_inputs(hidden, weight, targets, temperature)
+    N, V, D, dev, dt, hs, ws = _cross_entropy_inputs(hidden, weight, targets, temperature, ignore_index)
     _vector(lse, "lse", torch.float32, N, dev)
     _vector(grad_loss, "grad_loss", torch.float32, N, dev)
     with _work_on(dev, stream):

@@ -78,8 +78,9 @@ struct CePlan {
 };
 CePlan cross_entropy_plan(int64_t N, int64_t V, int64_t D, int dtype, bool backward);
 
-// Matrix kernels: rows of a tile's n side, by the call's rows.
-inline int ce_rows_of_tile(int64_t N) { return N <= 32 ? 32 : N <= 64 ? 64 : N <= 128 ? 128 : 256; }
+// Matrix kernels: a tile's n side (the call's rows) and, in dhidden, its m side.
+inline int ce_rows_of_tile(int64_t N, bool bf16) { return N <= 32 ? 32 : N <= 64 ? 64 : N <= 128 || !bf16 ? 128 : 256; }
+inline int ce_columns_of_tile(int64_t N, bool bf16) { return !bf16 && N > 64 ? 128 : 256; }
 
 hipError_t launch_cross_entropy(const CeArgs& a, int dtype, bool backward, hipStream_t stream);
 

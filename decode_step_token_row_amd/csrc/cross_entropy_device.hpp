@@ -47,7 +47,7 @@ void launch_cross_entropy_prep(const CeArgs& a, bool backward, hipStream_t strea
 void launch_cross_entropy_combine(const CeArgs& a, bool direct, hipStream_t stream);
 void launch_cross_entropy_dhidden(const CeArgs& a, bool bf16, hipStream_t stream);
 // cross_entropy_mfma.hip
-bool cross_entropy_matrix_path(const CeArgs& a, int dtype, bool backward);
-hipError_t launch_cross_entropy_matrix(const CeArgs& a, bool backward, hipStream_t stream);
+bool cross_entropy_matrix_path(const CeArgs& a, int dtype);
+hipError_t launch_cross_entropy_matrix(const CeArgs& a, int dtype, bool backward, hipStream_t stream);
 
 }  // namespace arcs

@@ -164,23 +164,7 @@ __device__ __forceinline__ void load8(const T* row, int64_t at, int64_t len, flo
   for (int e = 0; e < 8; ++e) out[e] = row != nullptr && at + e < len ? (float)row[at + e] : 0.0f;
 }
 
-// The same of float32 rows whose fours are aligned and whole, without a branch:
-// what lies outside is loaded from `safe` and dropped where it is stored, so
-// that no wait stands beside the loads.
-struct Eight {
-  f32x4 lo, hi;
-  bool has_lo, has_hi;
-};
-__device__ __forceinline__ Eight load8_aligned(const float* row, int64_t at, int64_t len, const float* safe) {
-  Eight v;
-  v.has_lo = row != nullptr && at + 4 <= len;
-  v.has_hi = row != nullptr && at + 8 <= len;
-  v.lo = *(const f32x4*)(v.has_lo ? row + at : safe);
-  v.hi = *(const f32x4*)(v.has_hi ? row + at + 4 : safe);
-  return v;
-}
-
-template <typename T, int MODE, bool ALIGNED>
+template <typename T, int MODE>
 __global__ __launch_bounds__(256, 3) void ce_general_kernel(CeArgs a, CePiece pc) {
   __shared__ float sA[2][kGenK * kGenLd], sB[2][kGenK * kGenLd];
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
@@ -232,31 +216,18 @@ __global__ __launch_bounds__(256, 3) void ce_general_kernel(CeArgs a, CePiece pc
     }
   };
   float va[8], vb[8];
-  Eight ea, eb;
   auto load = [&](int64_t k0) {
     int64_t at, len;
     const T* ra = a_row(k0, at, len);
-    if constexpr (ALIGNED) ea = load8_aligned(ra, at, len, W);
-    else load8<T>(ra, at, len, va);
+    load8<T>(ra, at, len, va);
     if constexpr (kLogits) {
-      if constexpr (ALIGNED) eb = load8_aligned(hrow, k0 + in_k, k_hi, W);
-      else load8<T>(hrow, k0 + in_k, k_hi, vb);
+      load8<T>(hrow, k0 + in_k, k_hi, vb);
     } else {
       const float* rs = s_row(k0, at, len);
-      if constexpr (ALIGNED) eb = load8_aligned(rs, at, len, S);
-      else load8<float>(rs, at, len, vb);
+      load8<float>(rs, at, len, vb);
     }
   };
   auto store = [&](int to) {
-    if (ALIGNED) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) {
-        va[e] = ea.has_lo ? ea.lo[e] : 0.0f;
-        va[4 + e] = ea.has_hi ? ea.hi[e] : 0.0f;
-        vb[e] = eb.has_lo ? eb.lo[e] : 0.0f;
-        vb[4 + e] = eb.has_hi ? eb.hi[e] : 0.0f;
-      }
-    }
     put(sA[to], kAOuter, va);
     put(sB[to], kBOuter, vb);
   };
@@ -389,7 +360,7 @@ CePlan cross_entropy_plan(int64_t N, int64_t V, int64_t D, int dtype, bool backw
   typedef unsigned __int128 u128;
   const bool bf16 = dtype == ARCS_DTYPE_BF16;
   p.rows = take((u128)N * sizeof(CeRow));
-  if (bf16) p.hc = take((u128)N * D * 2);
+  p.hc = take((u128)N * D * (bf16 ? 2 : 4));
   p.splits = 1;
   if (!backward) {
     p.slices = 8 * tiles(V, 256);
@@ -408,15 +379,14 @@ CePlan cross_entropy_plan(int64_t N, int64_t V, int64_t D, int dtype, bool backw
     p.splits = (int)(splits < 1 ? 1 : splits);
     p.place = take((u128)N * 4);
     p.ds = take((u128)N * p.piece * 4);
+    // dhidden's partial sums: the general kernel's splits or the matrix kernels' parts
     u128 slab = (u128)p.splits * N * D * 4;
-    if (bf16) {
-      const int64_t rows = ce_rows_of_tile(N);
-      // one workgroup for each compute unit, unless that leaves them less than 512 of k
-      const int64_t t = tiles(N, rows) * tiles(D, 256), most = t * tiles(p.piece, 512);
-      p.workers = most < 256 ? (int)tiles(most, 8) * 8 : 256;
-      const u128 parts = (u128)(p.workers + t) * rows * 256 * 4;
-      if (parts > slab) slab = parts;
-    }
+    const int64_t rows = ce_rows_of_tile(N, bf16), columns = ce_columns_of_tile(N, bf16);
+    // as many workgroups as the compute units hold, unless that leaves them less than 512 of k
+    const int64_t jobs = tiles(N, rows) * tiles(D, columns), share = jobs * tiles(p.piece, 512), full = columns == 128 ? 512 : 256;
+    p.workers = (int)(share < full ? tiles(share, 8) * 8 : full);
+    const u128 parts = (u128)(p.workers + jobs) * rows * columns * 4;
+    if (parts > slab) slab = parts;
     p.slab = take(slab);
   }
   if (at > (u128)INT64_MAX) p.fits = false;
@@ -439,37 +409,34 @@ void launch_cross_entropy_dhidden(const CeArgs& a, bool bf16, hipStream_t stream
   else hipLaunchKernelGGL(ce_dhidden_kernel<false>, grid, dim3(256), 0, stream, a);
 }
 
-template <typename T, bool ALIGNED>
+template <typename T>
 static hipError_t launch_general(CeArgs a, bool backward, hipStream_t stream) {
   const dim3 block(256);
   const unsigned nt = (unsigned)tiles(a.N, kGenTile), dt = (unsigned)tiles(a.D, kGenTile);
   if (!backward) {
     const CePiece pc = {0, a.V, 1, 0, 0};
     a.slices = 2 * tiles(a.V, kGenTile);
-    hipLaunchKernelGGL((ce_general_kernel<T, kCeStats, ALIGNED>), dim3((unsigned)tiles(a.V, kGenTile), nt), block, 0, stream, a, pc);
+    hipLaunchKernelGGL((ce_general_kernel<T, kCeStats>), dim3((unsigned)tiles(a.V, kGenTile), nt), block, 0, stream, a, pc);
     launch_cross_entropy_combine(a, false, stream);
     return hipGetLastError();
   }
   for (int64_t v0 = 0; v0 < a.V; v0 += a.ds_ld) {
     const CePiece pc = {v0, a.V - v0 < a.ds_ld ? a.V - v0 : a.ds_ld, v0 == 0, 0, 0};
     const unsigned vt = (unsigned)tiles(pc.len, kGenTile);
-    hipLaunchKernelGGL((ce_general_kernel<T, kCeDs, ALIGNED>), dim3(vt, nt), block, 0, stream, a, pc);
+    hipLaunchKernelGGL((ce_general_kernel<T, kCeDs>), dim3(vt, nt), block, 0, stream, a, pc);
     if (a.out_dhidden)
-      hipLaunchKernelGGL((ce_general_kernel<T, kCeDhidden, ALIGNED>), dim3(dt, nt, (unsigned)a.splits), block, 0, stream, a, pc);
+      hipLaunchKernelGGL((ce_general_kernel<T, kCeDhidden>), dim3(dt, nt, (unsigned)a.splits), block, 0, stream, a, pc);
     if (a.out_dweight)
-      hipLaunchKernelGGL((ce_general_kernel<T, kCeDweight, ALIGNED>), dim3(vt, dt), block, 0, stream, a, pc);
+      hipLaunchKernelGGL((ce_general_kernel<T, kCeDweight>), dim3(vt, dt), block, 0, stream, a, pc);
   }
   if (a.out_dhidden) launch_cross_entropy_dhidden(a, sizeof(T) == 2, stream);
   return hipGetLastError();
 }
 
 hipError_t launch_cross_entropy(const CeArgs& a, int dtype, bool backward, hipStream_t stream) {
-  if (cross_entropy_matrix_path(a, dtype, backward)) return launch_cross_entropy_matrix(a, backward, stream);
+  if (cross_entropy_matrix_path(a, dtype)) return launch_cross_entropy_matrix(a, dtype, backward, stream);
   launch_cross_entropy_prep(a, backward, stream);
-  if (dtype == ARCS_DTYPE_BF16) return launch_general<__bf16, false>(a, backward, stream);
-  const bool aligned = a.D % 4 == 0 && a.hidden_stride % 4 == 0 && a.weight_stride % 4 == 0 &&
-                       (((uintptr_t)a.hidden | (uintptr_t)a.weight) & 15u) == 0;
-  return aligned ? launch_general<float, true>(a, backward, stream) : launch_general<float, false>(a, backward, stream);
+  return dtype == ARCS_DTYPE_BF16 ? launch_general<__bf16>(a, backward, stream) : launch_general<float>(a, backward, stream);
 }
 
 }  // namespace arcs

@@ -20,25 +20,26 @@
 
 namespace arcs {
 
-constexpr int kTK = 64;                         // k of one tile
 __device__ __forceinline__ u32x4 uniform4(u32x4 d) {
 #pragma unroll
   for (int e = 0; e < 4; ++e) d[e] = __builtin_amdgcn_readfirstlane(d[e]);
   return d;
 }
 
-template <int MODE, int WM, int WN, int MT, int NT, int S>
+template <typename T, int MODE, int WM, int WN, int MT, int NT, int S>
 struct CeTile {
   static constexpr int kThreads = WM * WN * 64, kWaves = WM * WN;
   static constexpr int BM = WM * MT * 32, BN = WN * NT * 32;
   static constexpr bool kLogits = MODE == kCeStats || MODE == kCeDs;
   static constexpr bool kAOuter = !kLogits, kBOuter = MODE == kCeDweight;
-  static constexpr int kABytes = BM * kTK * 2, kBBytes = BN * kTK * 2, kStage = kABytes + kBBytes;
+  static constexpr bool kBf16 = sizeof(T) == 2;
+  static constexpr int kTK = 128 / sizeof(T);  // k of one tile
+  static constexpr int kABytes = BM * 128, kBBytes = BN * 128, kStage = kABytes + kBBytes;
   static constexpr int kALoads = BM / 8, kBLoads = BN / 8;  // of 1024 bytes each
   static constexpr int kAPer = (kALoads + kWaves - 1) / kWaves, kBPer = (kBLoads + kWaves - 1) / kWaves;
   static constexpr int kPer = kAPer + kBPer;
   // bfloat16 results go out through 32 rows of kOutM columns a wave
-  static constexpr bool kOut = MODE == kCeDs || MODE == kCeDweight;
+  static constexpr bool kOut = kBf16 && (MODE == kCeDs || MODE == kCeDweight);
   static constexpr int kOutM = MT % 2 == 0 && S * kStage + kWaves * 32 * 64 * 2 <= 163840 ? 64 : 32;
   static constexpr int kOutBytes = 32 * kOutM * 2, kLds = S * kStage + (kOut ? kWaves * kOutBytes : 0);
 };
@@ -55,23 +56,25 @@ __device__ __forceinline__ int ce_tile_index(int m, int n, int mt, int nt) {
 }
 
 // Where a lane's 16 bytes of load `inst` lie in its tile: row and element in the row.
-template <int W>
+template <typename T, int W>
 __device__ __forceinline__ void outer_place(int inst, int lane, int& k, int& col) {
-  constexpr int kLanes = W / 8;
+  constexpr int kLanes = W * (int)sizeof(T) / 16;
   k = inst * (64 / kLanes) + lane / kLanes;
   const int p = lane % kLanes;
   const int turn = W >= 128 ? (k & 3) << 1 : W == 64 ? ((k >> 1) & 1) << 1 : 0;
-  col = ((p >> 1) ^ turn) * 16 + (p & 1) * 8;
+  col = sizeof(T) == 2 ? ((p >> 1) ^ turn) * 16 + (p & 1) * 8 : p * 4;
 }
+template <typename T>
 __device__ __forceinline__ void inner_place(int inst, int lane, int& r, int& k) {
   r = inst * 8 + (lane >> 3);
-  k = ((lane & 7) ^ ((r >> 1) & 7)) * 8;
+  k = ((lane & 7) ^ ((r >> 1) & 7)) * (16 / (int)sizeof(T));
 }
 
-template <int MODE, int WM, int WN, int MT, int NT, int S>
-__global__ __launch_bounds__(WM* WN * 64) void ce_tile_kernel(CeArgs a, CePiece pc) {
-  using C = CeTile<MODE, WM, WN, MT, NT, S>;
-  constexpr int BM = C::BM, BN = C::BN;
+template <typename T, int MODE, int WM, int WN, int MT, int NT, int S>
+__global__ __launch_bounds__(WM* WN * 64, 2) void ce_tile_kernel(CeArgs a, CePiece pc) {
+  using C = CeTile<T, MODE, WM, WN, MT, NT, S>;
+  constexpr int BM = C::BM, BN = C::BN, kTK = C::kTK;
+  constexpr int64_t E = sizeof(T);
   __shared__ __align__(1024) char lds[C::kLds];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -106,11 +109,11 @@ __global__ __launch_bounds__(WM* WN * 64) void ce_tile_kernel(CeArgs a, CePiece 
   const char *pa, *pb;
   int64_t na, nb;
   uint32_t oa[C::kAPer], ob[C::kBPer];
-  const uint16_t* W = (const uint16_t*)a.weight + pc.v0 * a.weight_stride;
-  const uint16_t* H = (const uint16_t*)(pc.gather ? a.hidden : a.hc);
-  const uint16_t* Z = (const uint16_t*)a.ds;
-  const int64_t step_a = C::kLogits ? kTK * 2 : MODE == kCeDhidden ? kTK * a.weight_stride * 2 : kTK * a.D * 2;
-  const int64_t step_b = MODE == kCeDweight ? kTK * a.ds_ld * 2 : kTK * 2;
+  const T* W = (const T*)a.weight + pc.v0 * a.weight_stride;
+  const T* H = (const T*)(pc.gather ? a.hidden : a.hc);
+  const T* Z = (const T*)a.ds;
+  const int64_t step_a = C::kLogits ? 128 : MODE == kCeDhidden ? kTK * a.weight_stride * E : kTK * a.D * E;
+  const int64_t step_b = MODE == kCeDweight ? kTK * a.ds_ld * E : 128;
   auto place = [&](int job) {
     ce_tile_place(job, mt, nt, m0, n0);
     m0 *= BM;
@@ -130,13 +133,13 @@ __global__ __launch_bounds__(WM* WN * 64) void ce_tile_kernel(CeArgs a, CePiece 
       const int inst = (wave + t * C::kWaves) % C::kALoads;
       int r, c;
       if (!C::kAOuter) {
-        inner_place(inst, lane, r, c);
+        inner_place<T>(inst, lane, r, c);
         const int64_t left = M - 1 - m0;
-        oa[t] = (uint32_t)((r < left ? r : left) * a.weight_stride * 2 + c * 2);
+        oa[t] = (uint32_t)((r < left ? r : left) * a.weight_stride * E + c * E);
       } else {
-        outer_place<BM>(inst, lane, r, c);
+        outer_place<T, BM>(inst, lane, r, c);
         const int64_t ld = MODE == kCeDhidden ? a.weight_stride : a.D;
-        oa[t] = m0 + c < M ? (uint32_t)(r * ld * 2 + c * 2) : kNoLoad;
+        oa[t] = m0 + c < M ? (uint32_t)(r * ld * E + c * E) : kNoLoad;
       }
     }
 #pragma unroll
@@ -144,13 +147,13 @@ __global__ __launch_bounds__(WM* WN * 64) void ce_tile_kernel(CeArgs a, CePiece 
       const int inst = (wave + t * C::kWaves) % C::kBLoads;
       int r, c;
       if (!C::kBOuter) {
-        inner_place(inst, lane, r, c);
+        inner_place<T>(inst, lane, r, c);
         const int64_t left = N - 1 - n0, n = r < left ? r : left;
-        if (C::kLogits) ob[t] = (uint32_t)((direct ? (n0 + n) * a.hidden_stride : pc.gather ? (int64_t)a.rows[n0 + n].row * a.hidden_stride : n * a.D) * 2 + c * 2);
-        else ob[t] = (uint32_t)(n * a.ds_ld * 2 + c * 2);
+        if (C::kLogits) ob[t] = (uint32_t)((direct ? (n0 + n) * a.hidden_stride : pc.gather ? (int64_t)a.rows[n0 + n].row * a.hidden_stride : n * a.D) * E + c * E);
+        else ob[t] = (uint32_t)(n * a.ds_ld * E + c * E);
       } else {
-        outer_place<BN>(inst, lane, r, c);
-        ob[t] = (uint32_t)(r * a.ds_ld * 2 + c * 2);
+        outer_place<T, BN>(inst, lane, r, c);
+        ob[t] = (uint32_t)(r * a.ds_ld * E + c * E);
       }
     }
     if (C::kLogits) {
@@ -158,13 +161,13 @@ __global__ __launch_bounds__(WM* WN * 64) void ce_tile_kernel(CeArgs a, CePiece 
       pb = (const char*)(pc.gather ? H : H + n0 * a.D);
     } else if (MODE == kCeDhidden) {
       pa = (const char*)(W + k_lo * a.weight_stride + m0);
-      na = ((pc.len - k_lo) * a.weight_stride - m0) * 2;
+      na = ((pc.len - k_lo) * a.weight_stride - m0) * E;
       pb = (const char*)(Z + n0 * a.ds_ld + k_lo);
     } else {
       pa = (const char*)(H + m0);
-      na = (count * a.D - m0) * 2;
+      na = (count * a.D - m0) * E;
       pb = (const char*)(Z + n0);
-      nb = (count * a.ds_ld - n0) * 2;
+      nb = (count * a.ds_ld - n0) * E;
     }
   };
   // along k: the lane's first element's k in a tile, the same for each second load
@@ -172,9 +175,9 @@ __global__ __launch_bounds__(WM* WN * 64) void ce_tile_kernel(CeArgs a, CePiece 
 #pragma unroll
   for (int t = 0; t < 2; ++t) {
     int r, c;
-    inner_place((wave + t * C::kWaves) % C::kALoads, lane, r, c);
+    inner_place<T>((wave + t * C::kWaves) % C::kALoads, lane, r, c);
     ka[t] = (uint32_t)c;
-    inner_place((wave + t * C::kWaves) % C::kBLoads, lane, r, c);
+    inner_place<T>((wave + t * C::kWaves) % C::kBLoads, lane, r, c);
     kb[t] = (uint32_t)c;
   }
 
@@ -227,6 +230,7 @@ __global__ __launch_bounds__(WM* WN * 64) void ce_tile_kernel(CeArgs a, CePiece 
   for (int t = 0; t < 4; ++t) {
     const uint32_t inner = fr * 128 + (((t * 2 + fh) ^ ((lane >> 1) & 7)) * 16);
     auto outer = [&](int width, int at) {
+      if (!C::kBf16) return (uint32_t)((fh * 4 * width + at + fr) * 4);
       const int k = fh * 8 + ((lane & 15) >> 2);
       const int turn = width >= 128 ? (k & 3) << 1 : width == 64 ? ((k >> 1) & 1) << 1 : 0;
       return (uint32_t)(k * width * 2 + (((at >> 4) + ((lane >> 4) & 1)) ^ turn) * 32 + (lane & 3) * 8);
@@ -234,18 +238,37 @@ __global__ __launch_bounds__(WM* WN * 64) void ce_tile_kernel(CeArgs a, CePiece 
     pa_lds[t] = lds0 + (C::kAOuter ? outer(BM, wm + t * 32) : wm * 128 + inner);
     pb_lds[t] = lds0 + C::kABytes + (C::kBOuter ? outer(BN, wn + t * 32) : wn * 128 + inner);
   }
-  auto frag_inner = [](uint32_t at) { return *(const ARCS_LDS bf16x8*)(uintptr_t)at; };
+  // A fragment is 16 bytes: 8 k of bfloat16 for one 32 x 32 x 16 product, or 4 k of
+  // float32 for four of 32 x 32 x 2.
+  auto frag_inner = [](uint32_t at) { return *(const ARCS_LDS u32x4*)(uintptr_t)at; };
   auto frag_outer = [](uint32_t at, int width) {
-    const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((ARCS_LDS s16x4*)(uintptr_t)at);
-    const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((ARCS_LDS s16x4*)(uintptr_t)(at + 8 * width));
-    return __builtin_bit_cast(bf16x8, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
+    if constexpr (C::kBf16) {
+      const s16x4 x = __builtin_amdgcn_ds_read_tr16_b64_v4i16((ARCS_LDS s16x4*)(uintptr_t)at);
+      const s16x4 y = __builtin_amdgcn_ds_read_tr16_b64_v4i16((ARCS_LDS s16x4*)(uintptr_t)(at + 8 * width));
+      return __builtin_bit_cast(u32x4, __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7));
+    } else {
+      u32x4 f;
+#pragma unroll
+      for (int e = 0; e < 4; ++e) f[e] = *(const ARCS_LDS uint32_t*)(uintptr_t)(at + e * width * 4);
+      return f;
+    }
+  };
+  auto product = [](u32x4 x, u32x4 y, f32x16 c) {
+    if constexpr (C::kBf16) {
+      return __builtin_amdgcn_mfma_f32_32x32x16_bf16(__builtin_bit_cast(bf16x8, x), __builtin_bit_cast(bf16x8, y), c, 0, 0, 0);
+    } else {
+#pragma unroll
+      for (int e = 0; e < 4; ++e)
+        c = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(x[e]), __uint_as_float(y[e]), c, 0, 0, 0);
+      return c;
+    }
   };
 
   // Fragments of step ks + 1 are read while step ks multiplies.  The last step of
   // a tile reads from the next one: there the workgroup meets, once a tile, the
   // next tile has landed and this one's buffer is filled again.
   f32x16 acc[MT][NT];
-  bf16x8 fa[2][MT], fb[2][NT];
+  u32x4 fa[2][MT], fb[2][NT];
   auto read = [&](int kt, int ks) {
     const uint32_t at = (uint32_t)(kt % S) * C::kStage;
 #pragma unroll
@@ -260,7 +283,7 @@ __global__ __launch_bounds__(WM* WN * 64) void ce_tile_kernel(CeArgs a, CePiece 
     for (int i = 0; i < MT; ++i)
 #pragma unroll
       for (int j = 0; j < NT; ++j)
-        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[ks & 1][i], fb[ks & 1][j], acc[i][j], 0, 0, 0);
+        acc[i][j] = product(fa[ks & 1][i], fb[ks & 1][j], acc[i][j]);
     __builtin_amdgcn_sched_barrier(0);
   };
 
@@ -291,8 +314,7 @@ __global__ __launch_bounds__(WM* WN * 64) void ce_tile_kernel(CeArgs a, CePiece 
       constexpr int kProducts = MT * NT, kEach = (C::kPer + kProducts - 1) / kProducts;
 #pragma unroll
       for (int p = 0; p < kProducts; ++p) {
-        acc[p / NT][p % NT] =
-            __builtin_amdgcn_mfma_f32_32x32x16_bf16(fa[1][p / NT], fb[1][p % NT], acc[p / NT][p % NT], 0, 0, 0);
+        acc[p / NT][p % NT] = product(fa[1][p / NT], fb[1][p % NT], acc[p / NT][p % NT]);
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int l = p * kEach; l < (p + 1) * kEach && l < C::kPer; ++l) issue_one(from, l);
@@ -328,9 +350,9 @@ __global__ __launch_bounds__(WM* WN * 64) void ce_tile_kernel(CeArgs a, CePiece 
         row.a = 1.0f;
         if (n < N && !direct) row = a.rows[n];
         if (n < N && direct) {
-          float T;
-          const int kind = ce_row_kind(a, n, row.target, T);
-          row.a = kLog2e / (kind == 0 ? T : 1.0f);
+          float temperature;
+          const int kind = ce_row_kind(a, n, row.target, temperature);
+          row.a = kLog2e / (kind == 0 ? temperature : 1.0f);
           if (kind != 0) row.target = -1;
         }
         if (ragged) {
@@ -384,6 +406,41 @@ __global__ __launch_bounds__(WM* WN * 64) void ce_tile_kernel(CeArgs a, CePiece 
             f32x4 v = {acc[i][j][q * 4], acc[i][j][q * 4 + 1], acc[i][j][q * 4 + 2], acc[i][j][q * 4 + 3]};
             if (!pc.first) v += *out;
             *out = v;
+          }
+      }
+    }
+    if (!C::kBf16 && (MODE == kCeDs || MODE == kCeDweight)) {
+      const float g = MODE == kCeDweight ? a.head->gmax : 0.0f;
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        const int64_t n = en0 + wn + j * 32 + fr;
+        if (n >= N) continue;
+        CeRow row;
+        row.target = -1;
+        row.a = row.c = row.lse2 = 0.0f;
+        if (MODE == kCeDs) row = a.rows[n];
+        const int64_t to_target = (int64_t)row.target - pc.v0 - em0 - mw;
+        const int target = to_target >= 0 && to_target < MT * 32 ? (int)to_target : -1;
+        float* to = MODE == kCeDs ? (float*)a.ds + n * a.ds_ld + em0 + mw : (float*)a.out_dweight + (pc.v0 + n) * a.D + em0 + mw;
+#pragma unroll
+        for (int i = 0; i < MT; ++i)
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            f32x4 out;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int id = row_of(i, q * 4 + e);
+              float v = acc[i][j][q * 4 + e];
+              if (MODE == kCeDs) {
+                v = exp2_fast(fmaf(v, row.a, -row.lse2));
+                v = id == target ? v - 1.0f : v;
+                v = id < m_left ? v * row.c : 0.0f;
+              } else {
+                v *= g;
+              }
+              out[e] = v;
+            }
+            if (MODE == kCeDs || row_of(i, q * 4) < m_left) *(f32x4*)(to + row_of(i, q * 4)) = out;
           }
       }
     }
@@ -445,91 +502,103 @@ __global__ __launch_bounds__(WM* WN * 64) void ce_tile_kernel(CeArgs a, CePiece 
 
 // dhidden rows: the parts of each tile added up in the workers' order; zeros for
 // rows that are not listed.
+template <typename T, int BM>
 __global__ __launch_bounds__(256) void ce_dhidden_parts_kernel(CeArgs a, int BN) {
-  constexpr int BM = 256;
   const int64_t n = blockIdx.x;
-  const int m = blockIdx.y * 4 + (threadIdx.x >> 6), lane = threadIdx.x & 63;  // a wave takes one tile's columns
-  const int64_t d = m * BM + lane * 4;
+  const int64_t d = (int64_t)blockIdx.y * 1024 + threadIdx.x * 4;
   if (d >= a.D) return;
-  const int i = a.place[n];
+  const int i = a.place[n], m = (int)(d / BM);
   const int mt = (int)((a.D + BM - 1) / BM), nt = (a.head->count + BN - 1) / BN, all = mt * nt;
   f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
   if (i >= 0) {
     const int job = ce_tile_index(m, i / BN, mt, nt);
     const int lo = (int)((int64_t)job * a.workers / all), hi = (int)(((int64_t)(job + 1) * a.workers + all - 1) / all);
-    const float* p = a.slab + ((int64_t)job * BN + i % BN) * BM + lane * 4;
+    const float* p = a.slab + ((int64_t)job * BN + i % BN) * BM + d % BM;
 #pragma unroll 4
     for (int w = lo; w < hi; ++w) v += *(const f32x4*)(p + (int64_t)w * (BN * BM));
     v *= a.head->gmax;
   }
-  bf16x4 out;
+  if constexpr (sizeof(T) == 2) {
+    bf16x4 out;
 #pragma unroll
-  for (int e = 0; e < 4; ++e) out[e] = (__bf16)v[e];
-  *(bf16x4*)((__bf16*)a.out_dhidden + n * a.D + d) = out;
+    for (int e = 0; e < 4; ++e) out[e] = (__bf16)v[e];
+    *(bf16x4*)((__bf16*)a.out_dhidden + n * a.D + d) = out;
+  } else {
+    *(f32x4*)((float*)a.out_dhidden + n * a.D + d) = v;
+  }
 }
 
 // The hidden states of the listed rows, one after the other.
+template <typename T>
 __global__ __launch_bounds__(256) void ce_copy_kernel(CeArgs a) {
   const int64_t i = blockIdx.x;
   if (i >= a.head->count) return;
-  const u32x4* from = (const u32x4*)((const uint16_t*)a.hidden + (int64_t)a.rows[i].row * a.hidden_stride);
-  u32x4* to = (u32x4*)((uint16_t*)a.hc + i * a.D);
-  for (int64_t c = threadIdx.x; c < a.D / 8; c += 256) to[c] = from[c];
+  const u32x4* from = (const u32x4*)((const T*)a.hidden + (int64_t)a.rows[i].row * a.hidden_stride);
+  u32x4* to = (u32x4*)((T*)a.hc + i * a.D);
+  for (int64_t c = threadIdx.x; c < a.D * (int64_t)sizeof(T) / 16; c += 256) to[c] = from[c];
 }
 
 namespace {
 
 int64_t tiles(int64_t n, int64_t t) { return (n + t - 1) / t; }
 
-template <int MODE, int WM, int WN, int MT, int NT, int S>
+template <typename T, int MODE, int WM, int WN, int MT, int NT, int S>
 void launch_tile(const CeArgs& a, const CePiece& pc, hipStream_t stream) {
-  using C = CeTile<MODE, WM, WN, MT, NT, S>;
+  using C = CeTile<T, MODE, WM, WN, MT, NT, S>;
   const int64_t m = C::kLogits ? pc.len : a.D, n = MODE == kCeDweight ? pc.len : a.N;
   // as many workgroups as the compute units hold (by LDS), at most
   constexpr int64_t kMost = 256 * (163840 / C::kLds);
   const int64_t all = tiles(m, C::BM) * tiles(n, C::BN);
   const int64_t blocks = MODE == kCeDhidden ? a.workers : all < kMost ? tiles(all, 8) * 8 : kMost;
-  hipLaunchKernelGGL((ce_tile_kernel<MODE, WM, WN, MT, NT, S>), dim3((unsigned)blocks), dim3(C::kThreads), 0, stream, a, pc);
+  hipLaunchKernelGGL((ce_tile_kernel<T, MODE, WM, WN, MT, NT, S>), dim3((unsigned)blocks), dim3(C::kThreads), 0, stream, a, pc);
 }
 
-template <int MODE>
+// The tile of a call: by its rows, so that few rows are not padded to many.
+//   bfloat16  32 x 256 (32 x 128 where that leaves compute units without a tile), 64 x 256, 128 x 256, 256 x 256
+//   float32   the first three, and 128 x 128 for more rows: their products take so
+//             long that smaller tiles, two workgroups a compute unit, cost no time in
+//             loads and spread over the card more evenly
+template <typename T, int MODE>
 void launch_rows(const CeArgs& a, const CePiece& pc, hipStream_t stream) {
-  if constexpr (MODE != kCeDweight) {
-    const int rows = ce_rows_of_tile(a.N);
-    // 128 of the vocabulary a tile where 256 would leave compute units without one
-    if constexpr (MODE != kCeDhidden)
-      if (rows == 32 && tiles(pc.len, 256) < 256) return launch_tile<MODE, 4, 1, 1, 1, 4>(a, pc, stream);
-    if (rows == 32) return launch_tile<MODE, 8, 1, 1, 1, 4>(a, pc, stream);
-    if (rows == 64) return launch_tile<MODE, 4, 2, 2, 1, 3>(a, pc, stream);
-    if (rows == 128) return launch_tile<MODE, 4, 2, 2, 2, 3>(a, pc, stream);
+  const int rows = ce_rows_of_tile(a.N, sizeof(T) == 2);
+  if constexpr (sizeof(T) == 2) {
+    if constexpr (MODE == kCeDweight) return launch_tile<T, MODE, 2, 4, 4, 2, 2>(a, pc, stream);
+    else if (rows == 256) return launch_tile<T, MODE, 2, 4, 4, 2, 2>(a, pc, stream);
+    else if (rows == 128) return launch_tile<T, MODE, 4, 2, 2, 2, 3>(a, pc, stream);
+  } else {
+    if constexpr (MODE == kCeDweight) return launch_tile<T, MODE, 2, 2, 2, 2, 2>(a, pc, stream);
+    else if (rows == 128) return launch_tile<T, MODE, 2, 2, 2, 2, 2>(a, pc, stream);
   }
-  launch_tile<MODE, 2, 4, 4, 2, 2>(a, pc, stream);
+  if constexpr (MODE != kCeDweight) {
+    if (rows == 64) return launch_tile<T, MODE, 4, 2, 2, 1, 3>(a, pc, stream);
+    if constexpr (MODE != kCeDhidden)
+      if (tiles(pc.len, 256) < 256) return launch_tile<T, MODE, 4, 1, 1, 1, 4>(a, pc, stream);
+    launch_tile<T, MODE, 8, 1, 1, 1, 4>(a, pc, stream);
+  }
 }
 
-}  // namespace
-
-bool cross_entropy_matrix_path(const CeArgs& a, int dtype, bool backward) {
-  if (dtype != ARCS_DTYPE_BF16 || a.D % 8 != 0) return false;
-  const int64_t most = int64_t(1) << 22;  // a tile's rows lie within 2^31 bytes
-  if (a.hidden_stride % 8 != 0 || a.weight_stride % 8 != 0 || a.weight_stride >= most) return false;
-  if (((uintptr_t)a.hidden | (uintptr_t)a.weight | (uintptr_t)a.out_dweight | (uintptr_t)a.out_dhidden) & 15u) return false;
-  return true;
+// Slices of a row in STATS: the waves along m of its tiles.
+int64_t slices_of(int64_t V, int64_t N, bool bf16) {
+  const int rows = ce_rows_of_tile(N, bf16);
+  if (rows == 32) return tiles(V, 256) < 256 ? tiles(V, 128) * 4 : tiles(V, 256) * 8;
+  if (rows == 64) return tiles(V, 256) * 4;
+  if (rows == 128) return bf16 ? tiles(V, 256) * 4 : tiles(V, 128) * 2;
+  return tiles(V, 256) * 2;
 }
 
-hipError_t launch_cross_entropy_matrix(const CeArgs& args, bool backward, hipStream_t stream) {
-  CeArgs a = args;
+template <typename T>
+hipError_t launch_matrix(CeArgs a, bool backward, hipStream_t stream) {
+  constexpr bool kBf16 = sizeof(T) == 2;
   CePiece pc = {0, a.V, 1, 0, 0};
   // forward: rows are read where they are if one descriptor reaches them all
-  pc.gather = !backward && (unsigned __int128)a.N * (unsigned __int128)a.hidden_stride * 2 < kBufMost;
+  pc.gather = !backward && (unsigned __int128)a.N * (unsigned __int128)a.hidden_stride * sizeof(T) < kBufMost;
   // a tile's worth of rows or less: a list would save no product
   pc.direct = pc.gather && a.N <= 256;
   if (!pc.direct) launch_cross_entropy_prep(a, backward, stream);
-  if (!pc.gather) hipLaunchKernelGGL(ce_copy_kernel, dim3((unsigned)a.N), dim3(256), 0, stream, a);
+  if (!pc.gather) hipLaunchKernelGGL(ce_copy_kernel<T>, dim3((unsigned)a.N), dim3(256), 0, stream, a);
   if (!backward) {
-    const int rows = ce_rows_of_tile(a.N);
-    a.slices = rows == 32 ? tiles(a.V, tiles(a.V, 256) < 256 ? 128 : 256) * (tiles(a.V, 256) < 256 ? 4 : 8)
-                          : tiles(a.V, 256) * (rows == 256 ? 2 : 4);
-    launch_rows<kCeStats>(a, pc, stream);
+    a.slices = slices_of(a.V, a.N, kBf16);
+    launch_rows<T, kCeStats>(a, pc, stream);
     launch_cross_entropy_combine(a, pc.direct, stream);
     return hipGetLastError();
   }
@@ -537,14 +606,32 @@ hipError_t launch_cross_entropy_matrix(const CeArgs& args, bool backward, hipStr
     pc.v0 = v0;
     pc.len = a.V - v0 < a.ds_ld ? a.V - v0 : a.ds_ld;
     pc.first = v0 == 0;
-    launch_rows<kCeDs>(a, pc, stream);
-    if (a.out_dhidden) launch_rows<kCeDhidden>(a, pc, stream);
-    if (a.out_dweight) launch_rows<kCeDweight>(a, pc, stream);
+    launch_rows<T, kCeDs>(a, pc, stream);
+    if (a.out_dhidden) launch_rows<T, kCeDhidden>(a, pc, stream);
+    if (a.out_dweight) launch_rows<T, kCeDweight>(a, pc, stream);
   }
-  if (a.out_dhidden)
-    hipLaunchKernelGGL(ce_dhidden_parts_kernel, dim3((unsigned)a.N, (unsigned)tiles(a.D, 1024)), dim3(256), 0, stream, a,
-                       ce_rows_of_tile(a.N));
+  if (a.out_dhidden) {
+    const dim3 grid((unsigned)a.N, (unsigned)tiles(a.D, 1024));
+    const int rows = ce_rows_of_tile(a.N, kBf16);
+    if (ce_columns_of_tile(a.N, kBf16) == 128)
+      hipLaunchKernelGGL((ce_dhidden_parts_kernel<T, 128>), grid, dim3(256), 0, stream, a, rows);
+    else
+      hipLaunchKernelGGL((ce_dhidden_parts_kernel<T, 256>), grid, dim3(256), 0, stream, a, rows);
+  }
   return hipGetLastError();
+}
+
+}  // namespace
+
+bool cross_entropy_matrix_path(const CeArgs& a, int dtype) {
+  // rows on the 16-byte grid, and a tile's rows within 2^31 bytes
+  const int64_t each = dtype == ARCS_DTYPE_BF16 ? 8 : 4, most = int64_t(1) << (dtype == ARCS_DTYPE_BF16 ? 22 : 21);
+  if (a.D % each != 0 || a.hidden_stride % each != 0 || a.weight_stride % each != 0 || a.weight_stride >= most) return false;
+  return (((uintptr_t)a.hidden | (uintptr_t)a.weight | (uintptr_t)a.out_dweight | (uintptr_t)a.out_dhidden) & 15u) == 0;
+}
+
+hipError_t launch_cross_entropy_matrix(const CeArgs& a, int dtype, bool backward, hipStream_t stream) {
+  return dtype == ARCS_DTYPE_BF16 ? launch_matrix<__bf16>(a, backward, stream) : launch_matrix<float>(a, backward, stream);
 }
 
 }  // namespace arcs

@@ -34,6 +34,7 @@ __device__ __forceinline__ u32x4 buffer_of(const void* p, int64_t bytes) {
 // vector instruction has just written five: the first load of a descriptor has them.
 template <bool FIRST = true>
 __device__ __forceinline__ void load_to_lds(uint32_t to, uint32_t off, u32x4 from) {
+  to = __builtin_amdgcn_readfirstlane(to);
   if (FIRST)
     asm volatile("s_mov_b32 m0, %0\n\ts_nop 4\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" ::"s"(to), "v"(off), "s"(from)
                  : "memory", "m0");

@@ -111,9 +111,10 @@ struct W4 {
     }
     // 16 bytes a lane of each tile: k 128 step on
     __device__ __forceinline__ void load(u32x4 (&w)[RT], int step) const {
-      const int64_t at = (int64_t)step * (kW4Step / 2);
+      // a part's last step can begin past the end of the last row: nothing is left there
+      const int64_t at = (int64_t)step * (kW4Step / 2), left = bytes > at ? bytes - at : 0;
       const __amdgpu_buffer_rsrc_t d = __builtin_amdgcn_make_buffer_rsrc(
-          (void*)(base + at), (short)0, (int)(bytes - at < (int64_t)kBufMost ? bytes - at : (int64_t)kBufMost), 0x00020000);
+          (void*)(base + at), (short)0, (int)(left < (int64_t)kBufMost ? left : (int64_t)kBufMost), 0x00020000);
 #pragma unroll
       for (int t = 0; t < RT; ++t) w[t] = __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(d, off[t], 0, 0));
     }
@@ -431,6 +432,7 @@ __global__ __launch_bounds__(WB* WV * 64, MT == 2 ? 3 : 2) void w4_batch_kernel(
     }
     if (part + 1 < parts) scales.store(s_scale[(part + 1) & 1]);
   }
+  wait_loads<0>();
   w4_write<MT, RT, OF32>(a, total, b0 + wb * MT * 16, v0, r, j);
 }
 

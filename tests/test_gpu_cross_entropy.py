@@ -395,3 +395,99 @@ def test_decode_and_train_run(arcs):
     dh, dw = arcs.linear_cross_entropy_backward(hidden, weight, ids, lse, advantage, temperature=T)
     s = dict(hidden=hidden, weight=weight, targets=ids, temperature=T)
     check_gradients(dh, dw, reference(s, advantage), V, "bf16", True)
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_rows_far_apart(arcs, dtype):
+    """Offsets past 32 bits: hidden rows 8 MiB apart (2.5 GB in all, read through a
+    copy), and head rows 4 MiB apart (5 GB)."""
+    import torch
+    N, V, D = 300, 1230, 64
+    s, g = make(N, V, D, dtype, 41, True, 0.2, True)
+    want, lse = arcs.linear_cross_entropy(**s)
+    wh, ww = arcs.linear_cross_entropy_backward(s["hidden"], s["weight"], s["targets"], lse, g,
+                                                temperature=s["temperature"])
+    dt = s["hidden"].dtype
+    step_h, step_w = (8 << 20) // dt.itemsize, (4 << 20) // dt.itemsize - 64
+    far_h = torch.empty(N * step_h, dtype=dt, device="cuda").as_strided((N, D), (step_h, 1))
+    far_w = torch.empty(V * step_w, dtype=dt, device="cuda").as_strided((V, D), (step_w, 1))
+    far_h.copy_(s["hidden"])
+    far_w.copy_(s["weight"])
+    got, lse2 = arcs.linear_cross_entropy(far_h, far_w, s["targets"], temperature=s["temperature"])
+    dh, dw = arcs.linear_cross_entropy_backward(far_h, far_w, s["targets"], lse2, g, temperature=s["temperature"])
+    assert torch.equal(got, want) and torch.equal(dh, wh) and torch.equal(dw, ww)
+
+
+def test_many_pieces_and_tiles(arcs):
+    """Enough rows that the vocabulary is taken in several pieces, and enough tiles
+    that a workgroup takes more than one; rows checked against 64 bits on the GPU."""
+    import torch
+    N, V, D = 12000, 20000, 128
+    gen = torch.Generator(device="cuda").manual_seed(2)
+    h = torch.randn(N, D, generator=gen, device="cuda").to(torch.bfloat16)
+    w = (torch.randn(V, D, generator=gen, device="cuda") * 0.2).to(torch.bfloat16)
+    t = torch.randint(0, V, (N,), generator=gen, device="cuda").to(torch.int32)
+    t[::7] = IGNORE
+    g = torch.full((N,), 1.0 / N, device="cuda")
+    loss, lse = arcs.linear_cross_entropy(h, w, t)
+    on = t != IGNORE
+    rows = torch.nonzero(on)[:, 0]
+    z = h[rows].double() @ w.double().T
+    want_lse = torch.logsumexp(z, 1)
+    tr = t[rows].long()
+    # the bound of a logit, D = 128 terms of size |h| |w| (about 11 * 2.3), and its logarithm
+    assert (lse[rows].double() - want_lse).abs().max() < 2e-5
+    assert (loss[rows].double() - (want_lse - z.gather(1, tr[:, None])[:, 0])).abs().max() < 4e-5
+    assert (loss[~on] == 0).all() and (lse[~on] == 0).all()
+    dh, dw = arcs.linear_cross_entropy_backward(h, w, t, lse, g)
+    p = torch.exp(z - want_lse[:, None])
+    p.scatter_add_(1, tr[:, None], torch.full((len(rows), 1), -1.0, dtype=torch.float64, device="cuda"))
+    p /= N
+    for got, ref in ((dh[rows], p @ w.double()), (dw, p.T.contiguous() @ h[rows].double())):
+        # dz is rounded to bfloat16 (2^-9 on average at most) and so is the result
+        assert torch.linalg.norm(got.double() - ref) <= 2.0 ** -8 * torch.linalg.norm(ref)
+    assert (dh[~on] == 0).all()
+
+
+def test_calls_on_two_streams_at_once(arcs):
+    """Calls that overlap, each with a workspace of its own, do not meet."""
+    import torch
+    cases = [make(900, 3000, 256, "bf16", 50 + k, True, 0.2, True) for k in range(2)]
+    want = []
+    for s, g in cases:
+        loss, lse = arcs.linear_cross_entropy(**s)
+        want.append((loss, *arcs.linear_cross_entropy_backward(s["hidden"], s["weight"], s["targets"], lse, g,
+                                                               temperature=s["temperature"])))
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in cases]
+    got = [[], []]
+    for _ in range(4):
+        for k, (s, g) in enumerate(cases):
+            loss, lse = arcs.linear_cross_entropy(**s, stream=streams[k])
+            got[k].append((loss, *arcs.linear_cross_entropy_backward(s["hidden"], s["weight"], s["targets"], lse, g,
+                                                                     temperature=s["temperature"], stream=streams[k])))
+    torch.cuda.synchronize()
+    for k in range(2):
+        for one in got[k]:
+            assert all(torch.equal(x, y) for x, y in zip(one, want[k]))
+
+
+def test_binding_refuses(arcs):
+    """Mistakes in tensors raise before anything is launched."""
+    import torch
+    s, g = make(6, 40, 64, "bf16", 1)
+    h, w, t = s["hidden"], s["weight"], s["targets"]
+    for bad in (dict(targets=t.long()), dict(targets=t[:5]), dict(weight=w.float()), dict(weight=w[:, :32]),
+                dict(hidden=h.t()), dict(temperature=torch.ones(5, device="cuda")), dict(ignore_index=2**31),
+                dict(out_loss=torch.empty(6, device="cuda", dtype=torch.float64)),
+                dict(workspace=torch.empty(1 << 20, dtype=torch.uint8))):
+        with pytest.raises(ValueError):
+            arcs.linear_cross_entropy(**{**s, **bad})
+    with pytest.raises(TypeError):
+        arcs.linear_cross_entropy(h.half(), w.half(), t)
+    with pytest.raises(arcs.ArcsError):
+        arcs.linear_cross_entropy(h, w, t, workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(arcs.ArcsError):
+        arcs.linear_cross_entropy_backward(h, w, t, g, g, want_hidden=False, want_weight=False)
+    with pytest.raises(ValueError):
+        arcs.linear_cross_entropy_backward(h, w, t, g, g, out_dweight=torch.empty(40, 64, device="cuda"))

@@ -154,3 +154,49 @@ def test_logits_feed_the_sampler(arcs):
     assert torch.equal(top[:, 0], ids)
     want = torch.log_softmax(logits.double(), dim=1).gather(1, top.long())
     assert (lp.double() - want).abs().max() < 1e-5
+
+
+@pytest.mark.parametrize("B", [3, 40])
+def test_rows_far_apart(arcs, B):
+    """Offsets past 32 bits: weight rows 2 MiB apart (4.6 GB) and logit rows 2^30
+    elements apart (B = 3: 6 GB)."""
+    import torch
+    V, D, G = 2200, 320, 64
+    host, dev = make(B, V, D, G, True, "bf16", seed=19)
+    want = arcs.w4_logits(dev["hidden"], dev["qweight"], dev["scales"], G, zeros=dev["zeros"])
+    far = torch.empty(V << 21, dtype=torch.uint8, device="cuda").as_strided((V, D // 2), (1 << 21, 1))
+    far.copy_(dev["qweight"])
+    width = 1 << 30 if B == 3 else V
+    out = torch.empty(B * width, dtype=torch.bfloat16, device="cuda").as_strided((B, V), (width, 1))
+    got = arcs.w4_logits(dev["hidden"], far, dev["scales"], G, zeros=dev["zeros"], out=out)
+    assert torch.equal(got, want)
+
+
+@pytest.mark.parametrize("B,D,G", [(20, 32, 32), (70, 64, 64), (200, 128, 128), (33, 96, 32), (130, 320, 64)])
+def test_the_last_weight_row_ends_the_allocation(arcs, B, D, G):
+    """Hidden sizes that end inside a part of 256 k, and a vocabulary that ends
+    inside a tile: what lies past the rows meets zeros."""
+    import torch
+    V = 129
+    host, dev = make(B, V, D, G, True, "f32", seed=D)
+    got = arcs.w4_logits(dev["hidden"], dev["qweight"], dev["scales"], G, zeros=dev["zeros"], out_dtype=torch.float32)
+    check(got, host, G, "f32")
+
+
+def test_binding_refuses(arcs):
+    """Mistakes in tensors raise before anything is launched."""
+    import torch
+    host, dev = make(20, 64, 256, 64, True, "bf16", seed=1)
+    h, q, s, z = dev["hidden"], dev["qweight"], dev["scales"], dev["zeros"]
+    for args, kw in (((h.float(), q, s, 64), {}), ((h, q[:, :64], s, 64), {}), ((h, q, s, 32), {}),
+                     ((h, q.to(torch.int32), s, 64), {}), ((h, q, s, 64), dict(zeros=z[:32])),
+                     ((h, q, s, 64), dict(out=torch.empty(20, 63, device="cuda"))),
+                     ((h, q, s, 64), dict(out=torch.empty(20, 64, device="cuda"), out_dtype=torch.bfloat16))):
+        with pytest.raises(ValueError):
+            arcs.w4_logits(*args, **kw)
+    with pytest.raises(TypeError):
+        arcs.w4_logits(h, q, s.half(), 64)
+    with pytest.raises(arcs.ArcsError):
+        arcs.w4_logits(h, q, s, 64, workspace=torch.empty(256, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(arcs.ArcsError):
+        arcs.w4_logits(h[:, 1:225].as_strided((20, 192), (256, 1)), q[:, :96], s[:, :3], 64)
