@@ -11,6 +11,7 @@ from __future__ import annotations
 
 import contextlib
 import ctypes
+import functools
 import os
 from typing import Optional
 
@@ -166,10 +167,12 @@ def long_history_workspace_bytes(B: int, V: int) -> int:
     return int(library().arcs_long_history_workspace_bytes(int(B), int(V)))
 
 
+@functools.lru_cache(maxsize=256)
 def w4_logits_workspace_bytes(B: int, D: int, group_size: int) -> int:
     return int(library().arcs_w4_logits_workspace_bytes(int(B), int(D), int(group_size)))
 
 
+@functools.lru_cache(maxsize=256)
 def linear_cross_entropy_workspace_bytes(N: int, V: int, D: int, dtype: int, backward: bool = False) -> int:
     return int(library().arcs_linear_cross_entropy_workspace_bytes(int(N), int(V), int(D), int(dtype),
                                                                    1 if backward else 0))
@@ -522,11 +525,12 @@ def _work_on(device, stream):
 
 def _matrix(t, name: str, dtype, rows: int, cols: int, device):
     """A device matrix with unit column stride; returns its row stride."""
-    if t.dtype != dtype or t.dim() != 2 or t.shape[0] != rows or t.shape[1] != cols or t.device != device:
+    if t.dtype != dtype or t.shape != (rows, cols) or t.device != device:
         raise ValueError(f"{name} must be a [{rows}, {cols}] {dtype} tensor on {device}")
-    if t.stride(1) != 1 and cols > 1:
+    row, column = t.stride()
+    if column != 1 and cols > 1:
         raise ValueError(f"{name} rows must be contiguous (stride(1) == 1)")
-    return cols if rows == 1 else t.stride(0)
+    return cols if rows == 1 else row
 
 
 def _vector(t, name: str, dtype, n: int, device):
@@ -534,12 +538,13 @@ def _vector(t, name: str, dtype, n: int, device):
         raise ValueError(f"{name} must be a contiguous {dtype} tensor of {n} elements on {device}")
 
 
-def _hidden_shape(hidden, what: str = "hidden"):
+def _hidden_shape(hidden):
     if not hidden.is_cuda:
-        raise ValueError(f"{what} must be a device tensor")
+        raise ValueError("hidden must be a device tensor")
     if hidden.dim() != 2:
-        raise ValueError(f"{what} must be [rows, D]")
-    return hidden.shape[0], hidden.shape[1], hidden.device
+        raise ValueError("hidden must be [rows, D]")
+    rows, D = hidden.shape
+    return rows, D, hidden.device
 
 
 def w4_logits(hidden, qweight, scales, group_size: int, zeros=None, out=None, out_dtype=None, workspace=None,

@@ -431,7 +431,7 @@ const char* arcs_status_string(int code) {
     case ARCS_ERR_BAD_VOCAB: return "vocabulary size V must be in [1, 2^31-1]";
     case ARCS_ERR_BAD_STRIDE: return "row_stride must be >= V";
     case ARCS_ERR_BAD_DTYPE: return "dtype must be ARCS_DTYPE_BF16 or ARCS_DTYPE_F32";
-    case ARCS_ERR_WORKSPACE_TOO_SMALL: return "workspace smaller than arcs_sample_workspace_bytes()";
+    case ARCS_ERR_WORKSPACE_TOO_SMALL: return "workspace smaller than the call's *_workspace_bytes()";
     case ARCS_ERR_BAD_BUDGET: return "budget outside [0, 4096]";
     case ARCS_ERR_BAD_DRY: return "DRY breakers: NULL with n_breakers > 0, or n_breakers outside [0, 64]";
     case ARCS_ERR_SCRATCH_TOO_SMALL:
@@ -439,7 +439,7 @@ const char* arcs_status_string(int code) {
     case ARCS_ERR_BAD_HIDDEN: return "hidden size D must be in [1, ARCS_MAX_HIDDEN]";
     case ARCS_ERR_BAD_GROUP: return "group_size must be 32, 64 or 128 and divide D";
     case ARCS_ERR_LAUNCH: return "kernel launch failed";
-    case ARCS_ERR_MISALIGNED: return "logits pointer not aligned to its element size";
+    case ARCS_ERR_MISALIGNED: return "an array or its rows are not aligned as the call asks for";
     case ARCS_ERR_BAD_HISTORY: return "hist_ids and hist_offsets must both be NULL or both be set";
     case ARCS_ERR_BAD_TOP_N: return "n must be in [1, ARCS_MAX_TOP_LOGPROBS]";
     case ARCS_ERR_BAD_CAPACITY: return "ring capacity must be >= 1 and capacity * B must fit int64";

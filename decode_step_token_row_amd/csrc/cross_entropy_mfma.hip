@@ -1,15 +1,27 @@
-// Linear cross entropy on the bfloat16 matrix instruction.
+// Linear cross entropy on the matrix instructions (bfloat16 and float32 rows on
+// the 16-byte grid).
 //
 // One tile kernel runs the four products of the general kernel (STATS, DS,
-// DHIDDEN, DWEIGHT) on rows that are 16-byte aligned: C[m, n] = sum_k A[m, k]
-// B[n, k], 64 k at a time.  Tiles go from memory to LDS by the buffer loads
-// that write LDS directly, S tiles deep, one barrier a tile.  An operand whose
-// rows run along k is read back 16 bytes a lane; one whose rows run along m or
-// n (the head in DHIDDEN, both operands in DWEIGHT) through the transposing
-// LDS read, so no operand is stored twice.  The load writes LDS in lane order,
-// so bank conflicts are avoided by permuting the lanes' global addresses:
+// DHIDDEN, DWEIGHT): C[m, n] = sum_k A[m, k] B[n, k], 128 bytes of k at a time.
+// Tiles go from memory to LDS by the buffer loads that write LDS directly, S
+// tiles deep, one barrier a tile.  An operand whose rows run along k is read
+// back 16 bytes a lane; one whose rows run along m or n (the head in DHIDDEN,
+// both operands in DWEIGHT) through the transposing LDS read (bfloat16) or word
+// by word (float32), so no operand is stored twice.  The load writes LDS in lane
+// order, so bank conflicts (none are counted) are avoided by permuting the lanes'
+// global addresses:
 //   along k: a row's 128 bytes are 8 chunks, chunk c of row r at c ^ (r / 2 % 8);
 //   along m: a row's 32-byte chunks, chunk q of row k at q ^ 2 (k % 4).
+//
+// What bounds it: the products.  4,096 rows x 129,280 x 4,096 take 3.37 ms forward
+// (1,290 TFLOP/s; a large library product reaches 1,445 here), 256 x 256 tiles of
+// eight waves of 128 x 64.  Steps, at that size: the plain loop 3.75 ms;
+// fragments read one k step ahead of the products, across the barrier too,
+// 3.58; the next tile's loads between the products instead of before them, 3.52;
+// workgroups that stay and load their next tile before they write the last one
+// out, 3.37.  Slower: four waves of 128 x 128 (4.0), the head three tiles deep
+// (3.67).  Few rows are bound by reading the head: one row x 32,000 x 2,048 takes
+// 34 us with its launches (131 MB, 26 us at the rate of a copy).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -105,7 +117,7 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void ce_tile_kernel(CeArgs a, CePie
 
   // The tile that is loaded: descriptors at its first k, and the lanes' offsets.
   int64_t m0, n0;
-  int nk;
+  int nk, shift = 0;
   const char *pa, *pb;
   int64_t na, nb;
   uint32_t oa[C::kAPer], ob[C::kBPer];
@@ -127,6 +139,7 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void ce_tile_kernel(CeArgs a, CePie
       if (to < a.workers) k_hi = to * tiles_k / a.workers * kTK;
     }
     nk = k_hi > k_lo ? (int)((k_hi - k_lo + kTK - 1) / kTK) : 0;
+    if (C::kLogits) shift = nt == 1 ? (int)((uint32_t)job * 2654435761u >> 16) % nk : 0;
     na = nb = kBufMost;
 #pragma unroll
     for (int t = 0; t < C::kAPer; ++t) {
@@ -189,10 +202,15 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void ce_tile_kernel(CeArgs a, CePie
   };
   auto source = [&](int kt) {
     Source s;
-    const int64_t k = (int64_t)kt * kTK;
-    s.a = uniform4(buffer_of(pa + kt * step_a, kt >= nk ? 0 : C::kAOuter ? na - kt * step_a : (int64_t)kBufMost));
-    s.b = uniform4(buffer_of(pb + kt * step_b, kt >= nk ? 0 : C::kBOuter ? nb - kt * step_b : (int64_t)kBufMost));
+    const bool none = kt >= nk;
     s.to = lds0 + (uint32_t)(kt % S) * C::kStage;
+    if (C::kLogits) {
+      kt += shift;
+      kt = kt >= nk ? kt - nk : kt;
+    }
+    const int64_t k = (int64_t)kt * kTK;
+    s.a = uniform4(buffer_of(pa + kt * step_a, none ? 0 : C::kAOuter ? na - kt * step_a : (int64_t)kBufMost));
+    s.b = uniform4(buffer_of(pb + kt * step_b, none ? 0 : C::kBOuter ? nb - kt * step_b : (int64_t)kBufMost));
     // logits: the columns of the last tile past D are zeros
     s.left = (uint32_t)(a.D - k < kTK ? a.D - k : kTK);
     return s;

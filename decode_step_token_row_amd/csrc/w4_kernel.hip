@@ -16,9 +16,21 @@
 //
 // Batches of at most 16 rows take one launch: hidden states go through LDS, four
 // steps of 128 k at a time in two buffers, and weights from memory to registers
-// four steps ahead.  Larger batches have the hidden states prepared first, in the
-// workspace: in the nibbles' order and as the LDS holds them, with the groups'
-// sums beside them, so that a step is a plain copy to LDS that takes no registers.
+// four steps ahead.  What bounds them is reading the weights: one row x 129,280 x
+// 4,096 (277 MB) takes 53 us, 5.2 TB/s, the rate of a large copy.  It took 98 us
+// while a row's 64 bytes of one step were asked for at a time: each line of
+// weights and scales had left the L2 before its other half was wanted.
+//
+// Larger batches have the hidden states prepared first, in the workspace: in the
+// nibbles' order and as the LDS holds them, with the groups' sums beside them, so
+// that a step is a plain copy to LDS that takes no registers.  There the unpacking
+// (8 or 12 operations for 8 weights), the scaling of the groups' sums, the LDS
+// reads and the products take about the same time each, and overlap only in part:
+// 256 rows x 129,280 x 7,168 in groups of 64 with zero points take 530 us (900
+// TFLOP/s); without scaling 518 us, without unpacking 543, without loading weights
+// 528 of the 578 us of that time's form.  A tile of 128 rows x 32 columns a wave
+// unpacks each weight twice for 256 rows; 64 x 64 unpacks it four times and took
+// 590 us.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

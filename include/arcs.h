@@ -1,5 +1,7 @@
 /*
- * arcs.h -- on-device batched token sampling for AMD Instinct MI355X (gfx950).
+ * arcs.h -- on-device batched token sampling for AMD Instinct MI355X (gfx950),
+ * and the vocabulary head around it: logits from 4-bit weights, and the
+ * cross entropy of given tokens with its gradients.
  *
  * The library turns a [B, V] logits tensor that already lives in GPU memory
  * into one token id per row, without copying the logits to the host.  The
@@ -47,9 +49,9 @@ typedef enum arcs_status {
   ARCS_ERR_BAD_VOCAB = -3,           /* V <= 0 or V > 2^31 - 1                  */
   ARCS_ERR_BAD_STRIDE = -4,          /* row_stride < V                          */
   ARCS_ERR_BAD_DTYPE = -5,           /* dtype is not an arcs_dtype              */
-  ARCS_ERR_WORKSPACE_TOO_SMALL = -6, /* workspace_bytes < arcs_sample_workspace_bytes() */
+  ARCS_ERR_WORKSPACE_TOO_SMALL = -6, /* workspace_bytes below the call's *_workspace_bytes() */
   ARCS_ERR_LAUNCH = -7,              /* the HIP runtime rejected a launch       */
-  ARCS_ERR_MISALIGNED = -8,          /* logits not aligned to the element size  */
+  ARCS_ERR_MISALIGNED = -8,          /* an array not aligned as its call asks for */
   ARCS_ERR_BAD_HISTORY = -9,         /* exactly one of hist_ids/hist_offsets is NULL */
   ARCS_ERR_BAD_TOP_N = -10,          /* arcs_top_logprobs: n outside [1, ARCS_MAX_TOP_LOGPROBS] */
   ARCS_ERR_BAD_CAPACITY = -11,       /* arcs_commit_tokens: capacity 0, or capacity * B too large */
@@ -490,8 +492,9 @@ size_t arcs_w4_logits_workspace_bytes(int64_t B, int64_t D, int group_size);
  *               256-byte aligned, not read before it is written; calls that share
  *               one must be ordered on one stream
  * Products and sums are held in binary32.  The same call gives the same bits.
- * bfloat16 rows that are 16-byte aligned (both arrays, D % 8 == 0) take the
- * matrix kernels; others a general kernel, slower by a factor.
+ * Rows on the 16-byte grid (pointers, strides and D, in each array and output;
+ * weight_stride below 2^23 bytes) take the matrix kernels, others a general
+ * kernel that is slower by a factor.
  * Returns ARCS_OK or a negative arcs_status (nothing launched then);
  * ARCS_ERR_BAD_BATCH also where the call has more than 2^23 tiles of 128 x 128
  * logits or N exceeds 2^23.
@@ -516,9 +519,10 @@ int arcs_linear_cross_entropy(const void* hidden, int64_t hidden_stride, const v
  *   out_dweight  device [V, D] of dtype, dense, or NULL (not wanted); written
  *                whole, not added to.  One of the two must be given.
  *   workspace    arcs_linear_cross_entropy_workspace_bytes(N, V, D, dtype, 1)
- * Sums are held in binary32.  The matrix kernels hold dz of a piece in
- * bfloat16, in units of the largest |grad_loss / T| of the call.  Other
- * arguments and errors as the forward call; outputs must not overlap inputs.
+ * Sums are held in binary32.  For bfloat16 the matrix kernels hold dz of a
+ * piece in bfloat16, in units of the largest |grad_loss / T| of the call (so
+ * that equal weights are not rounded).  Other arguments and errors as the
+ * forward call; outputs must not overlap inputs.
  */
 int arcs_linear_cross_entropy_backward(const void* hidden, int64_t hidden_stride, const void* weight,
                                        int64_t weight_stride, int dtype, int64_t N, int64_t V, int64_t D,
