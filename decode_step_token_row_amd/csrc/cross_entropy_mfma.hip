@@ -139,6 +139,11 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void ce_tile_kernel(CeArgs a, CePie
       if (to < a.workers) k_hi = to * tiles_k / a.workers * kTK;
     }
     nk = k_hi > k_lo ? (int)((k_hi - k_lo + kTK - 1) / kTK) : 0;
+    // With one tile of rows every workgroup reads other weight rows, and begun together
+    // all ask for the same columns of rows a power of two apart, so for few of the
+    // memory's channels at a time: each begins its walk along k elsewhere (one row x
+    // 32,000 tokens, D = 2048: 34.3 us without, 28.7 with; 64 rows x 128,000: 270 and
+    // 273).  Tiles of the same weight rows share their loads, and begin together.
     if (C::kLogits) shift = nt == 1 ? (int)((uint32_t)job * 2654435761u >> 16) % nk : 0;
     na = nb = kBufMost;
 #pragma unroll

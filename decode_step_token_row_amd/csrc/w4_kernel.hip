@@ -134,7 +134,8 @@ struct W4 {
 
   // The scales of a workgroup's ROWS weight rows over kN groups, and the
   // constants of their zero points, on their way to LDS as [group][row] pairs.
-  // fetch only loads (a conversion beside a load would wait for it there).
+  // fetch only loads (a conversion beside a load would wait for it there).  Groups
+  // past the end get a scale of zero: the last group's may be infinite, and meets zeros.
   template <int ROWS, int kN, int THREADS>
   struct Scales {
     static_assert(ROWS * kN % THREADS == 0, "scales of a part over the threads");
@@ -143,6 +144,7 @@ struct W4 {
     uint32_t so[kPer], zo[kPer];
     uint32_t s[kPer], z[kPer];
     int groups;
+    bool past;
     __device__ __forceinline__ Scales(const W4Args& a, int64_t v0) {
       const int64_t v = v0 < a.V ? v0 : a.V - 1;
       sb = (const char*)a.scales + v * a.scale_stride * kScale;
@@ -158,7 +160,8 @@ struct W4 {
     }
     __device__ __forceinline__ void fetch(int part) {
       int g = part * kN + threadIdx.x % kN;  // THREADS is a multiple of kN
-      g = g < groups ? g : groups - 1;
+      past = g >= groups;
+      g = past ? groups - 1 : g;
 #pragma unroll
       for (int i = 0; i < kPer; ++i) {
         const char* p = sb + (so[i] + (uint32_t)g * kScale);
@@ -171,7 +174,7 @@ struct W4 {
       for (int i = 0; i < kPer; ++i) {
         const int e = threadIdx.x + i * THREADS;
         to[e % kN * ROWS + e / kN] =
-            make_uint2(SF32 ? s[i] : s[i] << 16, ZERO ? 0x42404240u - (z[i] & 15u) * 0x00040004u : 0u);
+            make_uint2(past ? 0 : SF32 ? s[i] : s[i] << 16, ZERO ? 0x42404240u - (z[i] & 15u) * 0x00040004u : 0u);
       }
     }
   };

@@ -116,10 +116,27 @@ def test_non_finite_rows_stay_in_their_row(arcs):
     assert got[3].isnan().all() and not got[17].isfinite().any() and got[:, 250].isnan().all()
 
 
-def test_side_stream_and_replays(arcs):
+@pytest.mark.parametrize("B,D,G", [(5, 96, 32), (16, 640, 64), (20, 96, 32), (70, 320, 64), (33, 128, 128)])
+def test_an_infinite_scale_in_the_last_group(arcs, B, D, G):
+    """A hidden size that ends inside a step: the infinite last scale gives what the definition
+    gives, an infinity of the group's sign, and no NaN from beyond the end."""
+    import torch
+    host, dev = make(B, 150, D, G, False, "f32", seed=D + B)
+    s = dev["scales"].clone()
+    s[70, -1] = float("inf")
+    dev["qweight"][70, -G // 2:] = 0xff  # 15 - 8 everywhere: no product with a zero level
+    h = dev["hidden"].clone()
+    h[:, -G:] = h[:, -G:].abs() + 0.25
+    got = arcs.w4_logits(h, dev["qweight"], s, G, out_dtype=torch.float32)
+    assert (got[:, 70] == float("inf")).all()
+    assert got[:, :70].isfinite().all() and got[:, 71:].isfinite().all()
+
+
+@pytest.mark.parametrize("B", [8, 40])
+def test_side_stream_and_replays(arcs, B):
     """A call on another stream, and a captured call replayed on new inputs."""
     import torch
-    B, V, D, G = 8, 1000, 1024, 128
+    V, D, G = 1000, 1024, 128
     host, dev = make(B, V, D, G, True, "bf16", seed=11)
     args = (dev["qweight"], dev["scales"], G)
     side = torch.cuda.Stream()
