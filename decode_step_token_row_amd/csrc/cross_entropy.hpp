@@ -7,8 +7,9 @@
 //
 // Rows whose target is ignore_index (masked) or refused (a target outside the
 // vocabulary, a temperature that is no positive finite number) are left out of
-// every product: a row list built on the device holds the others, and their
-// hidden states are never read (NaN there reaches nothing).
+// every product: a row list built on the device holds the others.  (Forward calls
+// of few rows compute all rows and write only the others' results.)  Either way
+// NaN in a left-out row's hidden states reaches nothing.
 #pragma once
 
 #include <hip/hip_runtime.h>

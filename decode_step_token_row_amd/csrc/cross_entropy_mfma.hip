@@ -21,7 +21,7 @@
 // workgroups that stay and load their next tile before they write the last one
 // out, 3.37.  Slower: four waves of 128 x 128 (4.0), the head three tiles deep
 // (3.67).  Few rows are bound by reading the head: one row x 32,000 x 2,048 takes
-// 34 us with its launches (131 MB, 26 us at the rate of a copy).
+// 29 us with its launches (131 MB, 26 us at the rate of a copy).
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -576,11 +576,16 @@ void launch_tile(const CeArgs& a, const CePiece& pc, hipStream_t stream) {
   hipLaunchKernelGGL((ce_tile_kernel<T, MODE, WM, WN, MT, NT, S>), dim3((unsigned)blocks), dim3(C::kThreads), 0, stream, a, pc);
 }
 
-// The tile of a call: by its rows, so that few rows are not padded to many.
-//   bfloat16  32 x 256 (32 x 128 where that leaves compute units without a tile), 64 x 256, 128 x 256, 256 x 256
+// The tile of a call: by its rows, so that few rows are not padded to many.  Against
+// 129,280 x 4,096 in bfloat16, in the tile taken and in the next larger one: 32 rows
+// 190 and 190 us forward, 694 and 701 backward; 64 rows 186 and 189, 724 and 730;
+// 128 rows 192 and 251, 841 and 876.
+//   bfloat16  32 x 256 (32 x 128 where that leaves compute units without a tile: one
+//             row x 32,000 x 2,048 28.6 us, 33.3 with 256), 64 x 256, 128 x 256, 256 x 256
 //   float32   the first three, and 128 x 128 for more rows: their products take so
 //             long that smaller tiles, two workgroups a compute unit, cost no time in
-//             loads and spread over the card more evenly
+//             loads and spread over the card more evenly (training step of 384 rows x
+//             32,000 x 1,024: 815 us, 925 with 128 x 256)
 template <typename T, int MODE>
 void launch_rows(const CeArgs& a, const CePiece& pc, hipStream_t stream) {
   const int rows = ce_rows_of_tile(a.N, sizeof(T) == 2);

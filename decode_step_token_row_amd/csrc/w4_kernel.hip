@@ -478,6 +478,9 @@ void launch_w4_batch(W4Args a, bool f32, hipStream_t stream) {
 
 template <int GROUP, bool ZERO, bool SF32>
 void launch_w4_typed(W4Args a, bool f32, hipStream_t stream) {
+  // The smallest tile that holds the batch, and from 65 rows on 128 rows a tile.  Against
+  // 129,280 x 4,096 in groups of 128, in the tile taken and in the next larger one: 16
+  // rows 65 and 69 us, 32 rows 81 and 95 us, 64 rows 98 and 147 us.
   if (a.B <= kW4FewRows) {
     launch_w4_rows<GROUP, ZERO, SF32>(a, f32, stream);
   } else if (a.B <= 32) {

@@ -474,10 +474,10 @@ size_t arcs_w4_logits_workspace_bytes(int64_t B, int64_t D, int group_size);
  *   out_lse[n] = ln sum_v exp(z_v),   out_loss[n] = out_lse[n] - z_target[n],
  * so -out_loss is the target's log-probability, as arcs_top_logprobs reports
  * it for the logits' distribution.  Rows whose target is ignore_index (which
- * may be any value) are left out: loss and lse 0, and their hidden states are
- * not read.  Rows whose target is outside [0, V), or whose T is NaN, <= 0 or
- * +inf, get loss and lse NaN and a row status.  Other NaN and infinities
- * propagate: a row with a NaN or +inf logit has a NaN loss.
+ * may be any value) are left out: loss and lse 0, and what their hidden states
+ * hold (NaN, say) reaches nothing.  Rows whose target is outside [0, V), or
+ * whose T is NaN, <= 0 or +inf, get loss and lse NaN and a row status.  Other NaN
+ * and infinities propagate: a row with a NaN or +inf logit has a NaN loss.
  *   hidden      device [N, hidden_stride] of dtype (ARCS_DTYPE_BF16 or
  *               ARCS_DTYPE_F32), hidden_stride >= D, D in 1 .. ARCS_MAX_HIDDEN
  *   weight      device [V, weight_stride] of the same dtype, weight_stride >= D
@@ -496,8 +496,8 @@ size_t arcs_w4_logits_workspace_bytes(int64_t B, int64_t D, int group_size);
  * weight_stride below 2^23 bytes) take the matrix kernels, others a general
  * kernel that is slower by a factor.
  * Returns ARCS_OK or a negative arcs_status (nothing launched then);
- * ARCS_ERR_BAD_BATCH also where the call has more than 2^23 tiles of 128 x 128
- * logits or N exceeds 2^23.
+ * ARCS_ERR_BAD_BATCH also for more than 65,535 tiles of 128 rows, or more than
+ * 2^23 tiles of 128 x 128 in [N, the larger of V and D].
  */
 int arcs_linear_cross_entropy(const void* hidden, int64_t hidden_stride, const void* weight,
                               int64_t weight_stride, int dtype, int64_t N, int64_t V, int64_t D,
