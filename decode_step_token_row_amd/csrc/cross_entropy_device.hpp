@@ -42,6 +42,17 @@ __device__ __forceinline__ int ce_row_kind(const CeArgs& a, int64_t n, int32_t& 
   return 0;
 }
 
+// The record of a listed row in the backward pass.
+__device__ __forceinline__ CeRow ce_row(const CeArgs& a, int64_t n, int32_t target, float T, float gmax) {
+  CeRow r = {};
+  r.row = (int32_t)n;
+  r.target = target;
+  r.a = kLog2e / T;
+  r.c = (a.grad_loss[n] / T) / gmax;
+  r.lse2 = a.lse[n] * kLog2e;
+  return r;
+}
+
 // cross_entropy_kernel.hip
 void launch_cross_entropy_prep(const CeArgs& a, bool backward, hipStream_t stream);
 void launch_cross_entropy_combine(const CeArgs& a, bool direct, hipStream_t stream);

@@ -60,13 +60,14 @@ __global__ __launch_bounds__(kPrepNT) void ce_prep_kernel(CeArgs a) {
     base += all;
     if (n >= a.N) continue;
     if (k == 0) {
-      CeRow r;
-      r.row = (int32_t)n;
-      r.target = t;
-      r.a = kLog2e / T;
-      r.c = BACKWARD ? (a.grad_loss[n] / T) / gmax : 0.0f;
-      r.lse2 = BACKWARD ? a.lse[n] * kLog2e : 0.0f;
-      r.pad[0] = r.pad[1] = r.pad[2] = 0;
+      CeRow r = {};
+      if (BACKWARD) {
+        r = ce_row(a, n, t, T, gmax);
+      } else {
+        r.row = (int32_t)n;
+        r.target = t;
+        r.a = kLog2e / T;
+      }
       a.rows[at] = r;
     }
     if (BACKWARD) {

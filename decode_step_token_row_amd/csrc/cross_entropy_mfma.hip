@@ -551,6 +551,59 @@ __global__ __launch_bounds__(256) void ce_dhidden_parts_kernel(CeArgs a, int BN)
   }
 }
 
+// Backward of at most kCeFewRows rows: the row list and the listed rows' hidden states
+// in one launch.  Each workgroup goes over all rows to place its own (both gradients, 64
+// rows x 8,000 x 1,024: 36.6 us, 39.4 with a list and then a copy).
+constexpr int kCeFewRows = 1024;
+
+template <typename T>
+__global__ __launch_bounds__(256) void ce_list_copy_kernel(CeArgs a) {
+  __shared__ int s_before[4], s_all[4];
+  __shared__ float s_max[4];
+  const int64_t n = blockIdx.x;
+  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+  int before = 0, all = 0;
+  float m = 0.0f;
+  for (int64_t o0 = 0; o0 < a.N; o0 += 256) {
+    const int64_t o = o0 + tid;
+    int32_t t;
+    float temperature;
+    const bool listed = o < a.N && ce_row_kind(a, o, t, temperature) == 0;
+    if (listed) {
+      const float g = fabsf(a.grad_loss[o] / temperature);
+      if (g < __builtin_inff() && g > m) m = g;
+    }
+    all += __popcll(__ballot(listed));
+    before += __popcll(__ballot(listed && o < n));
+  }
+  m = wave_max_f32(m);
+  if (lane == 0) {
+    s_before[wave] = before;
+    s_all[wave] = all;
+    s_max[wave] = m;
+  }
+  __syncthreads();
+  before = s_before[0] + s_before[1] + s_before[2] + s_before[3];
+  all = s_all[0] + s_all[1] + s_all[2] + s_all[3];
+  m = fmaxf(fmaxf(s_max[0], s_max[1]), fmaxf(s_max[2], s_max[3]));
+  const float gmax = m > 0.0f ? m : 1.0f;
+  int32_t target;
+  float temperature;
+  const bool listed = ce_row_kind(a, n, target, temperature) == 0;
+  if (tid == 0) {
+    if (n == 0) {
+      a.head->count = all;
+      a.head->gmax = gmax;
+    }
+    a.place[n] = listed ? before : -1;
+    if (listed) a.rows[before] = ce_row(a, n, target, temperature, gmax);
+  }
+  if (!listed) return;
+  const u32x4* from = (const u32x4*)((const T*)a.hidden + n * a.hidden_stride);
+  u32x4* to = (u32x4*)((T*)a.hc + before * a.D);
+  for (int64_t c = tid; c < a.D * (int64_t)sizeof(T) / 16; c += 256) to[c] = from[c];
+}
+
 // The hidden states of the listed rows, one after the other.
 template <typename T>
 __global__ __launch_bounds__(256) void ce_copy_kernel(CeArgs a) {
@@ -576,6 +629,17 @@ void launch_tile(const CeArgs& a, const CePiece& pc, hipStream_t stream) {
   hipLaunchKernelGGL((ce_tile_kernel<T, MODE, WM, WN, MT, NT, S>), dim3((unsigned)blocks), dim3(C::kThreads), 0, stream, a, pc);
 }
 
+// Whether the tiles of logits are too few for the compute units: then tiles of 64 (32)
+// rows x 64 take less time.  Forward, with them and without: bfloat16, D = 1,024, 64 rows x
+// 8,000 (32 tiles) 11.5 and 16.6 us, 300 x 8,000 (64) 21.6 and 35.4, D = 2,048, 300 x 15,000
+// (118) 46 and 55, but 900 x 7,000 (112) 38 and 36; float32, D = 512, 64 x 25,000 (98) 29
+// and 43, 20 x 25,000 (196) 26.5 and 19.8, and in the square tiles 200 x 12,000 x 1,024
+// (188) 66 and 75, 512 x 8,000 x 1,024 (252) 89 and 84.
+bool few_tiles(int64_t len, int64_t N, bool bf16) {
+  const int rows = ce_rows_of_tile(N, bf16);
+  return tiles(len, rows == 32 ? 128 : ce_columns_of_tile(N, bf16)) * tiles(N, rows) < (!bf16 && rows == 128 ? 192 : 128);
+}
+
 // The tile of a call: by its rows, so that few rows are not padded to many.  Against
 // 129,280 x 4,096 in bfloat16, in the tile taken and in the next larger one: 32 rows
 // 190 and 190 us forward, 694 and 701 backward; 64 rows 186 and 189, 724 and 730;
@@ -589,8 +653,20 @@ void launch_tile(const CeArgs& a, const CePiece& pc, hipStream_t stream) {
 template <typename T, int MODE>
 void launch_rows(const CeArgs& a, const CePiece& pc, hipStream_t stream) {
   const int rows = ce_rows_of_tile(a.N, sizeof(T) == 2);
+  if constexpr (MODE == kCeStats || MODE == kCeDs) {
+    if (few_tiles(pc.len, a.N, sizeof(T) == 2)) {
+      if (rows == 32) return launch_tile<T, MODE, 2, 1, 1, 1, 4>(a, pc, stream);
+      return launch_tile<T, MODE, 2, 2, 1, 1, 4>(a, pc, stream);
+    }
+  }
   if constexpr (sizeof(T) == 2) {
-    if constexpr (MODE == kCeDweight) return launch_tile<T, MODE, 2, 4, 4, 2, 2>(a, pc, stream);
+    if constexpr (MODE == kCeDweight) {
+      // two tiles of 128 x 128 run on a compute unit at once and even out a short launch (both
+      // gradients, 900 rows x 7,000 x 1,024: 96 us, 102 with 256 x 256); of a long one the larger
+      // tiles read less (512 x 30,000 x 2,048: 245 us, 250 with 128 x 128)
+      if (tiles(a.D, 256) * tiles(pc.len, 256) < 512) return launch_tile<T, MODE, 2, 2, 2, 2, 2>(a, pc, stream);
+      return launch_tile<T, MODE, 2, 4, 4, 2, 2>(a, pc, stream);
+    }
     else if (rows == 256) return launch_tile<T, MODE, 2, 4, 4, 2, 2>(a, pc, stream);
     else if (rows == 128) return launch_tile<T, MODE, 4, 2, 2, 2, 3>(a, pc, stream);
   } else {
@@ -608,6 +684,7 @@ void launch_rows(const CeArgs& a, const CePiece& pc, hipStream_t stream) {
 // Slices of a row in STATS: the waves along m of its tiles.
 int64_t slices_of(int64_t V, int64_t N, bool bf16) {
   const int rows = ce_rows_of_tile(N, bf16);
+  if (few_tiles(V, N, bf16)) return tiles(V, 64) * 2;
   if (rows == 32) return tiles(V, 256) < 256 ? tiles(V, 128) * 4 : tiles(V, 256) * 8;
   if (rows == 64) return tiles(V, 256) * 4;
   if (rows == 128) return bf16 ? tiles(V, 256) * 4 : tiles(V, 128) * 2;
@@ -622,8 +699,10 @@ hipError_t launch_matrix(CeArgs a, bool backward, hipStream_t stream) {
   pc.gather = !backward && (unsigned __int128)a.N * (unsigned __int128)a.hidden_stride * sizeof(T) < kBufMost;
   // a tile's worth of rows or less: a list would save no product
   pc.direct = pc.gather && a.N <= 256;
-  if (!pc.direct) launch_cross_entropy_prep(a, backward, stream);
-  if (!pc.gather) hipLaunchKernelGGL(ce_copy_kernel<T>, dim3((unsigned)a.N), dim3(256), 0, stream, a);
+  const bool few = backward && a.N <= kCeFewRows;
+  if (few) hipLaunchKernelGGL(ce_list_copy_kernel<T>, dim3((unsigned)a.N), dim3(256), 0, stream, a);
+  else if (!pc.direct) launch_cross_entropy_prep(a, backward, stream);
+  if (!pc.gather && !few) hipLaunchKernelGGL(ce_copy_kernel<T>, dim3((unsigned)a.N), dim3(256), 0, stream, a);
   if (!backward) {
     a.slices = slices_of(a.V, a.N, kBf16);
     launch_rows<T, kCeStats>(a, pc, stream);

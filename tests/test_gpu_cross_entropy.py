@@ -142,6 +142,17 @@ CASES = [
     (300, 5000, 128, "bf16", True, 0.25, True),
     (513, 300, 72, "f32", True, 0.1, True),
     (1100, 600, 320, "bf16", False, 0.6, True),
+    # vocabularies with enough tiles for the larger ones of each row count
+    (20, 16500, 64, "bf16", True, 0.2, True),
+    (20, 66003, 64, "bf16", False, 0.0, True),
+    (64, 33000, 64, "bf16", True, 0.0, True),
+    (100, 33001, 72, "bf16", False, 0.3, True),
+    (130, 33000, 1032, "bf16", True, 0.1, True),
+    (300, 16500, 64, "bf16", False, 0.5, False),
+    (20, 16500, 64, "f32", True, 0.2, True),
+    (50, 33001, 36, "f32", False, 0.0, True),
+    (200, 12500, 64, "f32", True, 0.3, True),
+    (1024, 500, 48, "bf16", True, 0.4, True),
 ]
 
 
