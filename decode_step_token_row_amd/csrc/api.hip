@@ -174,7 +174,7 @@ arcs::CeArgs cross_entropy_args(const void* hidden, int64_t hidden_stride, const
   a.place = (int32_t*)(w + p.place);
   a.partial = (float2*)(w + p.partial);
   a.slices = p.slices;
-  a.ytarget = (float*)(w + p.ytarget);
+  a.dtarget = (float*)(w + p.dtarget);
   a.ds = w + p.ds;
   a.ds_ld = p.piece;
   a.slab = (float*)(w + p.slab);

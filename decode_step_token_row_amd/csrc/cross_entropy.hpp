@@ -34,8 +34,9 @@ struct CeRow {
   int32_t target;  // in [0, V)
   float a;         // log2(e) / T: logits in base 2 are dot * a
   float c;         // (grad_loss / T) / gmax
-  float lse2;      // its logsumexp in base 2 (backward)
-  int32_t pad[3];
+  float lse2;      // its logsumexp in base 2 (backward), rounded,
+  float rest;      // and 2 to minus what the rounding left: p = 2^(dot * a - lse2) * rest
+  int32_t pad[2];
 };
 static_assert(sizeof(CeRow) == 32, "row record");
 
@@ -61,7 +62,7 @@ struct CeArgs {
   int32_t* place;   // [N] backward: a row's place in the list, -1 if it is not listed
   float2* partial;  // forward: [N][slices] (maximum, sum of 2^(y - maximum)) of y = z * log2(e)
   int64_t slices;
-  float* ytarget;   // forward: [N] y of the target
+  float* dtarget;   // forward: [N] the target's dot product
   void* ds;         // backward: [N][ds_ld] dz / gmax of one piece of the vocabulary
   int64_t ds_ld;    // (also the piece's length)
   float* slab;      // backward: partial sums of dhidden / gmax: [splits][N][D], or parts of tiles (matrix kernels)
@@ -72,7 +73,7 @@ struct CeArgs {
 
 // The workspace's parts, in bytes from its start.
 struct CePlan {
-  size_t rows, place, partial, ytarget, ds, slab, hc, total;
+  size_t rows, place, partial, dtarget, ds, slab, hc, total;
   int64_t slices, piece;
   int splits, workers;
   bool fits;  // the sizes fit size_t and the launch grids

@@ -13,7 +13,6 @@ typedef float f32x16 __attribute__((ext_vector_type(16)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr float kLog2e = 1.44269504088896340736f;
-constexpr float kLn2 = 0.69314718055994530942f;
 
 __device__ __forceinline__ float exp2_fast(float x) { return __builtin_amdgcn_exp2f(x); }
 __device__ __forceinline__ float finite_or_zero(float m) { return m == -__builtin_inff() ? 0.0f : m; }
@@ -49,7 +48,10 @@ __device__ __forceinline__ CeRow ce_row(const CeArgs& a, int64_t n, int32_t targ
   r.target = target;
   r.a = kLog2e / T;
   r.c = (a.grad_loss[n] / T) / gmax;
-  r.lse2 = a.lse[n] * kLog2e;
+  // a float32 product would be off by 2^-24 |lse|, and every probability by that factor
+  const double lse2 = (double)a.lse[n] * 1.4426950408889634074;
+  r.lse2 = (float)lse2;
+  r.rest = fabsf(r.lse2) < __builtin_inff() ? exp2f((float)((double)r.lse2 - lse2)) : 1.0f;
   return r;
 }
 

@@ -95,6 +95,7 @@ __global__ __launch_bounds__(256) void ce_combine_kernel(CeArgs a, int direct) {
   const int64_t i = blockIdx.x;
   const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
   int64_t n = i;
+  float scale;  // as the tiles had it
   if (direct) {
     int32_t target;
     float T;
@@ -104,9 +105,11 @@ __global__ __launch_bounds__(256) void ce_combine_kernel(CeArgs a, int direct) {
       if (tid == 0) a.out_loss[i] = a.out_lse[i] = k < 0 ? 0.0f : __builtin_nanf("");
       return;
     }
+    scale = kLog2e / T;
   } else {
     if (i >= a.head->count) return;
     n = a.rows[i].row;
+    scale = a.rows[i].a;
   }
   // each lane's slices, then the lanes', then the waves' (the first wave goes over the four)
   const float2* p = a.partial + i * a.slices;
@@ -126,9 +129,12 @@ __global__ __launch_bounds__(256) void ce_combine_kernel(CeArgs a, int direct) {
   __syncthreads();
   if (tid == 0) {
     for (int w = 1; w < 4; ++w) join(s_part[w].x, s_part[w].y);
-    const float l2 = m + log2f(sum);
-    a.out_lse[n] = l2 * kLn2;
-    a.out_loss[n] = (l2 - a.ytarget[i]) * kLn2;
+    // joined in 64 bits: each result is rounded once, at its own size, not at the maximum's
+    int e;
+    const float f = frexpf(sum, &e);
+    const double l2 = (double)m + (double)e + (double)log2f(f);
+    a.out_lse[n] = (float)(l2 * 0.69314718055994530942);
+    a.out_loss[n] = (float)((l2 - (double)a.dtarget[i] * (double)scale) * 0.69314718055994530942);
   }
 }
 
@@ -281,7 +287,7 @@ __global__ __launch_bounds__(256, 3) void ce_general_kernel(CeArgs a, CePiece pc
     if (kLogits) {
       CeRow row;
       row.target = -1;
-      row.a = row.c = row.lse2 = 0.0f;
+      row.a = row.c = row.lse2 = row.rest = 0.0f;
       if (n < N) row = a.rows[n];
       if (MODE == kCeStats) {
         float m = -__builtin_inff();
@@ -290,11 +296,10 @@ __global__ __launch_bounds__(256, 3) void ce_general_kernel(CeArgs a, CePiece pc
 #pragma unroll
           for (int r = 0; r < 16; ++r) {
             const int64_t v = row_of(i, r);
-            const float y = acc[i][j][r] * row.a;
-            acc[i][j][r] = y;
+            const float dot = acc[i][j][r], y = dot * row.a;
             if (v < M) {
               m = fmaxf(m, y);
-              if (pc.v0 + v == row.target) a.ytarget[n] = y;
+              if (pc.v0 + v == row.target) a.dtarget[n] = dot;
             }
           }
         m = fmaxf(m, __shfl_xor(m, 32, kWave));
@@ -304,7 +309,7 @@ __global__ __launch_bounds__(256, 3) void ce_general_kernel(CeArgs a, CePiece pc
         for (int i = 0; i < 2; ++i)
 #pragma unroll
           for (int r = 0; r < 16; ++r)
-            if (row_of(i, r) < M) sum += exp2_fast(acc[i][j][r] - mz);
+            if (row_of(i, r) < M) sum += exp2_fast(fmaf(acc[i][j][r], row.a, -mz));
         sum += __shfl_xor(sum, 32, kWave);
         // a slice is a wave's 64 rows of the tile
         if (fk == 0 && n < N) a.partial[n * a.slices + 2 * (int64_t)blockIdx.x + (wave & 1)] = make_float2(m, sum);
@@ -315,7 +320,7 @@ __global__ __launch_bounds__(256, 3) void ce_general_kernel(CeArgs a, CePiece pc
 #pragma unroll
           for (int r = 0; r < 16; ++r) {
             const int64_t v = row_of(i, r);
-            float p = exp2_fast(fmaf(acc[i][j][r], row.a, -row.lse2));
+            float p = exp2_fast(fmaf(acc[i][j][r], row.a, -row.lse2)) * row.rest;
             if (pc.v0 + v == row.target) p -= 1.0f;
             out[v] = v < M ? p * row.c : 0.0f;  // ds_ld is a multiple of the tile
           }
@@ -369,7 +374,7 @@ CePlan cross_entropy_plan(int64_t N, int64_t V, int64_t D, int dtype, bool backw
   p.splits = 1;
   if (!backward) {
     p.slices = 8 * tiles(V, 256);
-    p.ytarget = take((u128)N * 4);
+    p.dtarget = take((u128)N * 4);
     p.partial = take((u128)N * p.slices * sizeof(float2));
   } else {
     // dz of a piece: bfloat16 in the matrix kernels, float32 in the general one

@@ -409,7 +409,7 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void ce_tile_kernel(CeArgs a, CePie
           for (int i = 0; i < MT; ++i)
 #pragma unroll
             for (int r = 0; r < 16; ++r) t = row_of(i, r) == (int)to_target ? acc[i][j][r] : t;
-          if (mine) a.ytarget[n] = t * row.a;
+          if (mine) a.dtarget[n] = t;
         }
       }
     }
@@ -440,7 +440,7 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void ce_tile_kernel(CeArgs a, CePie
         if (n >= N) continue;
         CeRow row;
         row.target = -1;
-        row.a = row.c = row.lse2 = 0.0f;
+        row.a = row.c = row.lse2 = row.rest = 0.0f;
         if (MODE == kCeDs) row = a.rows[n];
         const int64_t to_target = (int64_t)row.target - pc.v0 - em0 - mw;
         const int target = to_target >= 0 && to_target < MT * 32 ? (int)to_target : -1;
@@ -455,7 +455,7 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void ce_tile_kernel(CeArgs a, CePie
               const int id = row_of(i, q * 4 + e);
               float v = acc[i][j][q * 4 + e];
               if (MODE == kCeDs) {
-                v = exp2_fast(fmaf(v, row.a, -row.lse2));
+                v = exp2_fast(fmaf(v, row.a, -row.lse2)) * row.rest;
                 v = id == target ? v - 1.0f : v;
                 v = id < m_left ? v * row.c : 0.0f;
               } else {
@@ -477,7 +477,7 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void ce_tile_kernel(CeArgs a, CePie
       for (int j = 0; j < NT; ++j) {
         CeRow row;
         row.target = -1;
-        row.a = row.c = row.lse2 = 0.0f;
+        row.a = row.c = row.lse2 = row.rest = 0.0f;
         if (MODE == kCeDs && en0 + wn + j * 32 + fr < N) row = a.rows[en0 + wn + j * 32 + fr];
         const int64_t to_target = (int64_t)row.target - pc.v0 - em0 - mw;
         const int target = to_target >= 0 && to_target < MT * 32 ? (int)to_target : -1;
@@ -493,7 +493,7 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void ce_tile_kernel(CeArgs a, CePie
                 float v = acc[i][j][q * 4 + e];
                 if (MODE == kCeDs) {
                   const int id = row_of(i, q * 4 + e);
-                  v = exp2_fast(fmaf(v, row.a, -row.lse2));
+                  v = exp2_fast(fmaf(v, row.a, -row.lse2)) * row.rest;
                   v = id == target ? v - 1.0f : v;
                   v = id < m_left ? v * row.c : 0.0f;
                 } else {
