@@ -26,7 +26,7 @@
 // that a step is a plain copy to LDS that takes no registers.  There the unpacking
 // (8 or 12 operations for 8 weights), the scaling of the groups' sums, the LDS
 // reads and the products take about the same time each, and overlap only in part:
-// 256 rows x 129,280 x 7,168 in groups of 64 with zero points take 530 us (900
+// 256 rows x 129,280 x 7,168 in groups of 64 with zero points take 530 to 570 us (830-900
 // TFLOP/s); without scaling 518 us, without unpacking 543, without loading weights
 // 528 of the 578 us of that time's form.  A tile of 128 rows x 32 columns a wave
 // unpacks each weight twice for 256 rows; 64 x 64 unpacks it four times and took
