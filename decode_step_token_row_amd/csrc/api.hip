@@ -331,7 +331,7 @@ int arcs_w4_logits(const void* hidden, int64_t B, int64_t D, int64_t hidden_stri
       misaligned(scales, scale_dtype == ARCS_DTYPE_BF16 ? 2 : 4) ||
       misaligned(logits, logits_dtype == ARCS_DTYPE_BF16 ? 2 : 4))
     return ARCS_ERR_MISALIGNED;
-  const size_t need = arcs::w4_workspace_bytes(B, D, group_size);
+  const size_t need = arcs::w4_workspace_bytes(B, D);
   if (workspace_bytes < need) return ARCS_ERR_WORKSPACE_TOO_SMALL;
   if (need > 0 && workspace == nullptr) return ARCS_ERR_NULL_POINTER;
   if (need > 0 && misaligned(workspace, 256)) return ARCS_ERR_MISALIGNED;
@@ -357,7 +357,7 @@ size_t arcs_w4_logits_workspace_bytes(int64_t B, int64_t D, int group_size) {
   if (B <= 0 || B > kMaxW4Batch || D <= 0 || D > ARCS_MAX_HIDDEN ||
       (group_size != 32 && group_size != 64 && group_size != 128))
     return 0;
-  return arcs::w4_workspace_bytes(B, D, group_size);
+  return arcs::w4_workspace_bytes(B, D);
 }
 
 int arcs_linear_cross_entropy(const void* hidden, int64_t hidden_stride, const void* weight,

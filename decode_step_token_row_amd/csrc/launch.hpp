@@ -125,10 +125,9 @@ struct W4Args {
   int tiles, batch_tiles;
   int64_t padded_rows;     // of the prepared hidden states
   char* prepared;
-  float* sums;
 };
 // Bytes of workspace (0 for batches that need none).
-size_t w4_workspace_bytes(int64_t B, int64_t D, int group);
+size_t w4_workspace_bytes(int64_t B, int64_t D);
 hipError_t launch_w4_logits(W4Args a, int scale_dtype, int logits_dtype, int group, void* workspace, hipStream_t stream);
 
 hipError_t launch_argmax(const void* logits, int dtype, int64_t B, int64_t V, int64_t stride,

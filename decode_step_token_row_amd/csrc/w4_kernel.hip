@@ -5,32 +5,30 @@
 // q is two weights a byte, the lower d in the low nibble.  The products run
 // on the bfloat16 matrix instruction with the batch as its rows and 16
 // vocabulary rows as its columns, so a lane needs the scale of one row only.
-// A nibble becomes an exact bfloat16 with an offset: 16 + q by an AND and an
-// OR on two weights at a time (0x4180 is 16.0 and bit 3 of its mantissa is 1),
-// or, with zero points, 48 + q - z by an AND and an addition of the row's
-// constant (0x4200 is 32.0, bit 2 is 1).  The offset's part of a group's sum,
-// 24 or 48 times the sum of the hidden state over the group, is what the
-// product's accumulator starts from, negated:
-//   sum (q - z) h = -48 sum h + sum (48 + q - z) h.
-// Scales are applied to the group's float32 sums, so no weight is rounded.
+// A nibble becomes the level q - z itself, exactly, in bfloat16 times 2^-19 (w4_unpack),
+// and the logits are multiplied by 2^19 at the end.  So a level of zero adds
+// nothing, an infinite hidden state keeps its level's sign and sums are no larger
+// than the definition's.  (Levels with an offset of 16 or 48, taken away again
+// through the accumulator's start, took 8 or 12 operations for 8 weights instead of
+// 17 to 19 but lost four to six bits of a sum to the offset's, and all of it with one
+// large hidden state.)  Scales are applied to the group's float32 sums, so no
+// weight is rounded.
 //
 // Batches of at most 16 rows take one launch: hidden states go through LDS, four
 // steps of 128 k at a time in two buffers, and weights from memory to registers
-// four steps ahead.  What bounds them is reading the weights: one row x 129,280 x
-// 4,096 (277 MB) takes 53 us, 5.2 TB/s, the rate of a large copy.  It took 98 us
-// while a row's 64 bytes of one step were asked for at a time: each line of
-// weights and scales had left the L2 before its other half was wanted.
+// four steps ahead.  What bounds them is reading the weights, beside which the
+// unpacking does not hide whole: one row x 129,280 x 4,096 (277 MB) takes 60 us,
+// 4.6 TB/s (a large copy reaches 5.1; levels with an offset took 54).  It took nearly
+// twice that while a row's 64 bytes of one step were asked for at a time: each line
+// of weights and scales had left the L2 before its other half was wanted.
 //
 // Larger batches have the hidden states prepared first, in the workspace: in the
-// nibbles' order and as the LDS holds them, with the groups' sums beside them, so
-// that a step is a plain copy to LDS that takes no registers.  There the unpacking
-// (8 or 12 operations for 8 weights), the scaling of the groups' sums, the LDS
-// reads and the products take about the same time each, and overlap only in part:
-// 256 rows x 129,280 x 7,168 in groups of 64 with zero points take 530 to 570 us (830-900
-// TFLOP/s); without scaling 518 us, without unpacking 543, without loading weights
-// 528 of the 578 us of that time's form.  A tile of 128 rows x 32 columns a wave
-// unpacks each weight twice for 256 rows; 64 x 64 unpacks it four times and took
-// 590 us.
+// nibbles' order and as the LDS holds them, so that a step is a plain copy to LDS
+// that takes no registers.  There the unpacking, the scaling of the groups' sums, the
+// LDS reads and the products take about the same time each, and overlap only in part:
+// 256 rows x 129,280 x 7,168 in groups of 64 with zero points take 557 us (850
+// TFLOP/s).  A tile of 128 rows x 32 columns a wave unpacks each weight twice for 256
+// rows; 64 x 64 a wave unpacks it four times and took 590 us where this one took 570.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -46,24 +44,43 @@ typedef float f32x4 __attribute__((ext_vector_type(4)));
 constexpr int64_t kW4FewRows = 16;
 constexpr int kW4Step = 128;  // k of one step: 16 bytes of a weight row in each of four lanes
 
-// Eight nibbles as bfloat16, in the order 0 4 1 5 2 6 3 7: 16 + q, or with zero
-// points (add = 0x42004200 + 4 (16 - z) in both halves) 48 + q - z.
-template <bool ZERO>
-__device__ __forceinline__ bf16x8 w4_unpack(uint32_t w, uint32_t add) {
-  u32x4 d;
-  if (ZERO) {
-    d[0] = ((w << 2) & 0x003C003Cu) + add;
-    d[1] = ((w >> 2) & 0x003C003Cu) + add;
-    d[2] = ((w >> 6) & 0x003C003Cu) + add;
-    d[3] = ((w >> 10) & 0x003C003Cu) + add;
-  } else {
-    d[0] = ((w << 3) & 0x00780078u) | 0x41804180u;
-    d[1] = ((w >> 1) & 0x00780078u) | 0x41804180u;
-    d[2] = ((w >> 5) & 0x00780078u) | 0x41804180u;
-    d[3] = ((w >> 9) & 0x00780078u) | 0x41804180u;
+// Eight nibbles less their zero point, times 2^-19, as bfloat16 in the order 0 4 1 5 2 6 3 7.
+// Two nibbles at a time become the binary16 numbers 128 + q / 8 (or, from the bits four
+// higher, 8 + q / 8); adding -(128 + z / 8) or -(8 + z / 8) gives (q - z) / 8 exactly.  Its
+// exponent field is 0 or 12 .. 15, whose upper three bits are 011, and its lower seven
+// mantissa bits are 0: with its lower twelve bits moved down by three, under the upper four
+// as they were, it is the bfloat16 with the exponent field 011 011xx, that is 2^-16 times the
+// number.  `zero` holds z in bits 0 .. 3 of both halves.
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+
+// The masks are registers to the compiler: an AND and an OR of two literals are two
+// instructions, of a register and a literal one (21 operations for 8 weights, 17 so).
+struct W4Masks {
+  uint32_t low = 0x000F000Fu, high = 0x00F000F0u;
+  __device__ __forceinline__ W4Masks() {
+    asm("" : "+v"(low));
+    asm("" : "+v"(high));
   }
+};
+
+template <bool ZERO>
+__device__ __forceinline__ bf16x8 w4_unpack(uint32_t w, uint32_t zero, const W4Masks& mask) {
+  const uint32_t low = ZERO ? zero | 0xD800D800u : 0xD808D808u, high = ZERO ? (zero << 4) | 0xC800C800u : 0xC880C880u;
+  auto level = [](uint32_t q, uint32_t less) {
+    const f16x2 x = __builtin_bit_cast(f16x2, q) + __builtin_bit_cast(f16x2, less);
+    const uint32_t b = __builtin_bit_cast(uint32_t, x);
+    return ((b >> 3) & 0x0FFF0FFFu) | (b & 0xF000F000u);
+  };
+  const uint32_t w8 = w >> 8;
+  u32x4 d;
+  d[0] = level((w & mask.low) | 0x58005800u, low);
+  d[1] = level((w & mask.high) | 0x48004800u, high);
+  d[2] = level((w8 & mask.low) | 0x58005800u, low);
+  d[3] = level((w8 & mask.high) | 0x48004800u, high);
   return __builtin_bit_cast(bf16x8, d);
 }
+
+constexpr float kW4Unit = 0x1p19f;  // what the sums of w4_unpack's levels are multiplied by
 
 // Eight bfloat16 in the same order.
 __device__ __forceinline__ u32x4 w4_order(u32x4 x) {
@@ -84,11 +101,6 @@ __device__ __forceinline__ u32x4 w4_turn(u32x4 w) {
   return u32x4{c[0], c[1], d[0], d[1]};
 }
 
-template <int CTRL>
-__device__ __forceinline__ float add_dpp(float x) {
-  return x + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), CTRL, 0xf, 0xf, true));
-}
-
 // GROUP 128: a lane's 16 bytes are 32 consecutive k and one product takes 8 of
 // each lane group's.  GROUP 32, 64: the 16 bytes are exchanged between the four
 // lane groups first, so that a product's 32 k are consecutive and lie in one group.
@@ -99,7 +111,6 @@ struct W4 {
   static constexpr bool kTurn = GROUP < 128;
   static constexpr int kScale = SF32 ? 4 : 2;               // bytes of a scale
   static constexpr int kScales = (kGroups * kScale + 3) / 4;  // words of a step's scales
-  static constexpr float kOffset = ZERO ? -48.0f : -24.0f;
 
   // Chunk c of 8 k of a step is lane group j's in product n; the LDS slot of (n, j) is 4 n + j
   // in a row of 16 chunks, then turned by the row, so that no two lanes of a read share a bank.
@@ -132,8 +143,8 @@ struct W4 {
     }
   };
 
-  // The scales of a workgroup's ROWS weight rows over kN groups, and the
-  // constants of their zero points, on their way to LDS as [group][row] pairs.
+  // The scales of a workgroup's ROWS weight rows over kN groups, and their
+  // zero points, on their way to LDS as [group][row] pairs.
   // fetch only loads (a conversion beside a load would wait for it there).  Groups
   // past the end get a scale of zero: the last group's may be infinite, and meets zeros.
   template <int ROWS, int kN, int THREADS>
@@ -174,21 +185,10 @@ struct W4 {
       for (int i = 0; i < kPer; ++i) {
         const int e = threadIdx.x + i * THREADS;
         to[e % kN * ROWS + e / kN] =
-            make_uint2(past ? 0 : SF32 ? s[i] : s[i] << 16, ZERO ? 0x42404240u - (z[i] & 15u) * 0x00040004u : 0u);
+            make_uint2(past ? 0 : SF32 ? s[i] : s[i] << 16, ZERO ? (z[i] & 15u) * 0x00010001u : 0u);
       }
     }
   };
-
-  // A lane's 8 k of a hidden row: their order, and (in the group's first lane) the group's sum.
-  static __device__ __forceinline__ float group_sum(u32x4 v) {
-    float s = (bf16_lo(v[0]) + bf16_hi(v[0])) + (bf16_lo(v[1]) + bf16_hi(v[1]));
-    s += (bf16_lo(v[2]) + bf16_hi(v[2])) + (bf16_lo(v[3]) + bf16_hi(v[3]));
-    s = add_dpp<0xB1>(s);                   // lanes 1 apart
-    s = add_dpp<0x4E>(s);                   // 2 apart
-    if (GROUP > 32) s = add_dpp<0x141>(s);  // the other four of eight
-    if (GROUP > 64) s = add_dpp<0x140>(s);  // the other eight of sixteen
-    return kOffset * s;
-  }
 };
 
 template <int MT, int RT, bool OF32>
@@ -203,8 +203,9 @@ __device__ __forceinline__ void w4_write(const W4Args& a, const f32x4 (&total)[M
       for (int e = 0; e < 4; ++e) {
         const int64_t row = b0 + m * 16 + j * 4 + e;
         if (row >= a.B) continue;
-        if (OF32) ((float*)a.logits)[row * a.row_stride + v] = total[m][t][e];
-        else ((__bf16*)a.logits)[row * a.row_stride + v] = (__bf16)total[m][t][e];
+        const float x = total[m][t][e] * kW4Unit;
+        if (OF32) ((float*)a.logits)[row * a.row_stride + v] = x;
+        else ((__bf16*)a.logits)[row * a.row_stride + v] = (__bf16)x;
       }
   }
 }
@@ -219,7 +220,6 @@ __global__ __launch_bounds__(256, 4) void w4_rows_kernel(W4Args a) {
   using K = W4<GROUP, ZERO, SF32>;
   constexpr int SC = kW4Stage, kRows = 16, kPer = kRows * SC * 16 / 256, kN = SC * K::kGroups;
   __shared__ __align__(16) char s_x[2][SC * kRows * 256];
-  __shared__ __align__(16) float s_sum[2][kN][kRows];
   __shared__ __align__(16) uint2 s_scale[2][64 * kN];
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -246,12 +246,11 @@ __global__ __launch_bounds__(256, 4) void w4_rows_kernel(W4Args a) {
       const int row = wave + p * 4;
       if (row >= a.B) continue;
       if ((int64_t)stage * SC * kW4Step + lane * 8 >= a.D) xr[p] = u32x4{0, 0, 0, 0};
-      const float s = K::group_sum(xr[p]);
       *(u32x4*)(x + row * 256 + ((K::slot(lane & 15) ^ row) * 16)) = w4_order(xr[p]);
-      if (lane % (GROUP / 8) == 0) s_sum[stage & 1][lane / (GROUP / 8)][row] = s;
     }
   };
 
+  const W4Masks mask;
   u32x4 next[SC][1];
   f32x4 total[1][1] = {{{0.0f, 0.0f, 0.0f, 0.0f}}};
   fetch_x(0);
@@ -282,11 +281,11 @@ __global__ __launch_bounds__(256, 4) void w4_rows_kernel(W4Args a) {
       for (int g = 0; g < K::kGroups; ++g) {
         const int gs = c * K::kGroups + g;
         const uint2 sc = scale[gs * 64];
-        f32x4 acc = *(const f32x4*)&s_sum[stage & 1][gs][j * 4];
+        f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
         for (int i = 0; i < K::kProducts; ++i) {
           const bf16x8 xf = *(const bf16x8*)(x + (c * kRows + r) * 256 + ((((g * K::kProducts + i) * 4 + j) ^ r) * 16));
-          acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf, w4_unpack<ZERO>(w[g * K::kProducts + i], sc.y), acc, 0, 0, 0);
+          acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf, w4_unpack<ZERO>(w[g * K::kProducts + i], sc.y, mask), acc, 0, 0, 0);
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) total[0][0][e] = fmaf(__uint_as_float(sc.x), acc[e], total[0][0][e]);
@@ -304,8 +303,7 @@ __global__ __launch_bounds__(256, 4) void w4_rows_kernel(W4Args a) {
 
 // ---------------------------------------------------------------------------
 // More rows.  The prepared hidden states of one step are 4096 bytes for every 16
-// rows: row x 256 bytes, chunk c of 8 k at slot(c) ^ row; rows past B are zeros.  The
-// sums are [step][group][row].
+// rows: row x 256 bytes, chunk c of 8 k at slot(c) ^ row; rows past B are zeros.
 // ---------------------------------------------------------------------------
 template <int GROUP, bool ZERO>
 __global__ __launch_bounds__(256) void w4_prepare_kernel(W4Args a) {
@@ -314,10 +312,8 @@ __global__ __launch_bounds__(256) void w4_prepare_kernel(W4Args a) {
   const int64_t step = blockIdx.x, tile = blockIdx.y, b = tile * 16 + row, k = step * kW4Step + c * 8;
   u32x4 v = {0, 0, 0, 0};
   if (b < a.B && k < a.D) v = *(const u32x4*)(a.hidden + b * a.hidden_stride + k);
-  const float s = K::group_sum(v);
   const int64_t tiles = a.padded_rows / 16;
   *(u32x4*)(a.prepared + (step * tiles + tile) * 4096 + row * 256 + ((K::slot(c) ^ row) * 16)) = w4_order(v);
-  if (c % (GROUP / 8) == 0) a.sums[(step * K::kGroups + c / (GROUP / 8)) * a.padded_rows + b] = s;
 }
 
 // Steps between two barriers: a row's 128 bytes, as far as LDS reaches.
@@ -330,9 +326,8 @@ __global__ __launch_bounds__(WB* WV * 64, MT == 2 ? 3 : 2) void w4_batch_kernel(
   constexpr int kWaves = WB * WV, kRows = WB * MT * 16;
   constexpr int kLoads = NS * kRows / 4, kPer = kLoads / kWaves;  // of 1024 bytes
   constexpr int kN = NS * K::kGroups;                             // groups of a part
-  constexpr int kSumLoads = (kN * kRows * 4 + 1023) / 1024;
-  constexpr int kSumAt = NS * kRows * 256, kStage = kSumAt + kSumLoads * 1024;
-  static_assert(kSumLoads <= kWaves && kLoads % kWaves == 0, "loads of a part over the waves");
+  constexpr int kStage = NS * kRows * 256;
+  static_assert(kLoads % kWaves == 0, "loads of a part over the waves");
   __shared__ __align__(1024) char lds[2 * kStage];
   __shared__ __align__(16) uint2 s_scale[2][kCols * kN];
   const int tid = threadIdx.x, lane = tid & 63;
@@ -352,11 +347,6 @@ __global__ __launch_bounds__(WB* WV * 64, MT == 2 ? 3 : 2) void w4_batch_kernel(
   const uint32_t lds0 = (uint32_t)(uintptr_t)(ARCS_LDS char*)lds;
   const int64_t step_x = a.padded_rows * 256;
   const char* px = a.prepared + b0 * 256;
-  const char* ps = (const char*)(a.sums + b0);
-  constexpr int kSumLanes = kRows / 4;  // lanes of one group's sums
-  const int sum_group = (wave * 64 + lane) / kSumLanes;
-  const uint32_t sum_off =
-      sum_group < kN ? (uint32_t)(sum_group * a.padded_rows * 4 + (wave * 64 + lane) % kSumLanes * 16) : kNoLoad;
   auto issue = [&](int part) {
     const uint32_t to = lds0 + (uint32_t)(part & 1) * kStage;
 #pragma unroll
@@ -365,8 +355,6 @@ __global__ __launch_bounds__(WB* WV * 64, MT == 2 ? 3 : 2) void w4_batch_kernel(
       load_to_lds(to + load * 1024u, (uint32_t)lane * 16,
                   buffer_of(px + ((int64_t)part * NS + step) * step_x + in * 1024, 1024));
     }
-    if (wave < kSumLoads)
-      load_to_lds(to + kSumAt + wave * 1024u, sum_off, buffer_of(ps + (int64_t)part * kN * a.padded_rows * 4, kBufMost));
   };
 
   f32x4 total[MT][RT];
@@ -374,6 +362,7 @@ __global__ __launch_bounds__(WB* WV * 64, MT == 2 ? 3 : 2) void w4_batch_kernel(
   for (int m = 0; m < MT; ++m)
 #pragma unroll
     for (int t = 0; t < RT; ++t) total[m][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  const W4Masks mask;
   u32x4 next[NS][RT];
   scales.fetch(0);
   issue(0);
@@ -393,9 +382,8 @@ __global__ __launch_bounds__(WB* WV * 64, MT == 2 ? 3 : 2) void w4_batch_kernel(
     const int ahead = part + 1 < parts ? (part + 1) * NS : 0;  // the last part's loads are not used
     const char* x = lds + (part & 1) * kStage;
     const uint2* scale = &s_scale[part & 1][wv * RT * 16 + r];
-    const float* sums = (const float*)(x + kSumAt);
     // Products p = 0 .. 4 NS - 1 of 32 k each; the hidden states of the next one are
-    // read while one runs.  Groups past D meet zeros (and the last group's scale).
+    // read while one runs.  Groups past D meet zeros, and a scale of zero.
     constexpr int kAll = 4 * NS;
     bf16x8 xf[2][MT];
     auto read_x = [&](int p) {
@@ -419,16 +407,14 @@ __global__ __launch_bounds__(WB* WV * 64, MT == 2 ? 3 : 2) void w4_batch_kernel(
 #pragma unroll
         for (int t = 0; t < RT; ++t) sc[t] = scale[gs * kCols + t * 16];
 #pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          const f32x4 start = *(const f32x4*)(sums + gs * kRows + (wb * MT + m) * 16 + j * 4);
+        for (int m = 0; m < MT; ++m)
 #pragma unroll
-          for (int t = 0; t < RT; ++t) acc[m][t] = start;
-        }
+          for (int t = 0; t < RT; ++t) acc[m][t] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
       }
       if (p + 1 < kAll) read_x(p + 1);
 #pragma unroll
       for (int t = 0; t < RT; ++t) {
-        const bf16x8 wf = w4_unpack<ZERO>(w[t][p % 4], sc[t].y);
+        const bf16x8 wf = w4_unpack<ZERO>(w[t][p % 4], sc[t].y, mask);
 #pragma unroll
         for (int m = 0; m < MT; ++m)
           acc[m][t] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(xf[p & 1][m], wf, acc[m][t], 0, 0, 0);
@@ -511,9 +497,9 @@ int64_t padded_rows(int64_t B) {
 
 }  // namespace
 
-size_t w4_workspace_bytes(int64_t B, int64_t D, int group) {
+size_t w4_workspace_bytes(int64_t B, int64_t D) {
   if (B <= kW4FewRows) return 0;
-  return (size_t)(padded_rows(B) * w4_steps(D) * (256 + 4 * (kW4Step / group)));
+  return (size_t)(padded_rows(B) * w4_steps(D) * 256);
 }
 
 hipError_t launch_w4_logits(W4Args a, int scale_dtype, int logits_dtype, int group, void* workspace, hipStream_t stream) {
@@ -521,7 +507,6 @@ hipError_t launch_w4_logits(W4Args a, int scale_dtype, int logits_dtype, int gro
   if (a.B > kW4FewRows) {
     a.padded_rows = padded_rows(a.B);
     a.prepared = (char*)workspace;
-    a.sums = (float*)(a.prepared + a.padded_rows * w4_steps(a.D) * 256);
   }
   if (group == 32) launch_w4_group<32>(a, sf32, f32, stream);
   else if (group == 64) launch_w4_group<64>(a, sf32, f32, stream);

@@ -431,9 +431,11 @@ int arcs_commit_tokens(const int32_t* ids, int64_t B, int64_t V, int32_t* next_i
  *   logits[b, v] = sum over groups g of
  *       scales[v, g] * sum over d in g of (q[v, d] - zeros[v, g]) * hidden[b, d]
  * with q in 0 .. 15 and zeros 8 where `zeros` is NULL.  Products and sums are
- * held in binary32 (weights and hidden states enter exactly) and each logit is
- * rounded once to its type.  A NaN or an infinity in a hidden state makes its
- * row's logits NaN or infinite, one in a scale its column's.
+ * held in binary32 (levels q - z and hidden states enter exactly, hidden states
+ * below 2^-107 in magnitude may count as 0) and each logit is rounded once to
+ * its type.  An infinity in a hidden state gives its row the infinities of the
+ * levels' signs, NaN at a level of 0; NaN and infinities in a scale reach its
+ * column.
  *   hidden         device bfloat16 [B, hidden_stride], rows 16-byte aligned
  *   D              hidden size, 1 .. ARCS_MAX_HIDDEN, a multiple of group_size
  *   qweight        device bytes [V, qweight_stride], rows 16-byte aligned: byte d / 2
