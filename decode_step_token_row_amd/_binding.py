@@ -180,6 +180,10 @@ def linear_cross_entropy_workspace_bytes(N: int, V: int, D: int, dtype: int, bac
 
 # --------------------------------------------------------------------------
 # torch-facing helpers
+#
+# `stream=` is the torch stream a call is enqueued on (the current one if it is
+# None).  The caller orders it against the streams that make the inputs and read
+# the results; tensors may be dropped as soon as the call returns.
 # --------------------------------------------------------------------------
 def _torch():
     import torch
@@ -190,6 +194,16 @@ def _stream_ptr(stream) -> int:
     torch = _torch()
     s = torch.cuda.current_stream() if stream is None else stream
     return int(s.cuda_stream)
+
+
+def _used_on(stream, *tensors) -> None:
+    """After a call on a given stream: tells the allocator that the stream uses these
+    tensors, so that one dropped right after the call (a workspace of the call's own
+    among them) is not handed out again while the kernels run."""
+    if isinstance(stream, _torch().cuda.Stream):
+        for t in tensors:
+            if t is not None and t.is_cuda:
+                t.record_stream(stream)
 
 
 def _dtype_code(t) -> int:
@@ -240,6 +254,7 @@ def argmax(logits, out=None, stream=None):
     st = library().arcs_argmax(_ptr(logits), _dtype_code(logits), B, V, stride, _ptr(out), _stream_ptr(stream))
     if st != OK:
         raise ArcsError(st, "arcs_argmax")
+    _used_on(stream, logits, out)
     return out
 
 
@@ -272,6 +287,7 @@ def top_logprobs(logits, n: int, temperature=None, out_ids=None, out_logprobs=No
                                      _stream_ptr(stream))
     if st != OK:
         raise ArcsError(st, "arcs_top_logprobs")
+    _used_on(stream, logits, temperature, out_ids, out_logprobs, out_status)
     return out_ids, out_logprobs
 
 
@@ -300,6 +316,7 @@ def commit_tokens(ids, V: int, position, ring, published, drained, fault, next_i
                                       _stream_ptr(stream))
     if st != OK:
         raise ArcsError(st, "arcs_commit_tokens")
+    _used_on(stream, ids, position, next_input)
 
 
 def _check_params(params, B):
@@ -343,6 +360,7 @@ def sample(logits, params, hist_ids=None, hist_offsets=None, seed: int = 0, step
                                ws_bytes, _stream_ptr(stream))
     if st != OK:
         raise ArcsError(st, "arcs_sample")
+    _used_on(stream, logits, params, hist_ids, hist_offsets, out, out_status, workspace)
     return out
 
 
@@ -365,6 +383,7 @@ def sample_noalloc(logits, params, hist_ids=None, hist_offsets=None, seed: int =
                                        int(step) & (2**64 - 1), _ptr(out), _ptr(out_status), _stream_ptr(stream))
     if st != OK:
         raise ArcsError(st, "arcs_sample_noalloc")
+    _used_on(stream, logits, params, hist_ids, hist_offsets, out, out_status)
     return out
 
 
@@ -405,6 +424,7 @@ def sample_dry(logits, params, hist_ids, hist_offsets, dry, breakers=None, seed:
                                    ws_bytes, _stream_ptr(stream))
     if st != OK:
         raise ArcsError(st, "arcs_sample_dry")
+    _used_on(stream, logits, params, hist_ids, hist_offsets, dry, breakers, out, out_status, workspace)
     return out
 
 
@@ -428,6 +448,7 @@ def sample_hybrid_nucleus(logits, temperature, top_p, budget: int = 32, seed: in
                                               _ptr(out_status), _stream_ptr(stream))
     if st != OK:
         raise ArcsError(st, "arcs_sample_hybrid_nucleus")
+    _used_on(stream, logits, temperature, top_p, out, out_kept, out_status)
     return out
 
 
@@ -468,6 +489,7 @@ def sample_keyed(logits, params, key, hist_ids=None, hist_offsets=None, advance:
                                      _stream_ptr(stream))
     if st != OK:
         raise ArcsError(st, "arcs_sample_keyed")
+    _used_on(stream, logits, params, key, hist_ids, hist_offsets, out, out_status, workspace)
     return out
 
 
@@ -521,7 +543,7 @@ def _head_stream(stream, device) -> int:
 def _work_on(device, stream):
     """The device and stream a head call runs on: the given stream, which has to
     be one of the tensors' device, or that device's current stream.  What the
-    call allocates then belongs to that stream."""
+    call allocates then belongs to that stream; _head_used says who else uses it."""
     torch = _torch()
     if stream is not None:
         if stream.device != device:
@@ -530,6 +552,14 @@ def _work_on(device, stream):
     if torch.cuda.current_device() != device.index:
         return torch.cuda.device(device)
     return _NO_CONTEXT
+
+
+def _head_used(stream, device, inputs, outputs) -> None:
+    """_used_on of a head call on a given stream, whose outputs, allocated on that
+    stream, the caller's current stream may go on with (ordered by the caller)."""
+    if stream is not None:
+        _used_on(stream, *inputs, *outputs)
+        _used_on(_torch().cuda.current_stream(device), *outputs)
 
 
 def _matrix(t, name: str, dtype, rows: int, cols: int, device):
@@ -587,6 +617,7 @@ def w4_logits(hidden, qweight, scales, group_size: int, zeros=None, out=None, ou
                                       _head_stream(stream, dev))
     if st != OK:
         raise ArcsError(st, "arcs_w4_logits")
+    _head_used(stream, dev, (hidden, qweight, scales, zeros, workspace), (out,))
     return out
 
 
@@ -653,6 +684,7 @@ def linear_cross_entropy(hidden, weight, targets, temperature=None, ignore_index
                                                  _head_stream(stream, dev))
     if st != OK:
         raise ArcsError(st, "arcs_linear_cross_entropy")
+    _head_used(stream, dev, (hidden, weight, targets, temperature, workspace), (out_loss, out_lse, out_status))
     return out_loss, out_lse
 
 
@@ -683,4 +715,6 @@ def linear_cross_entropy_backward(hidden, weight, targets, lse, grad_loss, tempe
             _head_stream(stream, dev))
     if st != OK:
         raise ArcsError(st, "arcs_linear_cross_entropy_backward")
+    _head_used(stream, dev, (hidden, weight, targets, temperature, lse, grad_loss, workspace),
+               (out_dhidden, out_dweight))
     return out_dhidden, out_dweight
