@@ -48,7 +48,8 @@ __device__ __forceinline__ CeRow ce_row(const CeArgs& a, int64_t n, int32_t targ
   r.target = target;
   r.a = kLog2e / T;
   r.c = (a.grad_loss[n] / T) / gmax;
-  // a float32 product would be off by 2^-24 |lse|, and every probability by that factor
+  // lse comes rounded to float32, so every probability is off by up to 2^-24 |lse|; a
+  // float32 product here would add as much again
   const double lse2 = (double)a.lse[n] * 1.4426950408889634074;
   r.lse2 = (float)lse2;
   r.rest = fabsf(r.lse2) < __builtin_inff() ? exp2f((float)((double)r.lse2 - lse2)) : 1.0f;

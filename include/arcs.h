@@ -516,6 +516,8 @@ int arcs_linear_cross_entropy(const void* hidden, int64_t hidden_stride, const v
  *   out_dweight[v] = sum_n dz[n, v] * hidden[n].
  * Rows that are ignored or refused have a zero gradient and add nothing.
  *   lse          device float[N], out_lse of the forward call on the same inputs
+ *                (its rounding to binary32, up to 2^-24 |lse|, is a relative error
+ *                of every p_v)
  *   grad_loss    device float[N]
  *   out_dhidden  device [N, D] of dtype, dense, or NULL (not wanted)
  *   out_dweight  device [V, D] of dtype, dense, or NULL (not wanted); written
@@ -523,8 +525,9 @@ int arcs_linear_cross_entropy(const void* hidden, int64_t hidden_stride, const v
  *   workspace    arcs_linear_cross_entropy_workspace_bytes(N, V, D, dtype, 1)
  * Sums are held in binary32.  For bfloat16 the matrix kernels hold dz of a
  * piece in bfloat16, in units of the largest |grad_loss / T| of the call (so
- * that equal weights are not rounded).  Other arguments and errors as the
- * forward call; outputs must not overlap inputs.
+ * that equal weights are not rounded); rows whose |grad_loss / T| is 2^-100 of
+ * the largest or less may have a gradient of 0, for float32 too.  Other
+ * arguments and errors as the forward call; outputs must not overlap inputs.
  */
 int arcs_linear_cross_entropy_backward(const void* hidden, int64_t hidden_stride, const void* weight,
                                        int64_t weight_stride, int dtype, int64_t N, int64_t V, int64_t D,
