@@ -124,6 +124,19 @@ def test_large_hidden_states_do_not_overflow(arcs, B, V, D, G, zeros):
 
 
 @pytest.mark.parametrize("zeros", [False, True])
+@pytest.mark.parametrize("B,V,D,G", SHAPES)
+def test_small_hidden_states(arcs, B, V, D, G, zeros):
+    """One channel of 2^-107 a row, the smallest that keeps every bit, the others 0."""
+    import torch
+    x = make(B, V, D, G, zeros, B + D, scale=(2.0 ** 10, 2.0 ** 11))
+    h = torch.zeros_like(x["hidden"])
+    at = (torch.arange(B, device="cuda") * 37) % D
+    h[torch.arange(B, device="cuda"), at] = 2.0 ** -107
+    x["hidden"] = h
+    assert torch.equal(call(arcs, x).double().cpu(), torch.from_numpy(definition(x)))
+
+
+@pytest.mark.parametrize("zeros", [False, True])
 @pytest.mark.parametrize("outlier", [False, True])
 @pytest.mark.parametrize("B,V,D,G", [(4, 500, 4096, 128), (24, 500, 4096, 32), (64, 500, 4096, 64), (100, 64, 4096, 128),
                                      (200, 300, 8192, 64)])
