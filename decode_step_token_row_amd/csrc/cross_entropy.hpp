@@ -68,7 +68,8 @@ struct CeArgs {
   float* slab;      // backward: partial sums of dhidden / gmax: [splits][N][D], or parts of tiles (matrix kernels)
   int splits;       // general kernel: of k in dhidden
   int workers;      // matrix kernels: workgroups that share dhidden's tiles
-  void* hc;         // backward, matrix kernels: [N][D] hidden states of the listed rows
+  void* hc;         // matrix kernels: [N][D] hidden states of the listed rows (backward, and forward
+                    // where one descriptor does not reach all rows)
 };
 
 // The workspace's parts, in bytes from its start.

@@ -8,14 +8,16 @@
 // back 16 bytes a lane; one whose rows run along m or n (the head in DHIDDEN,
 // both operands in DWEIGHT) through the transposing LDS read (bfloat16) or word
 // by word (float32), so no operand is stored twice.  The load writes LDS in lane
-// order, so bank conflicts (none are counted) are avoided by permuting the lanes'
+// order, so bank conflicts (none are counted in the loop, up to 7 % of the LDS
+// cycles in the results' way through LDS) are avoided by permuting the lanes'
 // global addresses:
 //   along k: a row's 128 bytes are 8 chunks, chunk c of row r at c ^ (r / 2 % 8);
 //   along m: a row's 32-byte chunks, chunk q of row k at q ^ 2 (k % 4).
 //
-// What bounds it: the products.  4,096 rows x 129,280 x 4,096 take 3.37 ms forward
-// (1,290 TFLOP/s; a large library product reaches 1,445 here), 256 x 256 tiles of
-// eight waves of 128 x 64.  Steps, at that size: the plain loop 3.75 ms;
+// What bounds it: the products.  4,096 rows x 129,280 x 4,096 take 3.4 to 3.6 ms
+// forward, by machine (1,210 to 1,270 TFLOP/s; a large library product reaches 1,445),
+// 256 x 256 tiles of eight waves of 128 x 64.  Steps, at that size, each beside the one
+// before on one machine: the plain loop 3.75 ms;
 // fragments read one k step ahead of the products, across the barrier too,
 // 3.58; the next tile's loads between the products instead of before them, 3.52;
 // workgroups that stay and load their next tile before they write the last one

@@ -26,7 +26,7 @@
 // nibbles' order and as the LDS holds them, so that a step is a plain copy to LDS
 // that takes no registers.  There the unpacking, the scaling of the groups' sums, the
 // LDS reads and the products take about the same time each, and overlap only in part:
-// 256 rows x 129,280 x 7,168 in groups of 64 with zero points take 557 us (850
+// 256 rows x 129,280 x 7,168 in groups of 64 with zero points take 550 to 560 us (850
 // TFLOP/s).  A tile of 128 rows x 32 columns a wave unpacks each weight twice for 256
 // rows; 64 x 64 a wave unpacks it four times and took 590 us where this one took 570.
 #include <hip/hip_runtime.h>
@@ -465,8 +465,14 @@ void launch_w4_batch(W4Args a, bool f32, hipStream_t stream) {
 template <int GROUP, bool ZERO, bool SF32>
 void launch_w4_typed(W4Args a, bool f32, hipStream_t stream) {
   // The smallest tile that holds the batch, and from 65 rows on 128 rows a tile.  Against
-  // 129,280 x 4,096 in groups of 128, in the tile taken and in the next larger one: 16
-  // rows 65 and 69 us, 32 rows 81 and 95 us, 64 rows 98 and 147 us.
+  // 129,280 x 7,168, in the tile taken and in the next larger one, without and with zero
+  // points (us):
+  //            groups of 32           64                     128
+  //   16 rows  162/157, 178/183       132/141, 143/165       127/133, 130/144
+  //   32 rows  163/301, 188/333       146/175, 170/198       138/154, 148/162
+  //   64 rows  304/332, 336/367       186/262, 210/273       165/237, 174/247
+  // (16 rows in groups of 32 are the one pair that is no better; against 4,096 it is
+  // 108/104 and 106/106.)
   if (a.B <= kW4FewRows) {
     launch_w4_rows<GROUP, ZERO, SF32>(a, f32, stream);
   } else if (a.B <= 32) {

@@ -451,6 +451,7 @@ int arcs_commit_tokens(const int32_t* ids, int64_t B, int64_t V, int32_t* next_i
  *                  256-byte aligned, not read before it is written; calls that
  *                  share one must be ordered on one stream; may be NULL when
  *                  none is needed
+ * The logits must not overlap an input.
  * Returns ARCS_OK or a negative arcs_status (nothing launched then):
  * ARCS_ERR_BAD_STRIDE for any stride below its row, or a stride of qweight,
  * scales or zeros above 2^21, ARCS_ERR_MISALIGNED for `hidden` or `qweight`
@@ -494,9 +495,10 @@ size_t arcs_w4_logits_workspace_bytes(int64_t B, int64_t D, int group_size);
  *               256-byte aligned, not read before it is written; calls that share
  *               one must be ordered on one stream
  * Products and sums are held in binary32.  The same call gives the same bits.
+ * Outputs must not overlap inputs or each other.
  * Rows on the 16-byte grid (pointers, strides and D, in each array and output;
  * weight_stride below 2^23 bytes) take the matrix kernels, others a general
- * kernel that is slower by a factor.
+ * kernel that takes 8 to 14 times as long in bfloat16 and 2 to 4 times in float32.
  * Returns ARCS_OK or a negative arcs_status (nothing launched then);
  * ARCS_ERR_BAD_BATCH also for more than 65,535 tiles of 128 rows, or more than
  * 2^23 tiles of 128 x 128 in [N, the larger of V and D].
