@@ -42,9 +42,11 @@ def make(N, V, D, dtype, seed):
     return h, w, t.to(torch.int32), T, rnd(N)
 
 
-def check(arcs, N, V, D, dtype, rounded, seed=1):
+def check(arcs, N, V, D, dtype, rounded, seed=1, spread=0):
     import torch
     h, w, t, T, g = make(N, V, D, dtype, seed)
+    if spread:  # upstream gradients from 2^-spread to 1
+        g = g * torch.exp2(-spread * torch.arange(N, device="cuda") / (N - 1)).float()
     loss, lse = arcs.linear_cross_entropy(h, w, t, temperature=T)
     dh, dw = arcs.linear_cross_entropy_backward(h, w, t, lse, g, temperature=T)
     rows = torch.nonzero(t != IGNORE)[:, 0]
@@ -101,3 +103,10 @@ def test_large_hidden_sizes(arcs, N, V, D, dtype, matrix):
 def test_general_kernel_does_not_round_dz(arcs, N, V, D):
     """bfloat16 rows off the 16-byte grid: only the inputs and the results are bfloat16."""
     check(arcs, N, V, D, "bf16", rounded=False)
+
+
+@pytest.mark.parametrize("D,dtype,matrix", [(64, "bf16", True), (64, "f32", True), (33, "bf16", False)])
+def test_upstream_gradients_of_very_different_sizes(arcs, D, dtype, matrix):
+    """dz is held in units of the call's largest upstream gradient: rows down to 2^-90 of it
+    keep the precision of their own gradient."""
+    check(arcs, 200, 1500, D, dtype, rounded=matrix and dtype == "bf16", spread=90)
