@@ -41,6 +41,12 @@ ERR_BAD_BUDGET = -13
 ERR_BAD_DRY = -14
 ERR_BAD_HIDDEN = -15
 ERR_BAD_GROUP = -16
+ERR_BAD_ACTIVATION = -17
+ERR_BAD_BIAS = -18
+ERR_BAD_MASK = -19
+ERR_OVERLAP = -20
+ERR_BAD_NORM = -21
+ERR_BAD_PLAN = -22
 DRY_MAX_WINDOW = 2048
 DRY_MAX_BREAKERS = 64
 NOALLOC_SCRATCH_BYTES = 16384
@@ -54,6 +60,10 @@ ROW_TIES_WIDE = 1  # arcs_row_params.flags bit
 ROW_HISTORY_TOO_LONG = 6
 ROW_VOCAB_TOO_LARGE = 7
 ROW_BAD_TARGET = 8
+ROW_BAD_MASK = 9
+ROW_NOTHING_ALLOWED = 10
+#: arcs_activation by the names `linear` takes
+ACTIVATIONS = {"none": 0, "relu": 1, "gelu": 2, "gelu_tanh": 3, "silu": 4, "softcap": 5}
 MAX_HIDDEN = 65536  # ARCS_MAX_HIDDEN
 MAX_HISTORY = 4096
 MAX_PENALTY_VOCAB = 262144
@@ -80,6 +90,9 @@ ROW_STATS_DTYPE = np.dtype(
      ("cut_value", "<f4"), ("max_logit", "<f4"), ("status", "<i4"), ("path", "<u4"),
      ("mass_total", "<f8"), ("mass_kept", "<f8"), ("uniform", "<f8"), ("reserved", "<u8")]
 )
+# struct arcs_tensor (32 bytes)
+TENSOR_DTYPE = np.dtype([("data", "<u8"), ("out", "<u8"), ("count", "<i8"), ("dtype", "<i4"), ("out_dtype", "<i4")])
+assert TENSOR_DTYPE.itemsize == 32
 assert ROW_PARAMS_DTYPE.itemsize == 32 and ROW_STATS_DTYPE.itemsize == 64
 
 
@@ -139,6 +152,28 @@ def library() -> ctypes.CDLL:
         lib.arcs_linear_cross_entropy_backward.restype = c_i
         lib.arcs_linear_cross_entropy_workspace_bytes.argtypes = [c_i64, c_i64, c_i64, c_i, c_i]
         lib.arcs_linear_cross_entropy_workspace_bytes.restype = ctypes.c_size_t
+        lib.arcs_linear.argtypes = [c_p, c_i64, c_p, c_i64, c_i, c_i64, c_i64, c_i64, c_p, c_i, ctypes.c_float, c_p,
+                                    c_i64, c_p, c_i, c_i64, c_p, c_p, ctypes.c_size_t, c_p]
+        lib.arcs_linear.restype = c_i
+        lib.arcs_linear_backward.argtypes = [c_p, c_i64, c_p, c_i64, c_i, c_i64, c_i64, c_i64, c_i, ctypes.c_float,
+                                             c_p, c_p, c_i, c_i64, c_p, c_p, c_p, c_p, ctypes.c_size_t, c_p]
+        lib.arcs_linear_backward.restype = c_i
+        for name in ("arcs_linear_workspace_bytes", "arcs_linear_backward_workspace_bytes"):
+            getattr(lib, name).argtypes = [c_i64, c_i64, c_i64, c_i, c_i]
+            getattr(lib, name).restype = ctypes.c_size_t
+        lib.arcs_adjust_logits.argtypes = [c_p, c_i, c_i64, c_i64, c_i64, c_p, c_p, c_p, c_p, c_p, c_p, c_p, c_i64,
+                                           c_i64, c_p, c_p, c_i, c_i64, c_p, c_p]
+        lib.arcs_adjust_logits.restype = c_i
+        lib.arcs_gradient_plan.argtypes = [c_p, c_i64, c_p, ctypes.c_size_t]
+        lib.arcs_gradient_plan.restype = c_i
+        lib.arcs_gradient_plan_bytes.argtypes = [c_p, c_i64]
+        lib.arcs_gradient_plan_bytes.restype = ctypes.c_size_t
+        lib.arcs_gradient_norm.argtypes = [c_p, ctypes.c_size_t, c_p, c_p, ctypes.c_size_t, c_p]
+        lib.arcs_gradient_norm.restype = c_i
+        lib.arcs_clip_gradients.argtypes = [c_p, ctypes.c_size_t, ctypes.c_double, c_p, c_p, ctypes.c_size_t, c_p]
+        lib.arcs_clip_gradients.restype = c_i
+        lib.arcs_gradient_workspace_bytes.argtypes = [ctypes.c_size_t]
+        lib.arcs_gradient_workspace_bytes.restype = ctypes.c_size_t
         lib.arcs_sample_workspace_bytes.argtypes = [c_i64, c_i64, c_i]
         lib.arcs_sample_workspace_bytes.restype = ctypes.c_size_t
         lib.arcs_long_history_workspace_bytes.argtypes = [c_i64, c_i64]
@@ -176,6 +211,13 @@ def w4_logits_workspace_bytes(B: int, D: int, group_size: int) -> int:
 def linear_cross_entropy_workspace_bytes(N: int, V: int, D: int, dtype: int, backward: bool = False) -> int:
     return int(library().arcs_linear_cross_entropy_workspace_bytes(int(N), int(V), int(D), int(dtype),
                                                                    1 if backward else 0))
+
+
+@functools.lru_cache(maxsize=256)
+def linear_workspace_bytes(N: int, V: int, D: int, dtype: int, rows_aligned: bool = False,
+                           backward: bool = False) -> int:
+    call = library().arcs_linear_backward_workspace_bytes if backward else library().arcs_linear_workspace_bytes
+    return int(call(int(N), int(V), int(D), int(dtype), 1 if rows_aligned else 0))
 
 
 # --------------------------------------------------------------------------
@@ -227,6 +269,12 @@ def _check_logits(logits):
 
 def _ptr(t) -> Optional[int]:
     return None if t is None else int(t.data_ptr())
+
+
+def _list_ptr(t) -> Optional[int]:
+    """_ptr of a list that may be given without elements, which torch has no address for:
+    the library tells it from one that is not given."""
+    return None if t is None else int(t.data_ptr()) or 256
 
 
 def params_to_device(params: np.ndarray, device="cuda"):
@@ -718,3 +766,270 @@ def linear_cross_entropy_backward(hidden, weight, targets, lse, grad_loss, tempe
     _head_used(stream, dev, (hidden, weight, targets, temperature, lse, grad_loss, workspace),
                (out_dhidden, out_dweight))
     return out_dhidden, out_dweight
+
+
+# --------------------------------------------------------------------------
+# linear layers
+# --------------------------------------------------------------------------
+def _rows_aligned(t, stride: int) -> bool:
+    """Whether the rows of a matrix are on the 16-byte grid, as arcs_linear asks."""
+    each = 16 // t.element_size()
+    return (t.data_ptr() % 16 == 0 and stride % each == 0 and t.shape[1] % each == 0
+            and stride * t.element_size() < 2**23)
+
+
+def _linear_inputs(hidden, weight, activation, softcap):
+    N, D, dev = _hidden_shape(hidden)
+    dt = _dtype_code_of(hidden, "hidden")
+    if weight.dim() != 2:
+        raise ValueError("weight must be [V, D]")
+    V = weight.shape[0]
+    hs = _matrix(hidden, "hidden", hidden.dtype, N, D, dev)
+    ws = _matrix(weight, "weight", hidden.dtype, V, D, dev)
+    act = ACTIVATIONS.get(activation)
+    if act is None:
+        raise ValueError(f"activation must be one of {', '.join(ACTIVATIONS)}")
+    return N, V, D, dev, dt, hs, ws, act, float(softcap), _rows_aligned(hidden, hs) and _rows_aligned(weight, ws)
+
+
+def linear(hidden, weight, bias=None, activation: str = "none", softcap: float = 0.0, residual=None, out=None,
+           out_dtype=None, out_pre=None, want_pre: bool = False, workspace=None, stream=None):
+    """arcs_linear: residual + act(hidden weight^T + bias), [N, V], in one pass: a head's
+    logits, ready for argmax, sample and top_logprobs, or a block in front of it.
+
+    ``hidden`` [N, D] and ``weight`` [V, D] bfloat16 or float32; ``bias`` [V] and
+    ``residual`` [N, V] of their type or None; ``activation`` one of ACTIVATIONS
+    ("softcap": softcap * tanh(z / softcap)).  ``out`` [N, V] bfloat16 or float32 with
+    contiguous rows (the residual itself is allowed), or None: a new tensor of ``out_dtype``
+    (the inputs' type).  With ``want_pre`` or ``out_pre`` (dense [N, V] of the inputs' type)
+    returns (out, pre): linear_backward needs pre where there is an activation.  The result
+    has no autograd graph.
+    """
+    torch = _torch()
+    N, V, D, dev, dt, hs, ws, act, cap, aligned = _linear_inputs(hidden, weight, activation, softcap)
+    if bias is not None:
+        _vector(bias, "bias", hidden.dtype, V, dev)
+    rs = 0 if residual is None else _matrix(residual, "residual", hidden.dtype, N, V, dev)
+    with _work_on(dev, stream):
+        if out is None:
+            out = torch.empty((N, V), dtype=hidden.dtype if out_dtype is None else out_dtype, device=dev)
+        elif out_dtype is not None and out.dtype != out_dtype:
+            raise ValueError("out is not of out_dtype")
+        odt = _dtype_code_of(out, "out")
+        os_ = _matrix(out, "out", out.dtype, N, V, dev)
+        if out_pre is None and want_pre:
+            out_pre = torch.empty((N, V), dtype=hidden.dtype, device=dev)
+        if out_pre is not None:
+            _vector(out_pre, "out_pre", hidden.dtype, N * V, dev)
+        workspace, ws_bytes = _head_workspace(workspace, linear_workspace_bytes(N, V, D, dt, aligned), dev)
+        st = library().arcs_linear(_ptr(hidden), hs, _ptr(weight), ws, dt, N, V, D, _ptr(bias), act, cap,
+                                   _ptr(residual), rs, _ptr(out), odt, os_, _ptr(out_pre), _ptr(workspace), ws_bytes,
+                                   _head_stream(stream, dev))
+    if st != OK:
+        raise ArcsError(st, "arcs_linear")
+    _head_used(stream, dev, (hidden, weight, bias, residual, workspace), (out, out_pre))
+    return out if out_pre is None else (out, out_pre)
+
+
+def linear_backward(hidden, weight, grad_out, pre=None, activation: str = "none", softcap: float = 0.0,
+                    out_dhidden=None, out_dweight=None, out_dbias=None, want_hidden: bool = True,
+                    want_weight: bool = True, want_bias: bool = False, workspace=None, stream=None):
+    """arcs_linear_backward: (dhidden [N, D], dweight [V, D], dbias [V]) of
+    sum(grad_out * out), in the inputs' type; None in place of one not wanted.
+
+    ``grad_out`` [N, V] bfloat16 or float32 with contiguous rows; ``pre`` the forward
+    call's (not needed without an activation).  The residual's gradient is grad_out.
+    """
+    torch = _torch()
+    N, V, D, dev, dt, hs, ws, act, cap, aligned = _linear_inputs(hidden, weight, activation, softcap)
+    gdt = _dtype_code_of(grad_out, "grad_out")
+    gs = _matrix(grad_out, "grad_out", grad_out.dtype, N, V, dev)
+    if pre is not None:
+        _vector(pre, "pre", hidden.dtype, N * V, dev)
+    with _work_on(dev, stream):
+        if want_hidden and out_dhidden is None:
+            out_dhidden = torch.empty((N, D), dtype=hidden.dtype, device=dev)
+        if want_weight and out_dweight is None:
+            out_dweight = torch.empty((V, D), dtype=hidden.dtype, device=dev)
+        if want_bias and out_dbias is None:
+            out_dbias = torch.empty(V, dtype=hidden.dtype, device=dev)
+        for t, name, n in ((out_dhidden, "out_dhidden", N * D), (out_dweight, "out_dweight", V * D),
+                           (out_dbias, "out_dbias", V)):
+            if t is not None:
+                _vector(t, name, hidden.dtype, n, dev)
+        workspace, ws_bytes = _head_workspace(workspace, linear_workspace_bytes(N, V, D, dt, aligned, True), dev)
+        st = library().arcs_linear_backward(_ptr(hidden), hs, _ptr(weight), ws, dt, N, V, D, act, cap, _ptr(pre),
+                                            _ptr(grad_out), gdt, gs, _ptr(out_dhidden), _ptr(out_dweight),
+                                            _ptr(out_dbias), _ptr(workspace), ws_bytes, _head_stream(stream, dev))
+    if st != OK:
+        raise ArcsError(st, "arcs_linear_backward")
+    _head_used(stream, dev, (hidden, weight, grad_out, pre, workspace), (out_dhidden, out_dweight, out_dbias))
+    return out_dhidden, out_dweight, out_dbias
+
+
+# --------------------------------------------------------------------------
+# logits before sampling
+# --------------------------------------------------------------------------
+def _lists(ids, offsets, name: str, B: int, dev):
+    """CSR lists of a batch: int32 ids and int64 [B + 1] offsets."""
+    torch = _torch()
+    if ids.dtype != torch.int32 or ids.device != dev or not ids.is_contiguous():
+        raise ValueError(f"{name}_ids must be a contiguous int32 tensor on {dev}")
+    _vector(offsets, f"{name}_offsets", torch.int64, B + 1, dev)
+
+
+def adjust_logits(logits, params=None, hist_ids=None, hist_offsets=None, bias_ids=None, bias_values=None,
+                  bias_offsets=None, mask=None, mask_rows=None, out=None, out_dtype=None, out_status=None, stream=None):
+    """arcs_adjust_logits: [B, V] logits with history penalties, biases and grammar masks
+    applied, ready for argmax, sample and top_logprobs (sample then takes the same
+    ``params`` and no history).
+
+    ``params`` sampling records (params_to_device), needed with a history; ``bias_ids`` int32,
+    ``bias_values`` float32 and ``bias_offsets`` int64 [B + 1]; ``mask`` int32 or uint32
+    [masks, >= ceil(V / 32)], bit v % 32 of word v / 32 set where token v is allowed;
+    ``mask_rows`` int32 [B], the mask of each row or -1, or None: row b has mask b.
+    ``out=logits`` works in place; None: a new tensor of ``out_dtype`` (the logits' type).
+    ``out_status`` int32 [B] takes the rows' codes (ROW_NOTHING_ALLOWED among them).
+    """
+    torch = _torch()
+    B, V, stride = _check_logits(logits)
+    dev = logits.device
+    dt = _dtype_code(logits)
+    stride = V if B == 1 else stride
+    if params is not None:
+        _vector(params, "params", torch.uint8, 32 * B, dev)
+    if (hist_ids is None) != (hist_offsets is None):
+        raise ValueError("hist_ids and hist_offsets go together")
+    if hist_ids is not None:
+        if params is None:
+            raise ValueError("a history needs params")
+        _lists(hist_ids, hist_offsets, "hist", B, dev)
+    if (bias_ids is None) != (bias_values is None) or (bias_ids is None) != (bias_offsets is None):
+        raise ValueError("bias_ids, bias_values and bias_offsets go together")
+    if bias_ids is not None:
+        _lists(bias_ids, bias_offsets, "bias", B, dev)
+        _vector(bias_values, "bias_values", torch.float32, bias_ids.numel(), dev)
+    masks = mask_stride = 0
+    if mask is not None:
+        if mask.dim() != 2 or mask.element_size() != 4 or mask.dtype.is_floating_point or mask.device != dev:
+            raise ValueError(f"mask must be an int32 matrix of words on {dev}")
+        if mask.stride(1) != 1 and mask.shape[1] > 1:
+            raise ValueError("mask rows must be contiguous (stride(1) == 1)")
+        if mask.shape[1] < (V + 31) // 32:
+            raise ValueError("mask rows must have a bit for every token")
+        masks, mask_stride = mask.shape[0], mask.shape[1] if mask.shape[0] == 1 else mask.stride(0)
+    if mask_rows is not None:
+        if mask is None:
+            raise ValueError("mask_rows needs a mask")
+        _vector(mask_rows, "mask_rows", torch.int32, B, dev)
+    with _work_on(dev, stream):
+        if out is None:
+            out = torch.empty((B, V), dtype=logits.dtype if out_dtype is None else out_dtype, device=dev)
+        elif out_dtype is not None and out.dtype != out_dtype:
+            raise ValueError("out is not of out_dtype")
+        odt = _dtype_code_of(out, "out")
+        os_ = _matrix(out, "out", out.dtype, B, V, dev)
+        if out_status is not None:
+            _vector(out_status, "out_status", torch.int32, B, dev)
+        st = library().arcs_adjust_logits(_ptr(logits), dt, B, V, stride, _ptr(params), _list_ptr(hist_ids),
+                                          _ptr(hist_offsets), _list_ptr(bias_ids), _list_ptr(bias_values),
+                                          _ptr(bias_offsets), _ptr(mask), masks, mask_stride, _ptr(mask_rows),
+                                          _ptr(out), odt, os_, _ptr(out_status), _head_stream(stream, dev))
+    if st != OK:
+        raise ArcsError(st, "arcs_adjust_logits")
+    _head_used(stream, dev, (logits, params, hist_ids, hist_offsets, bias_ids, bias_values, bias_offsets, mask,
+                             mask_rows), (out, out_status))
+    return out
+
+
+# --------------------------------------------------------------------------
+# the gradients' norm and clipping
+# --------------------------------------------------------------------------
+class TensorList:
+    """A list of gradients for gradient_norm and clip_gradients: its plan on the device,
+    made once (that copy is synchronous) and good as long as the tensors stay where they are.
+
+    ``tensors`` bfloat16 or float32, contiguous, on one device, of any shape; ``outs`` a
+    tensor of as many elements for each, where clip_gradients writes, or None: in place.  The
+    list keeps the tensors alive.  Memory that overlaps (the same tensor twice, say) is refused.
+    """
+
+    def __init__(self, tensors, outs=None):
+        torch = _torch()
+        self.tensors = list(tensors)
+        self.outs = self.tensors if outs is None else list(outs)
+        if len(self.outs) != len(self.tensors):
+            raise ValueError("outs must have a tensor for each of tensors")
+        if not self.tensors:
+            raise ValueError("a list of gradients needs a tensor")
+        self.device = self.tensors[0].device
+        for t, o in zip(self.tensors, self.outs):
+            for x in (t, o):
+                if not x.is_cuda or x.device != self.device or not x.is_contiguous():
+                    raise ValueError(f"gradients and outs must be contiguous device tensors on {self.device}")
+            if o.numel() != t.numel():
+                raise ValueError("each out must have as many elements as its gradient")
+        records = np.zeros(len(self.tensors), TENSOR_DTYPE)
+        records["data"] = [t.data_ptr() for t in self.tensors]
+        records["out"] = [o.data_ptr() for o in self.outs]
+        records["count"] = [t.numel() for t in self.tensors]
+        records["dtype"] = [_dtype_code_of(t, "a gradient") for t in self.tensors]
+        records["out_dtype"] = [_dtype_code_of(o, "an out") for o in self.outs]
+        self._refuse_overlaps(records)
+        n = len(records)
+        size = int(library().arcs_gradient_plan_bytes(records.ctypes.data, n))
+        plan = np.zeros(size, np.uint8)
+        st = library().arcs_gradient_plan(records.ctypes.data, n, plan.ctypes.data, size)
+        if st != OK:
+            raise ArcsError(st, "arcs_gradient_plan")
+        self.plan = torch.from_numpy(plan).to(self.device)
+        self.plan_bytes = size
+        self.workspace_bytes = int(library().arcs_gradient_workspace_bytes(size))
+
+    @staticmethod
+    def _refuse_overlaps(records):
+        """No two gradients and no two outs may share memory, and an out only with its own gradient,
+        whole."""
+        size = {DTYPE_BF16: 2, DTYPE_F32: 4}
+        ranges = set()
+        for r in records:
+            if r["count"] > 0:
+                data = (int(r["data"]), int(r["data"]) + int(r["count"]) * size[int(r["dtype"])])
+                out = (int(r["out"]), int(r["out"]) + int(r["count"]) * size[int(r["out_dtype"])])
+                for at in {data, out}:
+                    if at in ranges:
+                        raise ValueError("gradients and outs must not overlap")
+                    ranges.add(at)
+        last = 0
+        for lo, hi in sorted(ranges):
+            if lo < last:
+                raise ValueError("gradients and outs must not overlap")
+            last = hi
+
+
+def _norm_call(tensors, out_norm, workspace, stream, name, *more):
+    torch = _torch()
+    dev = tensors.device
+    with _work_on(dev, stream):
+        if out_norm is None:
+            out_norm = torch.empty(1, dtype=torch.float32, device=dev)
+        _vector(out_norm, "out_norm", torch.float32, 1, dev)
+        workspace, ws_bytes = _head_workspace(workspace, tensors.workspace_bytes, dev)
+        st = getattr(library(), name)(_list_ptr(tensors.plan), tensors.plan_bytes, *more, _ptr(out_norm),
+                                      _ptr(workspace), ws_bytes, _head_stream(stream, dev))
+    if st != OK:
+        raise ArcsError(st, name)
+    if stream is not None:
+        _head_used(stream, dev, (tensors.plan, workspace, *tensors.tensors), (out_norm, *tensors.outs))
+    return out_norm
+
+
+def gradient_norm(tensors: TensorList, out_norm=None, workspace=None, stream=None):
+    """arcs_gradient_norm: sqrt(sum of all squares) of the list's gradients, float32 [1] on the device."""
+    return _norm_call(tensors, out_norm, workspace, stream, "arcs_gradient_norm")
+
+
+def clip_gradients(tensors: TensorList, max_norm: float, out_norm=None, workspace=None, stream=None):
+    """arcs_clip_gradients: scales the list's gradients by max_norm / norm where their norm is
+    above max_norm (and finite), to the list's outs or in place; returns the norm before, float32 [1]."""
+    return _norm_call(tensors, out_norm, workspace, stream, "arcs_clip_gradients", float(max_norm))

@@ -11,6 +11,7 @@
 #include "arcs.h"
 #include "cross_entropy.hpp"
 #include "launch.hpp"
+#include "linear.hpp"
 
 // Device scratch of arcs_sample_noalloc: one copy per GPU, held until the
 // process ends, at its own address on each device.  Host code never uses the
@@ -182,6 +183,97 @@ arcs::CeArgs cross_entropy_args(const void* hidden, int64_t hidden_stride, const
   a.workers = p.workers;
   a.hc = w + p.hc;
   return a;
+}
+
+uintptr_t element_size(int dtype) { return dtype == ARCS_DTYPE_BF16 ? 2 : 4; }
+
+// Sizes the linear layer takes: tile counts fit an int, and a tile's rows of dz 31 bits.
+int linear_sizes(int64_t N, int64_t V, int64_t D, int dtype, bool backward) {
+  if (dtype != ARCS_DTYPE_BF16 && dtype != ARCS_DTYPE_F32) return ARCS_ERR_BAD_DTYPE;
+  if (N <= 0 || N > int64_t(1) << 22) return ARCS_ERR_BAD_BATCH;
+  if (V <= 0 || V > (backward ? (int64_t(1) << 21) - 8 : int64_t(1) << 24)) return ARCS_ERR_BAD_VOCAB;
+  if (N * V > int64_t(1) << 40) return ARCS_ERR_BAD_BATCH;
+  if (D <= 0 || D > ARCS_MAX_HIDDEN) return ARCS_ERR_BAD_HIDDEN;
+  return ARCS_OK;
+}
+
+// Arguments the two directions of the linear layer share.
+int check_linear(const void* hidden, int64_t hidden_stride, const void* weight, int64_t weight_stride, int dtype,
+                 int64_t N, int64_t V, int64_t D, int activation, float softcap, bool backward,
+                 const void* workspace, size_t workspace_bytes, bool* aligned) {
+  if (hidden == nullptr || weight == nullptr) return ARCS_ERR_NULL_POINTER;
+  int st = linear_sizes(N, V, D, dtype, backward);
+  if (st != ARCS_OK) return st;
+  if (hidden_stride < D || weight_stride < D) return ARCS_ERR_BAD_STRIDE;
+  if (activation < ARCS_ACT_NONE || activation > ARCS_ACT_SOFTCAP ||
+      (activation == ARCS_ACT_SOFTCAP && !(softcap > 0.0f && softcap <= 3.402823466e38f)))
+    return ARCS_ERR_BAD_ACTIVATION;
+  if (misaligned(hidden, element_size(dtype)) || misaligned(weight, element_size(dtype))) return ARCS_ERR_MISALIGNED;
+  *aligned = arcs::linear_rows_aligned(hidden, hidden_stride, D, dtype) &&
+             arcs::linear_rows_aligned(weight, weight_stride, D, dtype);
+  const size_t need = arcs::linear_plan(N, V, D, dtype, *aligned, backward).total;
+  if (workspace_bytes < need) return ARCS_ERR_WORKSPACE_TOO_SMALL;
+  if (need > 0 && workspace == nullptr) return ARCS_ERR_NULL_POINTER;
+  if (need > 0 && misaligned(workspace, 256)) return ARCS_ERR_MISALIGNED;
+  return ARCS_OK;
+}
+
+// Whether any two rows of two row-major arrays share bytes.  Rows of equal strides may lie
+// between each other's.
+bool rows_overlap(const void* p, int64_t p_stride, int64_t p_size, const void* q, int64_t q_stride, int64_t q_size,
+                  int64_t rows, int64_t columns) {
+  const __int128 p0 = (intptr_t)p, q0 = (intptr_t)q, ps = (__int128)p_stride * p_size, qs = (__int128)q_stride * q_size;
+  const __int128 pl = (__int128)columns * p_size, ql = (__int128)columns * q_size;
+  if (p0 + ps * (rows - 1) + pl <= q0 || q0 + qs * (rows - 1) + ql <= p0) return false;
+  if (ps != qs || rows == 1) return true;
+  const __int128 d = ((q0 - p0) % ps + ps) % ps;
+  return d < pl || ps - d < ql;
+}
+
+// A list of gradients, and how many pieces it has.
+int check_tensors(const arcs_tensor* tensors, int64_t n, int64_t* pieces) {
+  if (n < 0) return ARCS_ERR_BAD_BATCH;
+  if (n > 0 && tensors == nullptr) return ARCS_ERR_NULL_POINTER;
+  int64_t total = 0;
+  *pieces = 0;
+  for (int64_t i = 0; i < n; ++i) {
+    const arcs_tensor& t = tensors[i];
+    if ((t.dtype != ARCS_DTYPE_BF16 && t.dtype != ARCS_DTYPE_F32) ||
+        (t.out_dtype != ARCS_DTYPE_BF16 && t.out_dtype != ARCS_DTYPE_F32))
+      return ARCS_ERR_BAD_DTYPE;
+    if (t.count < 0 || t.count > (int64_t(1) << 40) - total) return ARCS_ERR_BAD_PLAN;
+    if (t.count > 0 && t.data == nullptr) return ARCS_ERR_NULL_POINTER;
+    if (misaligned(t.data, element_size(t.dtype)) || misaligned(t.out, element_size(t.out_dtype)))
+      return ARCS_ERR_MISALIGNED;
+    if (t.count > 0 && t.out == t.data && t.out_dtype != t.dtype) return ARCS_ERR_OVERLAP;
+    total += t.count;
+    *pieces += (t.count + arcs::kNormPiece - 1) / arcs::kNormPiece;
+  }
+  return ARCS_OK;
+}
+
+size_t norm_workspace(size_t plan_bytes) {
+  const int groups = arcs::norm_groups((int64_t)(plan_bytes / sizeof(arcs::NormPiece)));
+  return groups > 0 ? ((size_t)groups * 8 + 255) / 256 * 256 : 0;
+}
+
+int norm_impl(const void* plan, size_t plan_bytes, double max_norm, float* out_norm, void* workspace,
+              size_t workspace_bytes, bool clip, void* stream) {
+  if (out_norm == nullptr || (plan == nullptr && plan_bytes > 0)) return ARCS_ERR_NULL_POINTER;
+  if (plan_bytes % sizeof(arcs::NormPiece) != 0) return ARCS_ERR_BAD_PLAN;
+  if (misaligned(plan, 8) || misaligned(out_norm, 4)) return ARCS_ERR_MISALIGNED;
+  const size_t need = norm_workspace(plan_bytes);
+  if (workspace_bytes < need) return ARCS_ERR_WORKSPACE_TOO_SMALL;
+  if (need > 0 && workspace == nullptr) return ARCS_ERR_NULL_POINTER;
+  if (need > 0 && misaligned(workspace, 256)) return ARCS_ERR_MISALIGNED;
+  arcs::NormArgs a = {};
+  a.plan = (const arcs::NormPiece*)plan;
+  a.pieces = (int64_t)(plan_bytes / sizeof(arcs::NormPiece));
+  a.max_norm = max_norm;
+  a.out_norm = out_norm;
+  a.sums = (double*)workspace;
+  hipError_t e = arcs::launch_norm(a, clip, (hipStream_t)stream);
+  return e == hipSuccess ? ARCS_OK : ARCS_ERR_LAUNCH;
 }
 
 }  // namespace
@@ -412,6 +504,178 @@ size_t arcs_linear_cross_entropy_workspace_bytes(int64_t N, int64_t V, int64_t D
   return p.fits ? p.total : 0;
 }
 
+int arcs_linear(const void* hidden, int64_t hidden_stride, const void* weight, int64_t weight_stride, int dtype,
+                int64_t N, int64_t V, int64_t D, const void* bias, int activation, float softcap,
+                const void* residual, int64_t residual_stride, void* out, int out_dtype, int64_t out_stride,
+                void* out_pre, void* workspace, size_t workspace_bytes, void* stream) {
+  if (out == nullptr) return ARCS_ERR_NULL_POINTER;
+  bool aligned;
+  int st = check_linear(hidden, hidden_stride, weight, weight_stride, dtype, N, V, D, activation, softcap, false,
+                        workspace, workspace_bytes, &aligned);
+  if (st != ARCS_OK) return st;
+  if (out_dtype != ARCS_DTYPE_BF16 && out_dtype != ARCS_DTYPE_F32) return ARCS_ERR_BAD_DTYPE;
+  if (out_stride < V || (residual != nullptr && residual_stride < V)) return ARCS_ERR_BAD_STRIDE;
+  const uintptr_t es = element_size(dtype);
+  if (misaligned(bias, es) || misaligned(residual, es) || misaligned(out_pre, es) ||
+      misaligned(out, element_size(out_dtype)))
+    return ARCS_ERR_MISALIGNED;
+  if (residual == out && (out_dtype != dtype || residual_stride != out_stride)) return ARCS_ERR_OVERLAP;
+  arcs::LinearArgs a = {};
+  a.hidden = hidden;
+  a.hidden_stride = hidden_stride;
+  a.weight = weight;
+  a.weight_stride = weight_stride;
+  a.N = N;
+  a.V = V;
+  a.D = D;
+  a.act = activation;
+  a.cap = softcap;
+  a.bias = bias;
+  a.residual = residual;
+  a.residual_stride = residual_stride;
+  a.out = out;
+  a.out_stride = out_stride;
+  a.out_bf16 = out_dtype == ARCS_DTYPE_BF16;
+  a.out_pre = out_pre;
+  a.workspace = (char*)workspace;
+  hipError_t e = arcs::launch_linear(a, dtype, aligned, (hipStream_t)stream);
+  return e == hipSuccess ? ARCS_OK : ARCS_ERR_LAUNCH;
+}
+
+int arcs_linear_backward(const void* hidden, int64_t hidden_stride, const void* weight, int64_t weight_stride,
+                         int dtype, int64_t N, int64_t V, int64_t D, int activation, float softcap,
+                         const void* pre, const void* grad_out, int grad_dtype, int64_t grad_stride,
+                         void* out_dhidden, void* out_dweight, void* out_dbias, void* workspace,
+                         size_t workspace_bytes, void* stream) {
+  if (grad_out == nullptr || (out_dhidden == nullptr && out_dweight == nullptr && out_dbias == nullptr))
+    return ARCS_ERR_NULL_POINTER;
+  bool aligned;
+  int st = check_linear(hidden, hidden_stride, weight, weight_stride, dtype, N, V, D, activation, softcap, true,
+                        workspace, workspace_bytes, &aligned);
+  if (st != ARCS_OK) return st;
+  if (activation != ARCS_ACT_NONE && pre == nullptr) return ARCS_ERR_NULL_POINTER;
+  if (grad_dtype != ARCS_DTYPE_BF16 && grad_dtype != ARCS_DTYPE_F32) return ARCS_ERR_BAD_DTYPE;
+  if (grad_stride < V) return ARCS_ERR_BAD_STRIDE;
+  const uintptr_t es = element_size(dtype);
+  if (misaligned(pre, es) || misaligned(grad_out, element_size(grad_dtype)) || misaligned(out_dhidden, es) ||
+      misaligned(out_dweight, es) || misaligned(out_dbias, es))
+    return ARCS_ERR_MISALIGNED;
+  arcs::LinearArgs a = {};
+  a.hidden = hidden;
+  a.hidden_stride = hidden_stride;
+  a.weight = weight;
+  a.weight_stride = weight_stride;
+  a.N = N;
+  a.V = V;
+  a.D = D;
+  a.act = activation;
+  a.cap = softcap;
+  a.pre = pre;
+  a.grad = grad_out;
+  a.grad_stride = grad_stride;
+  a.grad_bf16 = grad_dtype == ARCS_DTYPE_BF16;
+  a.out_dhidden = out_dhidden;
+  a.out_dweight = out_dweight;
+  a.out_dbias = out_dbias;
+  a.workspace = (char*)workspace;
+  hipError_t e = arcs::launch_linear_backward(a, dtype, aligned, (hipStream_t)stream);
+  return e == hipSuccess ? ARCS_OK : ARCS_ERR_LAUNCH;
+}
+
+size_t arcs_linear_workspace_bytes(int64_t N, int64_t V, int64_t D, int dtype, int rows_aligned) {
+  return linear_sizes(N, V, D, dtype, false) == ARCS_OK ? arcs::linear_plan(N, V, D, dtype, rows_aligned != 0, false).total : 0;
+}
+
+size_t arcs_linear_backward_workspace_bytes(int64_t N, int64_t V, int64_t D, int dtype, int rows_aligned) {
+  return linear_sizes(N, V, D, dtype, true) == ARCS_OK ? arcs::linear_plan(N, V, D, dtype, rows_aligned != 0, true).total : 0;
+}
+
+int arcs_adjust_logits(const void* logits, int dtype, int64_t B, int64_t V, int64_t row_stride,
+                       const arcs_row_params* params, const int32_t* hist_ids, const int64_t* hist_offsets,
+                       const int32_t* bias_ids, const float* bias_values, const int64_t* bias_offsets,
+                       const uint32_t* mask, int64_t masks, int64_t mask_stride, const int32_t* mask_rows,
+                       void* out, int out_dtype, int64_t out_stride, int32_t* out_status, void* stream) {
+  int st = check_common(logits, dtype, B, V, row_stride, out);
+  if (st != ARCS_OK) return st;
+  if (out_dtype != ARCS_DTYPE_BF16 && out_dtype != ARCS_DTYPE_F32) return ARCS_ERR_BAD_DTYPE;
+  if (!arcs::adjust_fits(B, V)) return ARCS_ERR_BAD_BATCH;
+  if (out_stride < V) return ARCS_ERR_BAD_STRIDE;
+  if ((hist_ids == nullptr) != (hist_offsets == nullptr)) return ARCS_ERR_BAD_HISTORY;
+  if (hist_ids != nullptr && params == nullptr) return ARCS_ERR_NULL_POINTER;
+  if ((bias_ids == nullptr) != (bias_values == nullptr) || (bias_ids == nullptr) != (bias_offsets == nullptr))
+    return ARCS_ERR_BAD_BIAS;
+  if (mask == nullptr ? mask_rows != nullptr : masks < (mask_rows != nullptr ? 1 : B)) return ARCS_ERR_BAD_MASK;
+  if (mask != nullptr && mask_stride < (V + 31) / 32) return ARCS_ERR_BAD_STRIDE;
+  if (misaligned(params, 4) || misaligned(hist_ids, 4) || misaligned(hist_offsets, 8) || misaligned(bias_ids, 4) ||
+      misaligned(bias_values, 4) || misaligned(bias_offsets, 8) || misaligned(mask, 4) || misaligned(mask_rows, 4) ||
+      misaligned(out, element_size(out_dtype)) || misaligned(out_status, 4))
+    return ARCS_ERR_MISALIGNED;
+  const bool in_place = out == logits && out_dtype == dtype && (B == 1 || out_stride == row_stride);
+  if (!in_place && rows_overlap(logits, row_stride, element_size(dtype), out, out_stride, element_size(out_dtype), B, V))
+    return ARCS_ERR_OVERLAP;
+  arcs::AdjustArgs a = {};
+  a.logits = logits;
+  a.V = V;
+  a.stride = row_stride;
+  a.params = params;
+  a.hist_ids = hist_ids;
+  a.hist_offsets = hist_offsets;
+  a.bias_ids = bias_ids;
+  a.bias_values = bias_values;
+  a.bias_offsets = bias_offsets;
+  a.mask = mask;
+  a.masks = masks;
+  a.mask_stride = mask_stride;
+  a.mask_rows = mask_rows;
+  a.out = out;
+  a.out_stride = out_stride;
+  a.in_place = in_place;
+  a.out_status = out_status;
+  hipError_t e = arcs::launch_adjust(a, dtype, out_dtype, B, (hipStream_t)stream);
+  return e == hipSuccess ? ARCS_OK : ARCS_ERR_LAUNCH;
+}
+
+size_t arcs_gradient_plan_bytes(const arcs_tensor* tensors, int64_t n) {
+  int64_t pieces;
+  return check_tensors(tensors, n, &pieces) == ARCS_OK ? (size_t)pieces * sizeof(arcs::NormPiece) : 0;
+}
+
+int arcs_gradient_plan(const arcs_tensor* tensors, int64_t n, void* plan, size_t plan_bytes) {
+  int64_t pieces;
+  int st = check_tensors(tensors, n, &pieces);
+  if (st != ARCS_OK) return st;
+  if (plan_bytes != (size_t)pieces * sizeof(arcs::NormPiece)) return ARCS_ERR_BAD_PLAN;
+  if (pieces > 0 && plan == nullptr) return ARCS_ERR_NULL_POINTER;
+  if (misaligned(plan, 8)) return ARCS_ERR_MISALIGNED;
+  arcs::NormPiece* to = (arcs::NormPiece*)plan;
+  for (int64_t i = 0; i < n; ++i) {
+    const arcs_tensor& t = tensors[i];
+    for (int64_t at = 0; at < t.count; at += arcs::kNormPiece) {
+      arcs::NormPiece p = {};
+      p.from = (const char*)t.data + at * element_size(t.dtype);
+      p.to = t.out == nullptr ? nullptr : (char*)t.out + at * element_size(t.out_dtype);
+      p.count = (int32_t)(t.count - at < arcs::kNormPiece ? t.count - at : arcs::kNormPiece);
+      p.bf16 = t.dtype == ARCS_DTYPE_BF16;
+      p.to_bf16 = t.out_dtype == ARCS_DTYPE_BF16;
+      *to++ = p;
+    }
+  }
+  return ARCS_OK;
+}
+
+int arcs_gradient_norm(const void* plan, size_t plan_bytes, float* out_norm, void* workspace,
+                       size_t workspace_bytes, void* stream) {
+  return norm_impl(plan, plan_bytes, 0.0, out_norm, workspace, workspace_bytes, false, stream);
+}
+
+int arcs_clip_gradients(const void* plan, size_t plan_bytes, double max_norm, float* out_norm, void* workspace,
+                        size_t workspace_bytes, void* stream) {
+  if (!(max_norm >= 0.0)) return ARCS_ERR_BAD_NORM;
+  return norm_impl(plan, plan_bytes, max_norm, out_norm, workspace, workspace_bytes, true, stream);
+}
+
+size_t arcs_gradient_workspace_bytes(size_t plan_bytes) { return norm_workspace(plan_bytes); }
+
 size_t arcs_long_history_workspace_bytes(int64_t B, int64_t V) {
   if (B <= 0 || V <= 0) return 0;
   const unsigned __int128 n = (unsigned __int128)B * (unsigned __int128)V * 4u;
@@ -438,6 +702,12 @@ const char* arcs_status_string(int code) {
       return "the shape needs more workspace than arcs_sample_noalloc's scratch (ARCS_NOALLOC_SCRATCH_BYTES)";
     case ARCS_ERR_BAD_HIDDEN: return "hidden size D must be in [1, ARCS_MAX_HIDDEN]";
     case ARCS_ERR_BAD_GROUP: return "group_size must be 32, 64 or 128 and divide D";
+    case ARCS_ERR_BAD_ACTIVATION: return "activation must be an arcs_activation, softcap positive and finite";
+    case ARCS_ERR_BAD_BIAS: return "bias ids, values and offsets must all be NULL or all be set";
+    case ARCS_ERR_BAD_MASK: return "mask_rows without a mask, or fewer masks than rows";
+    case ARCS_ERR_OVERLAP: return "an output overlaps an input";
+    case ARCS_ERR_BAD_NORM: return "max_norm must be >= 0";
+    case ARCS_ERR_BAD_PLAN: return "a gradient's count or the plan's size is not valid";
     case ARCS_ERR_LAUNCH: return "kernel launch failed";
     case ARCS_ERR_MISALIGNED: return "an array or its rows are not aligned as the call asks for";
     case ARCS_ERR_BAD_HISTORY: return "hist_ids and hist_offsets must both be NULL or both be set";
@@ -451,6 +721,8 @@ const char* arcs_status_string(int code) {
     case ARCS_ROW_HISTORY_TOO_LONG: return "row: penalties need at most ARCS_MAX_HISTORY distinct history ids";
     case ARCS_ROW_VOCAB_TOO_LARGE: return "row: penalties need V <= ARCS_MAX_PENALTY_VOCAB";
     case ARCS_ROW_BAD_TARGET: return "row: target outside [0, V) and not ignore_index";
+    case ARCS_ROW_BAD_MASK: return "row: mask row outside [0, masks) and not -1";
+    case ARCS_ROW_NOTHING_ALLOWED: return "row: the mask leaves no token";
     default: return "unknown status";
   }
 }

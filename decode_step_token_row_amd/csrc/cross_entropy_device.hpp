@@ -6,11 +6,9 @@
 
 #include "cross_entropy.hpp"
 #include "device_common.hpp"
+#include "mfma_tile.hpp"
 
 namespace arcs {
-
-typedef float f32x16 __attribute__((ext_vector_type(16)));
-typedef float f32x4 __attribute__((ext_vector_type(4)));
 
 constexpr float kLog2e = 1.44269504088896340736f;
 

@@ -31,14 +31,9 @@
 #include "cross_entropy_device.hpp"
 #include "launch.hpp"
 #include "lds_load.hpp"
+#include "mfma_tile.hpp"
 
 namespace arcs {
-
-__device__ __forceinline__ u32x4 uniform4(u32x4 d) {
-#pragma unroll
-  for (int e = 0; e < 4; ++e) d[e] = __builtin_amdgcn_readfirstlane(d[e]);
-  return d;
-}
 
 template <typename T, int MODE, int WM, int WN, int MT, int NT, int S>
 struct CeTile {
@@ -57,32 +52,6 @@ struct CeTile {
   static constexpr int kOutM = MT % 2 == 0 && S * kStage + kWaves * 32 * 64 * 2 <= 163840 ? 64 : 32;
   static constexpr int kOutBytes = 32 * kOutM * 2, kLds = S * kStage + (kOut ? kWaves * kOutBytes : 0);
 };
-
-// Tile `id` of mt x nt: bands of eight along m, in a band m first.
-__device__ __forceinline__ void ce_tile_place(int id, int mt, int nt, int64_t& m, int64_t& n) {
-  const int band = id / (8 * nt), in = id - band * 8 * nt, high = mt - band * 8 < 8 ? mt - band * 8 : 8;
-  m = band * 8 + in % high;
-  n = in / high;
-}
-__device__ __forceinline__ int ce_tile_index(int m, int n, int mt, int nt) {
-  const int band = m / 8, high = mt - band * 8 < 8 ? mt - band * 8 : 8;
-  return band * 8 * nt + n * high + m - band * 8;
-}
-
-// Where a lane's 16 bytes of load `inst` lie in its tile: row and element in the row.
-template <typename T, int W>
-__device__ __forceinline__ void outer_place(int inst, int lane, int& k, int& col) {
-  constexpr int kLanes = W * (int)sizeof(T) / 16;
-  k = inst * (64 / kLanes) + lane / kLanes;
-  const int p = lane % kLanes;
-  const int turn = W >= 128 ? (k & 3) << 1 : W == 64 ? ((k >> 1) & 1) << 1 : 0;
-  col = sizeof(T) == 2 ? ((p >> 1) ^ turn) * 16 + (p & 1) * 8 : p * 4;
-}
-template <typename T>
-__device__ __forceinline__ void inner_place(int inst, int lane, int& r, int& k) {
-  r = inst * 8 + (lane >> 3);
-  k = ((lane & 7) ^ ((r >> 1) & 7)) * (16 / (int)sizeof(T));
-}
 
 template <typename T, int MODE, int WM, int WN, int MT, int NT, int S>
 __global__ __launch_bounds__(WM* WN * 64, 2) void ce_tile_kernel(CeArgs a, CePiece pc) {
@@ -129,7 +98,7 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void ce_tile_kernel(CeArgs a, CePie
   const int64_t step_a = C::kLogits ? 128 : MODE == kCeDhidden ? kTK * a.weight_stride * E : kTK * a.D * E;
   const int64_t step_b = MODE == kCeDweight ? kTK * a.ds_ld * E : 128;
   auto place = [&](int job) {
-    ce_tile_place(job, mt, nt, m0, n0);
+    tile_place(job, mt, nt, m0, n0);
     m0 *= BM;
     n0 *= BN;
     int64_t k_lo = 0, k_hi = C::kLogits ? a.D : MODE == kCeDhidden ? pc.len : count;
@@ -536,7 +505,7 @@ __global__ __launch_bounds__(256) void ce_dhidden_parts_kernel(CeArgs a, int BN)
   const int mt = (int)((a.D + BM - 1) / BM), nt = (a.head->count + BN - 1) / BN, all = mt * nt;
   f32x4 v = {0.0f, 0.0f, 0.0f, 0.0f};
   if (i >= 0) {
-    const int job = ce_tile_index(m, i / BN, mt, nt);
+    const int job = tile_index(m, i / BN, mt, nt);
     const int lo = (int)((int64_t)job * a.workers / all), hi = (int)(((int64_t)(job + 1) * a.workers + all - 1) / all);
     const float* p = a.slab + ((int64_t)job * BN + i % BN) * BM + d % BM;
 #pragma unroll 4

@@ -130,6 +130,54 @@ struct W4Args {
 size_t w4_workspace_bytes(int64_t B, int64_t D);
 hipError_t launch_w4_logits(W4Args a, int scale_dtype, int logits_dtype, int group, void* workspace, hipStream_t stream);
 
+// One adjustment of logits (arcs_adjust_logits).
+struct AdjustArgs {
+  const void* logits;
+  int64_t V;
+  int64_t stride;
+  const arcs_row_params* params;  // [B], or NULL: no penalties
+  const int32_t* hist_ids;
+  const int64_t* hist_offsets;
+  const int32_t* bias_ids;
+  const float* bias_values;
+  const int64_t* bias_offsets;
+  const uint32_t* mask;           // [masks, mask_stride], or NULL
+  int64_t masks, mask_stride;
+  const int32_t* mask_rows;       // [B], or NULL: row b has mask b
+  void* out;
+  int64_t out_stride;
+  int in_place;                   // out is logits
+  int32_t* out_status;            // [B], or NULL
+  // set by the launch
+  int slices, per_row;
+};
+// Whether the launch grid holds the call.
+bool adjust_fits(int64_t B, int64_t V);
+hipError_t launch_adjust(AdjustArgs a, int dtype, int out_dtype, int64_t B, hipStream_t stream);
+
+// A piece of a gradient, as the plan lists it.
+struct NormPiece {
+  const void* from;
+  void* to;
+  int32_t count;
+  int32_t bf16, to_bf16;
+  int32_t pad;
+};
+static_assert(sizeof(NormPiece) == 32, "plan record");
+// One norm of gradients, or clipping to it (arcs_gradient_norm, arcs_clip_gradients).
+struct NormArgs {
+  const NormPiece* plan;
+  int64_t pieces;
+  double max_norm;
+  float* out_norm;
+  double* sums;  // workspace: [groups]
+  int groups;    // set by the launch
+};
+constexpr int64_t kNormPiece = 4096;  // elements of a piece at most
+// Workgroups of the launches.
+inline int norm_groups(int64_t pieces) { return (int)(pieces < 2048 ? pieces : 2048); }
+hipError_t launch_norm(NormArgs a, bool clip, hipStream_t stream);
+
 hipError_t launch_argmax(const void* logits, int dtype, int64_t B, int64_t V, int64_t stride,
                          bool vec, int32_t* out, hipStream_t stream);
 hipError_t launch_sample(const SampleArgs& a, int dtype, int64_t B, bool vec, hipStream_t stream);

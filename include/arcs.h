@@ -1,7 +1,8 @@
 /*
  * arcs.h -- on-device batched token sampling for AMD Instinct MI355X (gfx950),
- * and the vocabulary head around it: logits from 4-bit weights, and the
- * cross entropy of given tokens with its gradients.
+ * and the vocabulary head around it: logits from 4-bit weights, linear layers
+ * with their gradients, the cross entropy of given tokens with its gradients,
+ * adjustments of logits before sampling, and the gradients' norm and clipping.
  *
  * The library turns a [B, V] logits tensor that already lives in GPU memory
  * into one token id per row, without copying the logits to the host.  The
@@ -59,7 +60,13 @@ typedef enum arcs_status {
   ARCS_ERR_BAD_BUDGET = -13,         /* arcs_sample_hybrid_nucleus: budget outside [0, 4096] */
   ARCS_ERR_BAD_DRY = -14,            /* arcs_sample_dry: breakers NULL or n_breakers outside [0, 64] */
   ARCS_ERR_BAD_HIDDEN = -15,         /* hidden size D outside [1, ARCS_MAX_HIDDEN] */
-  ARCS_ERR_BAD_GROUP = -16           /* arcs_w4_logits: group_size not 32, 64 or 128, or no divisor of D */
+  ARCS_ERR_BAD_GROUP = -16,          /* arcs_w4_logits: group_size not 32, 64 or 128, or no divisor of D */
+  ARCS_ERR_BAD_ACTIVATION = -17,     /* arcs_linear: no arcs_activation, or softcap not positive and finite */
+  ARCS_ERR_BAD_BIAS = -18,           /* arcs_adjust_logits: some of the three bias arrays are NULL, not all */
+  ARCS_ERR_BAD_MASK = -19,           /* arcs_adjust_logits: mask_rows without a mask, or fewer masks than rows */
+  ARCS_ERR_OVERLAP = -20,            /* an output overlaps an input and is not that input in place */
+  ARCS_ERR_BAD_NORM = -21,           /* arcs_clip_gradients: max_norm is NaN or negative */
+  ARCS_ERR_BAD_PLAN = -22            /* gradients: a tensor's count or the plan's size is not valid */
 } arcs_status;
 
 /* Per-row status codes written to out_status[b] (out_ids[b] = -1 when != 0). */
@@ -74,7 +81,9 @@ enum {
                                         and no long-history workspace */
   ARCS_ROW_VOCAB_TOO_LARGE = 7,      /* penalties active, V > ARCS_MAX_PENALTY_VOCAB,
                                         and no long-history workspace */
-  ARCS_ROW_BAD_TARGET = 8            /* arcs_linear_cross_entropy: target outside [0, V) and not ignore_index */
+  ARCS_ROW_BAD_TARGET = 8,           /* arcs_linear_cross_entropy: target outside [0, V) and not ignore_index */
+  ARCS_ROW_BAD_MASK = 9,             /* arcs_adjust_logits: mask row outside [0, masks) and not -1 */
+  ARCS_ROW_NOTHING_ALLOWED = 10      /* arcs_adjust_logits: the mask leaves no token */
 };
 
 /* Limits of the penalty tables kept in LDS (per row): distinct history ids
@@ -92,7 +101,7 @@ enum {
   ARCS_FAULT_RING_OVERRUN = 2        /* the ring slot still holds a step not drained yet */
 };
 
-/* Largest hidden size of arcs_w4_logits and arcs_linear_cross_entropy. */
+/* Largest hidden size of arcs_w4_logits, arcs_linear and arcs_linear_cross_entropy. */
 #define ARCS_MAX_HIDDEN 65536
 
 /* Limits of arcs_top_logprobs: entries per row, and V. */
@@ -539,6 +548,169 @@ int arcs_linear_cross_entropy_backward(const void* hidden, int64_t hidden_stride
 
 /* Bytes of workspace the two calls above need (0 for sizes they refuse). */
 size_t arcs_linear_cross_entropy_workspace_bytes(int64_t N, int64_t V, int64_t D, int dtype, int backward);
+
+/* Activations of arcs_linear. */
+typedef enum arcs_activation {
+  ARCS_ACT_NONE = 0,
+  ARCS_ACT_RELU = 1,
+  ARCS_ACT_GELU = 2,       /* z (1 + erf(z / sqrt 2)) / 2 */
+  ARCS_ACT_GELU_TANH = 3,  /* z (1 + tanh(sqrt(2 / pi) (z + 0.044715 z^3))) / 2 */
+  ARCS_ACT_SILU = 4,       /* z / (1 + exp(-z)) */
+  ARCS_ACT_SOFTCAP = 5     /* c tanh(z / c), c = softcap */
+} arcs_activation;
+
+/*
+ * arcs_linear: a linear layer with bias, activation and residual, in one pass:
+ * the logits of a head whose weights are not quantised, for arcs_argmax,
+ * arcs_sample and arcs_top_logprobs, or the blocks in front of it, such as a
+ * draft head's hidden + silu(weight hidden + bias).  Per row n:
+ *   z = hidden[n] weight^T + bias,   out[n] = residual[n] + act(z).
+ * Products, sums and the activation are held in binary32 and each result is
+ * rounded once to its type.  NaN and infinities propagate.
+ *   hidden      device [N, hidden_stride] of dtype (ARCS_DTYPE_BF16 or
+ *               ARCS_DTYPE_F32), hidden_stride >= D, D in 1 .. ARCS_MAX_HIDDEN
+ *   weight      device [V, weight_stride] of dtype, weight_stride >= D
+ *   bias        device [V] of dtype, or NULL
+ *   activation  an arcs_activation; softcap is read for ARCS_ACT_SOFTCAP only,
+ *               and has to be positive and finite there
+ *   residual    device [N, residual_stride] of dtype, residual_stride >= V, or NULL
+ *   out         device [N, out_stride] of out_dtype, out_stride >= V; may be
+ *               the residual itself where type and stride are the same
+ *   out_pre     device [N, V] of dtype, dense: z, which the backward pass of an
+ *               activation needs; or NULL
+ *   workspace   device scratch of at least arcs_linear_workspace_bytes(),
+ *               256-byte aligned, not read before it is written; calls that share
+ *               one must be ordered on one stream; may be NULL when none is needed
+ * The same call gives the same bits.  Outputs must not overlap inputs (but for
+ * the residual) or each other.  Rows of hidden and weight that are not on the
+ * 16-byte grid (pointer, stride and D; strides of 2^23 bytes or more count as such)
+ * are copied to the workspace first, unless N is at most 16.
+ * Returns ARCS_OK or a negative arcs_status (nothing launched then);
+ * ARCS_ERR_BAD_BATCH also for N above 2^22 or N * V above 2^40,
+ * ARCS_ERR_BAD_VOCAB also for V above 2^24.
+ */
+int arcs_linear(const void* hidden, int64_t hidden_stride, const void* weight, int64_t weight_stride, int dtype,
+                int64_t N, int64_t V, int64_t D, const void* bias, int activation, float softcap,
+                const void* residual, int64_t residual_stride, void* out, int out_dtype, int64_t out_stride,
+                void* out_pre, void* workspace, size_t workspace_bytes, void* stream);
+
+/*
+ * arcs_linear_backward: the gradients of sum(grad_out * out) of the call above:
+ *   dz = grad_out * act'(z),   out_dhidden = dz weight,
+ *   out_dweight = dz^T hidden,   out_dbias = the sums of dz over n.
+ * (The residual's gradient is grad_out itself.)
+ *   pre          out_pre of the forward call, [N, V] of dtype, dense; may be NULL
+ *                for ARCS_ACT_NONE
+ *   grad_out     device [N, grad_stride] of grad_dtype, grad_stride >= V
+ *   out_dhidden  device [N, D] of dtype, dense, or NULL (not wanted)
+ *   out_dweight  device [V, D] of dtype, dense, or NULL (not wanted)
+ *   out_dbias    device [V] of dtype, or NULL (not wanted); one of the three
+ *                must be given; each is written whole, not added to
+ *   workspace    arcs_linear_backward_workspace_bytes()
+ * dz is rounded to dtype before the products (as z was), and summed for out_dbias
+ * before that; sums are held in binary32 or more.  Other arguments and errors as the
+ * forward call; ARCS_ERR_BAD_VOCAB also for V above 2^21 - 8.
+ */
+int arcs_linear_backward(const void* hidden, int64_t hidden_stride, const void* weight, int64_t weight_stride,
+                         int dtype, int64_t N, int64_t V, int64_t D, int activation, float softcap,
+                         const void* pre, const void* grad_out, int grad_dtype, int64_t grad_stride,
+                         void* out_dhidden, void* out_dweight, void* out_dbias, void* workspace,
+                         size_t workspace_bytes, void* stream);
+
+/*
+ * Bytes of workspace the two calls need (0 for sizes they refuse).
+ * rows_aligned: whether all rows of hidden and weight are on the 16-byte grid
+ * (pointers, strides and D, and strides below 2^23 bytes); 0 is enough for either.
+ */
+size_t arcs_linear_workspace_bytes(int64_t N, int64_t V, int64_t D, int dtype, int rows_aligned);
+size_t arcs_linear_backward_workspace_bytes(int64_t N, int64_t V, int64_t D, int dtype, int rows_aligned);
+
+/*
+ * arcs_adjust_logits: logits as the sampler is to see them: penalties for what a
+ * row's history holds, biases, and the tokens its grammar allows.  Per row b,
+ * in binary32 and in this order:
+ *   1. ids in the history: the presence, frequency and repetition penalties of
+ *      params[b], the same operations as arcs_sample's (ids outside [0, V) are
+ *      skipped; duplicates count).  The rows then go to arcs_sample with the same
+ *      records and without a history;
+ *   2. ids in the bias list: their bias is added (the sum in list order
+ *      of those of an id listed more than once; ids outside [0, V) are skipped);
+ *   3. tokens whose mask bit is 0 become -inf, whatever they held;
+ * then each value is rounded once to out_dtype.  Other tokens keep their value,
+ * NaN and infinities too.
+ *   params        device, arcs_row_params[B] (its other fields are not read), or
+ *                 NULL: no penalties (the history must be NULL then)
+ *   hist_ids, hist_offsets   as in arcs_sample, or both NULL
+ *   bias_ids      device int32, bias_values device float, bias_offsets device
+ *                 int64[B + 1] CSR offsets into both; or all three NULL
+ *   mask          device uint32 [masks, mask_stride], mask_stride >= ceil(V / 32):
+ *                 bit v % 32 of word v / 32 is 1 where token v is allowed; or NULL
+ *   mask_rows     device int32[B]: the mask of each row, -1 for a row without
+ *                 one; or NULL: row b has mask b (masks >= B then)
+ *   out           device [B, out_stride] of out_dtype, out_stride >= V; may be
+ *                 `logits` itself with the same type and stride: then only
+ *                 16-byte groups that change are written
+ *   out_status    device int32[B]: ARCS_ROW_OK; ARCS_ROW_BAD_PENALTY (a penalty
+ *                 is not finite, or repetition < 0) or ARCS_ROW_BAD_MASK: the row
+ *                 is filled with NaN; ARCS_ROW_NOTHING_ALLOWED: the mask leaves
+ *                 no token, the row is -inf.  Or NULL
+ * Outputs must not overlap inputs otherwise (ARCS_ERR_OVERLAP where logits and
+ * out do).  Returns ARCS_OK or a negative arcs_status (nothing launched then);
+ * ARCS_ERR_BAD_BATCH also for B * (ceil(V / 4096) + 1) above 2^31 - 1.
+ */
+int arcs_adjust_logits(const void* logits, int dtype, int64_t B, int64_t V, int64_t row_stride,
+                       const arcs_row_params* params, const int32_t* hist_ids, const int64_t* hist_offsets,
+                       const int32_t* bias_ids, const float* bias_values, const int64_t* bias_offsets,
+                       const uint32_t* mask, int64_t masks, int64_t mask_stride, const int32_t* mask_rows,
+                       void* out, int out_dtype, int64_t out_stride, int32_t* out_status, void* stream);
+
+/* One tensor of a list of gradients: `count` elements, dense. */
+typedef struct arcs_tensor {
+  const void* data;  /* device, aligned to its element; may be NULL when count is 0 */
+  void* out;         /* where arcs_clip_gradients writes: `data` (in place, of the same type)
+                        or memory that overlaps no tensor; NULL: arcs_gradient_norm only */
+  int64_t count;     /* >= 0 */
+  int32_t dtype;
+  int32_t out_dtype;
+} arcs_tensor;
+
+/*
+ * arcs_gradient_plan: lists the pieces of n tensors (a host array) in `plan`, host
+ * memory of arcs_gradient_plan_bytes().  The caller copies the plan to the device once
+ * and uses it as long as the tensors stay where they are.  Tensors must not
+ * overlap each other.  Nothing is launched.  ARCS_ERR_BAD_BATCH for n < 0,
+ * ARCS_ERR_BAD_PLAN for a count below 0 or a total above 2^40 elements,
+ * ARCS_ERR_OVERLAP for an `out` that is `data` of another type.
+ */
+int arcs_gradient_plan(const arcs_tensor* tensors, int64_t n, void* plan, size_t plan_bytes);
+/* Bytes of the plan of n tensors (0 for a list that is refused, and for one without elements). */
+size_t arcs_gradient_plan_bytes(const arcs_tensor* tensors, int64_t n);
+
+/*
+ * arcs_gradient_norm: out_norm[0] = sqrt(sum of x^2 over all elements of the plan's
+ * tensors), summed in binary64 in an order that does not depend on timing and
+ * rounded once to binary32 (0 for an empty plan).
+ *   plan        device copy of arcs_gradient_plan's, 8-byte aligned; may be
+ *               NULL when plan_bytes is 0
+ *   out_norm    device float[1]
+ *   workspace   device scratch of at least arcs_gradient_workspace_bytes(plan_bytes),
+ *               256-byte aligned; calls that share one must be ordered on one stream
+ */
+int arcs_gradient_norm(const void* plan, size_t plan_bytes, float* out_norm, void* workspace,
+                       size_t workspace_bytes, void* stream);
+
+/*
+ * arcs_clip_gradients: the norm as above and, where it is above max_norm and
+ * finite, every element times max_norm / norm (taken in binary64, rounded to
+ * binary32 and then to its output's type).  Otherwise the elements keep their
+ * values: tensors in place are not touched, others are copied to their outputs.
+ *   max_norm    >= 0 (ARCS_ERR_BAD_NORM for NaN and negative values)
+ * Every tensor of the plan needs its `out`.
+ */
+int arcs_clip_gradients(const void* plan, size_t plan_bytes, double max_norm, float* out_norm, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+size_t arcs_gradient_workspace_bytes(size_t plan_bytes);
 
 /* Library version, major * 10000 + minor * 100 + patch. */
 int arcs_version(void);
