@@ -26,7 +26,9 @@ BUILD_DIR = os.path.join(PKG, "_build")
 
 SOURCES = ["api.hip", "argmax_kernel.hip", "sample_kernel.hip", "logprobs_kernel.hip", "commit_kernel.hip",
            "hybrid_kernel.hip", "w4_kernel.hip", "cross_entropy_kernel.hip",
-           "cross_entropy_mfma.hip", "linear_kernel.hip", "linear_mfma.hip", "adjust_kernel.hip", "norm_kernel.hip"]
+           "cross_entropy_mfma.hip", "linear_kernel.hip", "linear_forward_bf16.hip", "linear_forward_f32.hip",
+           "linear_dhidden_bf16.hip", "linear_dhidden_f32.hip", "linear_dweight_bf16.hip", "linear_dweight_f32.hip",
+           "adjust_kernel.hip", "norm_kernel.hip"]
 ARCH = os.environ.get("ARCS_OFFLOAD_ARCH", "gfx950")
 
 COMMON = [

@@ -206,7 +206,7 @@ int check_linear(const void* hidden, int64_t hidden_stride, const void* weight, 
   if (st != ARCS_OK) return st;
   if (hidden_stride < D || weight_stride < D) return ARCS_ERR_BAD_STRIDE;
   if (activation < ARCS_ACT_NONE || activation > ARCS_ACT_SOFTCAP ||
-      (activation == ARCS_ACT_SOFTCAP && !(softcap > 0.0f && softcap <= 3.402823466e38f)))
+      (activation == ARCS_ACT_SOFTCAP && !(softcap >= 0x1p-100f && softcap <= 0x1p100f)))
     return ARCS_ERR_BAD_ACTIVATION;
   if (misaligned(hidden, element_size(dtype)) || misaligned(weight, element_size(dtype))) return ARCS_ERR_MISALIGNED;
   *aligned = arcs::linear_rows_aligned(hidden, hidden_stride, D, dtype) &&
@@ -530,6 +530,7 @@ int arcs_linear(const void* hidden, int64_t hidden_stride, const void* weight, i
   a.D = D;
   a.act = activation;
   a.cap = softcap;
+  a.inv_cap = activation == ARCS_ACT_SOFTCAP ? 1.0f / softcap : 0.0f;
   a.bias = bias;
   a.residual = residual;
   a.residual_stride = residual_stride;
@@ -570,6 +571,7 @@ int arcs_linear_backward(const void* hidden, int64_t hidden_stride, const void* 
   a.D = D;
   a.act = activation;
   a.cap = softcap;
+  a.inv_cap = activation == ARCS_ACT_SOFTCAP ? 1.0f / softcap : 0.0f;
   a.pre = pre;
   a.grad = grad_out;
   a.grad_stride = grad_stride;
@@ -702,7 +704,7 @@ const char* arcs_status_string(int code) {
       return "the shape needs more workspace than arcs_sample_noalloc's scratch (ARCS_NOALLOC_SCRATCH_BYTES)";
     case ARCS_ERR_BAD_HIDDEN: return "hidden size D must be in [1, ARCS_MAX_HIDDEN]";
     case ARCS_ERR_BAD_GROUP: return "group_size must be 32, 64 or 128 and divide D";
-    case ARCS_ERR_BAD_ACTIVATION: return "activation must be an arcs_activation, softcap positive and finite";
+    case ARCS_ERR_BAD_ACTIVATION: return "activation must be an arcs_activation, softcap within 2^-100 .. 2^100";
     case ARCS_ERR_BAD_BIAS: return "bias ids, values and offsets must all be NULL or all be set";
     case ARCS_ERR_BAD_MASK: return "mask_rows without a mask, or fewer masks than rows";
     case ARCS_ERR_OVERLAP: return "an output overlaps an input";

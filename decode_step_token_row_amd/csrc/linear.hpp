@@ -19,7 +19,7 @@ struct LinearArgs {
   int64_t weight_stride;
   int64_t N, V, D;
   int act;
-  float cap;
+  float cap, inv_cap;  // SOFTCAP: 1 / cap
   // forward
   const void* bias;      // [V] of T, or NULL
   const void* residual;  // [N, residual_stride] of T, or NULL
@@ -49,6 +49,8 @@ struct LinearShape {
   int columns;  // of the tile along m
   int workers;  // workgroups that share all tiles evenly, each a part of k of some; 0: whole tiles
 };
+// The tiles of a product: of those built for the mode and type, and of the ways to share them,
+// the ones that cost least.
 LinearShape linear_shape(int mode, int64_t M, int64_t N, int64_t K, bool bf16);
 
 // The workspace's parts, in bytes from its start.
@@ -69,7 +71,7 @@ bool linear_rows_aligned(const void* p, int64_t stride, int64_t columns, int dty
 hipError_t launch_linear(LinearArgs a, int dtype, bool aligned, hipStream_t stream);
 hipError_t launch_linear_backward(LinearArgs a, int dtype, bool aligned, hipStream_t stream);
 
-// linear_mfma.hip: one product on the tile kernels.
+// One product on the tile kernels (linear_tile.hpp; one source for each mode and type).
 struct LinearProduct {
   const void *a, *b;
   int64_t lda, ldb;  // elements between rows
@@ -86,8 +88,14 @@ struct LinearProduct {
   void* pre;
   int64_t ldp;
   int act;
-  float cap;
+  float cap, inv_cap;  // SOFTCAP: 1 / cap
 };
+hipError_t launch_linear_forward_bf16(const LinearProduct& p, hipStream_t stream);
+hipError_t launch_linear_forward_f32(const LinearProduct& p, hipStream_t stream);
+hipError_t launch_linear_dhidden_bf16(const LinearProduct& p, hipStream_t stream);
+hipError_t launch_linear_dhidden_f32(const LinearProduct& p, hipStream_t stream);
+hipError_t launch_linear_dweight_bf16(const LinearProduct& p, hipStream_t stream);
+hipError_t launch_linear_dweight_f32(const LinearProduct& p, hipStream_t stream);
 hipError_t launch_linear_product(const LinearProduct& p, int mode, int dtype, hipStream_t stream);
 // linear_kernel.hip: at most kLinearFewRows rows of the forward pass.
 constexpr int64_t kLinearFewRows = 16;

@@ -14,49 +14,126 @@ namespace arcs {
 __device__ __forceinline__ float widen(float x) { return x; }
 __device__ __forceinline__ float widen(__bf16 x) { return (float)x; }
 
+constexpr float kLog2E = 1.44269504088896340736f;
 constexpr float kGeluA = 0.79788456080286535588f;  // sqrt(2 / pi)
 constexpr float kGeluB = 0.044715f;
 
-// act(z).  All in binary32; the activation is the same for a whole launch.  The normal
-// distribution function and (1 + tanh u) / 2 = 1 / (1 + exp(-2 u)) are taken in the forms that
-// keep their digits where they are near 0.
-__device__ __forceinline__ float act_value(float z, int act, float cap) {
-  switch (act) {
+// exp2 and the reciprocal of the vector unit are off by one unit in the last place; an
+// exponential's argument x is rounded, so exp(x) is off by |x| 2^-24 more, which the uses
+// below multiply by something that falls as fast.  (The library's expf and division made dz
+// three times as long as its way through memory.)
+__device__ __forceinline__ float exp_fast(float x) { return __builtin_amdgcn_exp2f(x * kLog2E); }
+__device__ __forceinline__ float rcp_fast(float x) { return __builtin_amdgcn_rcpf(x); }
+
+// The normal distribution function's smaller tail at z, times 2: erfc(|z| / sqrt 2) =
+// t (a1 + t (a2 + t (a3 + t (a4 + t a5)))) e, t = 1 / (1 + p |z| / sqrt 2), e = exp(-z^2 / 2), off by
+// at most 1.5e-7 (Abramowitz and Stegun, Handbook of Mathematical Functions, 7.1.26).
+__device__ __forceinline__ float normal_tail2(float z, float& e) {
+  const float t = rcp_fast(fmaf(0.3275911f * 0.70710678118654752440f, fabsf(z), 1.0f));
+  e = exp_fast(-0.5f * z * z);
+  float s = fmaf(t, 1.061405429f, -1.453152027f);
+  s = fmaf(t, s, 1.421413741f);
+  s = fmaf(t, s, -0.284496736f);
+  s = fmaf(t, s, 0.254829592f);
+  return s * t * e;
+}
+
+// tanh u: its series to u^9 up to 1/4 (the next term is 8e-9 of it), above that (1 - e) / (1 + e)
+// with e = exp(-2 |u|).
+__device__ __forceinline__ float tanh_fast(float u) {
+  const float w = u * u;
+  float s = fmaf(w, 62.0f / 2835.0f, -17.0f / 315.0f);
+  s = fmaf(w, s, 2.0f / 15.0f);
+  s = fmaf(w, s, -1.0f / 3.0f);
+  s = fmaf(w * s, u, u);
+  const float e = exp_fast(-2.0f * fabsf(u));
+  const float far = __builtin_copysignf((1.0f - e) * rcp_fast(1.0f + e), u);
+  return fabsf(u) < 0.25f ? s : far;
+}
+
+// act(z) in binary32.  (1 + tanh u) / 2 = 1 / (1 + exp(-2 u)) keeps its digits where it is near 0.
+template <int ACT>
+__device__ __forceinline__ float act_value(float z, float cap, float inv_cap) {
+  switch (ACT) {
     case ARCS_ACT_RELU: return z > 0.0f || z != z ? z : 0.0f;
-    case ARCS_ACT_GELU: return 0.5f * z * erfcf(z * -0.70710678118654752440f);
-    case ARCS_ACT_GELU_TANH: return z / (1.0f + expf(-2.0f * kGeluA * fmaf(kGeluB * z * z, z, z)));
-    case ARCS_ACT_SILU: return z / (1.0f + expf(-z));
-    case ARCS_ACT_SOFTCAP: return cap * tanhf(z / cap);
+    case ARCS_ACT_GELU: {
+      float e;
+      const float tail = 0.5f * normal_tail2(z, e);
+      return z * (z < 0.0f ? tail : 1.0f - tail);
+    }
+    case ARCS_ACT_GELU_TANH: return z * rcp_fast(1.0f + exp_fast(-2.0f * kGeluA * fmaf(kGeluB * z * z, z, z)));
+    case ARCS_ACT_SILU: return z * rcp_fast(1.0f + exp_fast(-z));
+    case ARCS_ACT_SOFTCAP: return cap * tanh_fast(z * inv_cap);
     default: return z;
   }
 }
 
 // act'(z).  1 - tanh^2 u is taken as 4 e / (1 + e)^2 with e = exp(-2 |u|), which keeps its
 // digits where tanh u is near 1.
-__device__ __forceinline__ float act_slope(float z, int act, float cap) {
-  switch (act) {
+template <int ACT>
+__device__ __forceinline__ float act_slope(float z, float inv_cap) {
+  switch (ACT) {
     case ARCS_ACT_RELU: return z > 0.0f ? 1.0f : z != z ? z : 0.0f;
-    case ARCS_ACT_GELU:
-      return 0.5f * erfcf(z * -0.70710678118654752440f) + z * expf(-0.5f * z * z) * 0.39894228040143267794f;
+    case ARCS_ACT_GELU: {
+      float e;
+      const float tail = 0.5f * normal_tail2(z, e);
+      return fmaf(e > 0.0f ? z * 0.39894228040143267794f : 0.0f, e, z < 0.0f ? tail : 1.0f - tail);
+    }
     case ARCS_ACT_GELU_TANH: {
       const float zz = z * z, u = kGeluA * fmaf(kGeluB * zz, z, z);
-      const float e = expf(-2.0f * fabsf(u)), d = 1.0f / (1.0f + e);
-      const float half = u >= 0.0f ? d : e * d;  // (1 + tanh u) / 2
-      // e is 0 where the rest may be infinite
-      const float rest = e > 0.0f ? 2.0f * z * e * d * d * kGeluA * fmaf(3.0f * kGeluB, zz, 1.0f) : 0.0f;
+      const float e = exp_fast(-2.0f * fabsf(u)), d = rcp_fast(1.0f + e), ed = e * d;
+      // half = (1 + tanh u) / 2; e is 0 where the rest may be infinite
+      const float half = u >= 0.0f ? d : ed;
+      const float rest = e > 0.0f ? 2.0f * kGeluA * z * ed * d * fmaf(3.0f * kGeluB, zz, 1.0f) : 0.0f;
       return z != z ? z : half + rest;
     }
     case ARCS_ACT_SILU: {
-      const float e = expf(-fabsf(z)), d = 1.0f / (1.0f + e);
-      const float s = z >= 0.0f ? d : e * d;
+      const float e = exp_fast(-fabsf(z)), d = rcp_fast(1.0f + e), ed = e * d;
+      const float s = z >= 0.0f ? d : ed;
       // z s (1 - s), 0 in the limit
-      return z != z ? z : s + (e > 0.0f ? z * e * d * d : 0.0f);
+      return z != z ? z : s + (e > 0.0f ? z * ed * d : 0.0f);
     }
     case ARCS_ACT_SOFTCAP: {
-      const float e = expf(-2.0f * fabsf(z / cap)), d = 1.0f / (1.0f + e);
+      const float e = exp_fast(-2.0f * fabsf(z * inv_cap)), d = rcp_fast(1.0f + e);
       return z != z ? z : 4.0f * e * d * d;
     }
     default: return 1.0f;
+  }
+}
+
+// The activation is the same for a whole launch: one branch for several elements, whose
+// chains of operations then overlap.
+template <int ACT, int E>
+__device__ __forceinline__ void act_each(float (&v)[E], float cap, float inv_cap) {
+#pragma unroll
+  for (int e = 0; e < E; ++e) v[e] = act_value<ACT>(v[e], cap, inv_cap);
+}
+template <int E>
+__device__ __forceinline__ void act_values(float (&v)[E], int act, float cap, float inv_cap) {
+  switch (act) {
+    case ARCS_ACT_RELU: return act_each<ARCS_ACT_RELU>(v, cap, inv_cap);
+    case ARCS_ACT_GELU: return act_each<ARCS_ACT_GELU>(v, cap, inv_cap);
+    case ARCS_ACT_GELU_TANH: return act_each<ARCS_ACT_GELU_TANH>(v, cap, inv_cap);
+    case ARCS_ACT_SILU: return act_each<ARCS_ACT_SILU>(v, cap, inv_cap);
+    case ARCS_ACT_SOFTCAP: return act_each<ARCS_ACT_SOFTCAP>(v, cap, inv_cap);
+    default: return;
+  }
+}
+// g times act'(z)
+template <int ACT, int E>
+__device__ __forceinline__ void slope_each(float (&g)[E], const float (&z)[E], float inv_cap) {
+#pragma unroll
+  for (int e = 0; e < E; ++e) g[e] *= act_slope<ACT>(z[e], inv_cap);
+}
+template <int E>
+__device__ __forceinline__ void act_slopes(float (&g)[E], const float (&z)[E], int act, float inv_cap) {
+  switch (act) {
+    case ARCS_ACT_RELU: return slope_each<ARCS_ACT_RELU>(g, z, inv_cap);
+    case ARCS_ACT_GELU: return slope_each<ARCS_ACT_GELU>(g, z, inv_cap);
+    case ARCS_ACT_GELU_TANH: return slope_each<ARCS_ACT_GELU_TANH>(g, z, inv_cap);
+    case ARCS_ACT_SILU: return slope_each<ARCS_ACT_SILU>(g, z, inv_cap);
+    case ARCS_ACT_SOFTCAP: return slope_each<ARCS_ACT_SOFTCAP>(g, z, inv_cap);
+    default: return;
   }
 }
 
@@ -92,6 +169,31 @@ __device__ __forceinline__ void load_some(const T* p, int n, float (&v)[E]) {
 #pragma unroll
     for (int e = 0; e < E; ++e) v[e] = e < n ? widen(p[e]) : 0.0f;
   }
+}
+// Eight consecutive elements as they are in memory, so that the loads can fly while other work is
+// done; `n` of them exist (zeros past n).
+template <typename T>
+struct Raw8 {
+  u32x4 q[sizeof(T) / 2];
+};
+template <typename T>
+__device__ __forceinline__ void load_raw(Raw8<T>& r, const T* p, int n) {
+  if (n >= 8) {
+#pragma unroll
+    for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.q[i] = load16((const char*)p + i * 16);
+  } else {
+    T t[8];
+#pragma unroll
+    for (int e = 0; e < 8; ++e) t[e] = e < n ? p[e] : (T)0.0f;
+    __builtin_memcpy(&r, t, sizeof(r));
+  }
+}
+template <typename T>
+__device__ __forceinline__ void widen_raw(const Raw8<T>& r, float (&v)[8]) {
+  T t[8];
+  __builtin_memcpy(t, &r, sizeof(r));
+#pragma unroll
+  for (int e = 0; e < 8; ++e) v[e] = widen(t[e]);
 }
 // Writes n of E consecutive elements.
 template <typename T, int E>

@@ -1,0 +1,13 @@
+// dz^T hidden in bfloat16: the tiles that linear_shape chooses from.
+#include "linear_tile.hpp"
+
+namespace arcs {
+
+hipError_t launch_linear_dweight_bf16(const LinearProduct& p, hipStream_t stream) {
+  const bool known = launch_linear_tile<__bf16, kLinDweight, 2, 4, 4, 2, 2>(p, stream) ||
+                     launch_linear_tile<__bf16, kLinDweight, 2, 2, 2, 2, 2>(p, stream) ||
+                     launch_linear_tile<__bf16, kLinDweight, 2, 2, 1, 1, 4>(p, stream);
+  return known ? hipGetLastError() : hipErrorInvalidValue;
+}
+
+}  // namespace arcs

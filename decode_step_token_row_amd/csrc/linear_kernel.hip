@@ -71,54 +71,78 @@ __global__ __launch_bounds__(kFewWaves * 64) void linear_few_kernel(LinearArgs a
   for (int i = 0; i < kFewWaves; ++i) z += part[i][c][row];
   if (a.bias != nullptr) z += widen(((const T*)a.bias)[v0 + c]);
   if (a.out_pre != nullptr) ((T*)a.out_pre)[row * a.V + v0 + c] = (T)z;
-  float y = act_value(z, a.act, a.cap);
-  if (a.residual != nullptr) y += widen(((const T*)a.residual)[row * a.residual_stride + v0 + c]);
-  if (a.out_bf16) ((__bf16*)a.out)[row * a.out_stride + v0 + c] = (__bf16)y;
-  else ((float*)a.out)[row * a.out_stride + v0 + c] = y;
+  float y[1] = {z};
+  act_values(y, a.act, a.cap, a.inv_cap);
+  if (a.residual != nullptr) y[0] += widen(((const T*)a.residual)[row * a.residual_stride + v0 + c]);
+  if (a.out_bf16) ((__bf16*)a.out)[row * a.out_stride + v0 + c] = (__bf16)y[0];
+  else ((float*)a.out)[row * a.out_stride + v0 + c] = y[0];
 }
 
 // ---------------------------------------------------------------------------
 // backward: dz and the columns' sums
 // ---------------------------------------------------------------------------
-// A thread has 8 columns of chunk_rows rows.  The sums take dz before it is rounded to T.
-// dz may be NULL (only dbias is wanted, or grad_out is dz as it is), and so may the sums.
-template <typename T, typename G>
-__global__ __launch_bounds__(128) void linear_dz_kernel(LinearArgs a, T* dz, int64_t ldz, float* sums, int64_t chunk_rows) {
-  const int64_t v = ((int64_t)blockIdx.x * 128 + threadIdx.x) * 8;
-  if (v >= ldz && v >= a.V) return;
-  const int left = (int)(a.V - v < 8 ? a.V - v : 8);
-  const int64_t n0 = (int64_t)blockIdx.y * chunk_rows, n1 = n0 + chunk_rows < a.N ? n0 + chunk_rows : a.N;
-  float sum[8] = {};
-  if (left > 0) {
-#pragma unroll 2
-    for (int64_t n = n0; n < n1; ++n) {
-      float g[8];
-      load_some<G, 8>((const G*)a.grad + n * a.grad_stride + v, left, g);
-      if (a.act != ARCS_ACT_NONE) {
-        float z[8];
-        load_some<T, 8>((const T*)a.pre + n * a.V + v, left, z);
+// A workgroup has 256 columns of ROWS * 8 rows: a thread 8 columns of ROWS rows, all loaded at
+// once.  The sums take dz before it is rounded to T; a workgroup's meet in LDS.  dz may be
+// NULL (only dbias is wanted, or grad_out is dz as it is), and so may the sums.
+template <typename T, typename G, int ROWS>
+__global__ __launch_bounds__(256) void linear_dz_kernel(LinearArgs a, T* dz, int64_t ldz, float* sums) {
+  __shared__ __align__(16) float part[8][256];
+  const int tid = threadIdx.x, c = (tid & 31) * 8, r = tid >> 5;
+  const int64_t v = (int64_t)blockIdx.x * 256 + c;
+  const int left = (int)(a.V - v < 8 ? a.V - v : 8);  // <= 0 past V
+  const int64_t n0 = (int64_t)blockIdx.y * (ROWS * 8) + r;
+  Raw8<G> g[ROWS];
+  Raw8<T> z[ROWS];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) g[e] = e < left ? g[e] * act_slope(z[e], a.act, a.cap) : 0.0f;
-      }
-#pragma unroll
-      for (int e = 0; e < 8; ++e) sum[e] += g[e];
-      if (dz != nullptr) store_some<T, 8>(dz + n * ldz + v, 8, g);  // zeros past V, up to ldz
-    }
-    if (sums != nullptr) store_some<float, 8>(sums + blockIdx.y * a.V + v, left, sum);
+  for (int i = 0; i < ROWS; ++i) {
+    const int64_t n = n0 + i * 8;
+    const int have = n < a.N ? left : 0;
+    load_raw(g[i], (const G*)a.grad + n * a.grad_stride + v, have);
+    if (a.act != ARCS_ACT_NONE) load_raw(z[i], (const T*)a.pre + n * a.V + v, have);
   }
+  float sum[8] = {};
+#pragma unroll
+  for (int i = 0; i < ROWS; ++i) {
+    float x[8];
+    widen_raw(g[i], x);
+    if (a.act != ARCS_ACT_NONE) {
+      float y[8];
+      widen_raw(z[i], y);
+      act_slopes(x, y, a.act, a.inv_cap);  // past V both are 0
+    }
+#pragma unroll
+    for (int e = 0; e < 8; ++e) sum[e] += x[e];
+    const int64_t n = n0 + i * 8;
+    if (dz != nullptr && n < a.N && left > 0) store_some<T, 8>(dz + n * ldz + v, 8, x);  // zeros past V, up to ldz
+  }
+  if (sums == nullptr) return;
+  *(f32x4*)&part[r][c] = f32x4{sum[0], sum[1], sum[2], sum[3]};
+  *(f32x4*)&part[r][c + 4] = f32x4{sum[4], sum[5], sum[6], sum[7]};
+  __syncthreads();
+  float s = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) s += part[i][tid];
+  const int64_t at = (int64_t)blockIdx.x * 256 + tid;
+  if (at < a.V) sums[blockIdx.y * a.V + at] = s;
 }
 
+// The chunks' sums added up, in an order of their numbers.
 template <typename T>
 __global__ __launch_bounds__(256) void linear_dbias_kernel(const float* sums, int64_t V, int64_t chunks, T* out) {
-  __shared__ double part[4][64];
-  const int c = threadIdx.x & 63, g = threadIdx.x >> 6;
-  const int64_t v = (int64_t)blockIdx.x * 64 + c;
+  __shared__ double part[16][17];
+  const int c = threadIdx.x & 15, g = threadIdx.x >> 4;
+  const int64_t v = (int64_t)blockIdx.x * 16 + c;
   double s = 0.0;
-  if (v < V)
-    for (int64_t i = g; i < chunks; i += 4) s += (double)sums[i * V + v];
+  if (v < V) {
+#pragma unroll 8
+    for (int64_t i = g; i < chunks; i += 16) s += (double)sums[i * V + v];
+  }
   part[g][c] = s;
   __syncthreads();
-  if (g == 0 && v < V) out[v] = (T)(float)((part[0][c] + part[1][c]) + (part[2][c] + part[3][c]));
+  if (g != 0 || v >= V) return;
+#pragma unroll
+  for (int i = 1; i < 16; ++i) s += part[i][c];
+  out[v] = (T)(float)s;
 }
 
 // Rows of `columns` elements to rows of ld, zeros behind them.
@@ -139,6 +163,10 @@ namespace {
 
 int64_t tiles(int64_t n, int64_t t) { return (n + t - 1) / t; }
 size_t padded(int64_t bytes) { return (size_t)((bytes + 255) / 256 * 256); }
+
+// Rows of a workgroup of linear_dz_kernel: 32, four loads a thread in flight, or 8 where that
+// leaves compute units without work (DZ8).
+int64_t dz_chunk_rows(int64_t N, int64_t V) { return tiles(N, 32) * tiles(V, 256) < 512 ? 8 : 32; }
 
 size_t slab_bytes(int mode, int64_t M, int64_t N, int64_t K, bool bf16) {
   const LinearShape s = linear_shape(mode, M, N, K, bf16);
@@ -192,7 +220,15 @@ hipError_t forward(LinearArgs a, int dtype, bool aligned, hipStream_t stream) {
   p.ldp = a.V;
   p.act = a.act;
   p.cap = a.cap;
+  p.inv_cap = a.inv_cap;
   return launch_linear_product(p, kLinForward, dtype, stream);
+}
+
+template <typename T, typename G>
+void launch_dz(const LinearArgs& a, T* dz, int64_t ldz, float* sums, int64_t chunk_rows, hipStream_t stream) {
+  const dim3 grid((unsigned)tiles(a.V, 256), (unsigned)tiles(a.N, chunk_rows));
+  if (chunk_rows == 8) hipLaunchKernelGGL((linear_dz_kernel<T, G, 1>), grid, dim3(256), 0, stream, a, dz, ldz, sums);
+  else hipLaunchKernelGGL((linear_dz_kernel<T, G, 4>), grid, dim3(256), 0, stream, a, dz, ldz, sums);
 }
 
 template <typename T>
@@ -206,14 +242,11 @@ hipError_t backward(LinearArgs a, int dtype, bool aligned, hipStream_t stream) {
   float* sums = a.out_dbias != nullptr ? (float*)(a.workspace + plan.dbias) : nullptr;
   const int64_t chunks = tiles(a.N, plan.chunk_rows);
   if (dz != nullptr || sums != nullptr) {
-    const dim3 grid((unsigned)tiles(a.V, 1024), (unsigned)chunks);
-    if (a.grad_bf16)
-      hipLaunchKernelGGL((linear_dz_kernel<T, __bf16>), grid, dim3(128), 0, stream, a, dz, plan.ldz, sums, plan.chunk_rows);
-    else
-      hipLaunchKernelGGL((linear_dz_kernel<T, float>), grid, dim3(128), 0, stream, a, dz, plan.ldz, sums, plan.chunk_rows);
+    if (a.grad_bf16) launch_dz<T, __bf16>(a, dz, plan.ldz, sums, plan.chunk_rows, stream);
+    else launch_dz<T, float>(a, dz, plan.ldz, sums, plan.chunk_rows, stream);
   }
   if (sums != nullptr)
-    hipLaunchKernelGGL(linear_dbias_kernel<T>, dim3((unsigned)tiles(a.V, 64)), dim3(256), 0, stream, sums, a.V, chunks,
+    hipLaunchKernelGGL(linear_dbias_kernel<T>, dim3((unsigned)tiles(a.V, 16)), dim3(256), 0, stream, sums, a.V, chunks,
                        (T*)a.out_dbias);
   LinearProduct p = {};
   p.slab = (float*)(a.workspace + plan.slab);
@@ -251,6 +284,71 @@ hipError_t backward(LinearArgs a, int dtype, bool aligned, hipStream_t stream) {
 
 }  // namespace
 
+// What a product costs in tiles of a kind, in microseconds: `start` for the launch and the first
+// loads, then for each round of tiles `step` (`alone` where no compute unit has two) for
+// each 128 bytes of k and `end` for the results; shared tiles cost their parts' way
+// through memory (bytes per microsecond) and `join` for the second launch.  Fitted to the times
+// of 51 sizes of each mode in bfloat16 and 13 in float32 (17 .. 4,096 rows, 200 .. 130,000
+// columns, k of 100 .. 11,008), measured in every kind and sharing: what the costs
+// name takes 0.5 % longer in the geometric mean than the best, 25 % at most (of 10 us).  On
+// both sides of the choice, for instance, forward: 4,096 x 4,096 x 4,096 125 us in 256 x 256
+// and 148 in 128 x 128; 512 x 11,008 x 4,096 68 in 128 x 128, 92 in 256 x 256 shared; 256 x
+// 4,096 x 4,096 23 in 64 x 64, 26 in 128 x 128 shared.  (256 x 128, 256 x 64 and 128 x 64 in
+// bfloat16, other depths of k and four waves of 128 x 128 each gained less than 1 % somewhere.)
+struct TileCost {
+  int columns, rows, slots;  // slots: workgroups that the card holds at once
+  double alone, step, end, start, join, rate;
+};
+constexpr TileCost kCostsBf16[] = {
+    {256, 256, 256, 1.50, 1.50, 6.6, 2.0, 2.6, 5.6e6},
+    {128, 128, 512, 0.69, 1.08, 3.1, 2.0, 6.2, 6.1e6},
+    {64, 64, 512, 0.29, 0.52, 1.8, 2.0, 4.2, 3.2e6},
+    {128, 32, 512, 0.34, 0.61, 1.8, 2.0, 5.0, 3.5e6},  // not in DWEIGHT
+};
+constexpr TileCost kCostsF32[] = {
+    {128, 64, 512, 1.12, 2.03, 1.3, 2.6, 5.3, 4.6e6},
+    {64, 64, 512, 0.63, 1.25, 0.8, 3.0, 4.8, 3.9e6},
+    {128, 32, 512, 0.77, 1.37, 1.2, 2.5, 5.8, 4.3e6},  // not in DWEIGHT
+};
+
+LinearShape linear_shape(int mode, int64_t M, int64_t N, int64_t K, bool bf16) {
+  const TileCost* costs = bf16 ? kCostsBf16 : kCostsF32;
+  const int kinds = (bf16 ? 4 : 3) - (mode == kLinDweight ? 1 : 0);
+  const double steps = (double)tiles(K, bf16 ? 64 : 32);
+  LinearShape best = {0, 0, 0};
+  double least = 0.0;
+  for (int i = 0; i < kinds; ++i) {
+    const TileCost& c = costs[i];
+    if (c.rows > 32 && c.rows > 2 * N && mode != kLinDweight) continue;  // mostly empty
+    const double all = (double)tiles(M, c.columns) * (double)tiles(N, c.rows);
+    for (int workers = 0; workers <= 512; workers = workers == 0 ? 128 : workers * 2) {
+      double cost = c.start;
+      if (workers > 0) {
+        if (all > 400 || all * steps < workers) continue;
+        cost += c.join + c.end + all * steps / workers * (workers <= 256 ? c.alone : c.step) +
+                (all + workers) * c.columns * c.rows * 8.0 / c.rate;
+      } else if (all <= 256) {
+        cost += steps * c.alone + c.end;
+      } else {
+        const double rounds = all / c.slots;
+        cost += (rounds < 4.0 ? __builtin_ceil(rounds) : rounds + 0.5) * (steps * c.step + c.end);
+      }
+      if (best.rows == 0 || cost < least) {
+        least = cost;
+        best = {c.rows, c.columns, workers};
+      }
+    }
+  }
+  return best;
+}
+
+hipError_t launch_linear_product(const LinearProduct& p, int mode, int dtype, hipStream_t stream) {
+  const bool bf16 = dtype == ARCS_DTYPE_BF16;
+  if (mode == kLinForward) return bf16 ? launch_linear_forward_bf16(p, stream) : launch_linear_forward_f32(p, stream);
+  if (mode == kLinDhidden) return bf16 ? launch_linear_dhidden_bf16(p, stream) : launch_linear_dhidden_f32(p, stream);
+  return bf16 ? launch_linear_dweight_bf16(p, stream) : launch_linear_dweight_f32(p, stream);
+}
+
 bool linear_rows_aligned(const void* p, int64_t stride, int64_t columns, int dtype) {
   // a tile's rows lie within 2^31 bytes
   const int64_t each = dtype == ARCS_DTYPE_BF16 ? 8 : 4, most = int64_t(1) << (dtype == ARCS_DTYPE_BF16 ? 22 : 21);
@@ -263,7 +361,7 @@ LinearPlan linear_plan(int64_t N, int64_t V, int64_t D, int dtype, bool aligned,
   LinearPlan p = {};
   p.ldd = tiles(D, each) * each;
   p.ldz = tiles(V, 8) * 8;  // linear_dz_kernel writes 8 columns at a time
-  p.chunk_rows = N <= 16 * 256 ? 16 : tiles(N, 256);
+  p.chunk_rows = dz_chunk_rows(N, V);
   if (!backward && N <= kLinearFewRows) return p;
   size_t at = 0;
   auto part = [&](size_t bytes) {

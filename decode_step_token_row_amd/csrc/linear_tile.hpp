@@ -9,6 +9,8 @@
 // compute units without work, all workgroups share the tiles evenly, each a part of k of
 // one or more: their float32 parts go to the workspace and linear_join_kernel adds them up
 // in the workgroups' order, so that results do not depend on timing.
+#pragma once
+
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
@@ -18,6 +20,29 @@
 #include "mfma_tile.hpp"
 
 namespace arcs {
+
+// The epilogue on E consecutive results of row n, `left` of which exist:
+// FORWARD: out = residual + act(v + bias), pre = v + bias.
+template <typename T, bool FORWARD, int E>
+__device__ __forceinline__ void linear_finish(const LinearProduct& p, int64_t n, int64_t m, int left, float (&v)[E],
+                                              const float (&bias)[E], const float (&residual)[E]) {
+  if constexpr (FORWARD) {
+    if (p.bias != nullptr) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[e] += bias[e];
+    }
+    if (p.pre != nullptr) store_some<T, E>((T*)p.pre + n * p.ldp + m, left, v);
+    act_values(v, p.act, p.cap, p.inv_cap);
+    if (p.residual != nullptr) {
+#pragma unroll
+      for (int e = 0; e < E; ++e) v[e] += residual[e];
+    }
+    if (p.out_bf16) store_some<__bf16, E>((__bf16*)p.out + n * p.ldo + m, left, v);
+    else store_some<float, E>((float*)p.out + n * p.ldo + m, left, v);
+  } else {
+    store_some<T, E>((T*)p.out + n * p.ldo + m, left, v);
+  }
+}
 
 template <typename T, int MODE, int WM, int WN, int MT, int NT, int S>
 struct LinTile {
@@ -30,9 +55,7 @@ struct LinTile {
   static constexpr int kALoads = BM / 8, kBLoads = BN / 8;  // of 1024 bytes each
   static constexpr int kAPer = (kALoads + kWaves - 1) / kWaves, kBPer = (kBLoads + kWaves - 1) / kWaves;
   static constexpr int kPer = kAPer + kBPer;
-  // bfloat16 results go out through 32 rows of kOutM columns a wave
-  static constexpr int kOutM = MT % 2 == 0 && S * kStage + kWaves * 32 * 64 * 2 <= 163840 ? 64 : 32;
-  static constexpr int kOutBytes = 32 * kOutM * 2;
+  static constexpr int kOutBytes = 32 * 32 * 4;  // of a wave, for results on their way out
   static constexpr int kLds = S * kStage + kWaves * kOutBytes;
 };
 
@@ -88,7 +111,8 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void linear_tile_kernel(LinearProdu
     nk = k_hi > k_lo ? (int)((k_hi - k_lo + kTK - 1) / kTK) : 0;
     // With one tile of rows every workgroup reads other weight rows, and begun together all
     // ask for the same columns of rows a power of two apart, so for few of the memory's
-    // channels at a time: each begins its walk along k elsewhere.
+    // channels at a time: each begins its walk along k elsewhere.  Tiles of the same weight
+    // rows share their loads, and begin together.
     if (!C::kAOuter && !SHARED) shift = nt == 1 ? (int)((uint32_t)job * 2654435761u >> 16) % nk : 0;
     na = nb = kBufMost;
 #pragma unroll
@@ -301,11 +325,8 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void linear_tile_kernel(LinearProdu
     }
 
     // A lane holds column n = lane % 32 of each 32 x 32 product and rows
-    // 8 (r / 4) + 4 (lane / 32) + r % 4: in the lane's wave, row_of + mw of the tile.
-    auto row_of = [](int i, int r) { return i * 32 + 8 * (r >> 2) + (r & 3); };
-    const int mw = wm + 4 * fh;
-    const int m_left = (int)(M - em0 < BM ? M - em0 : BM) - mw;  // rows of the lane that exist
-    if (SHARED) {
+    // 8 (r / 4) + 4 (lane / 32) + r % 4.
+    if constexpr (SHARED) {
       // part worker + job of the slab, [BN][BM]: each pair of them is met once
       float* part = p.slab + (int64_t)(worker + done) * (BM * BN);
 #pragma unroll
@@ -316,97 +337,77 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void linear_tile_kernel(LinearProdu
         for (int i = 0; i < MT; ++i)
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
-            if (row_of(i, q * 4) >= m_left) continue;
+            const int ml = wm + 4 * fh + i * 32 + q * 8;
+            if (em0 + ml >= M) continue;
             const f32x4 v = {acc[i][j][q * 4], acc[i][j][q * 4 + 1], acc[i][j][q * 4 + 2], acc[i][j][q * 4 + 3]};
-            *(f32x4*)(part + nl * BM + mw + row_of(i, q * 4)) = v;
+            *(f32x4*)(part + nl * BM + ml) = v;
           }
       }
     } else {
-      // out = residual + act(acc + bias); pass 0 writes acc + bias where it is wanted
-      const bool plain = MODE != kLinForward;
-      for (int pass = plain || p.pre == nullptr ? 1 : 0; pass < 2; ++pass) {
-        void* to = pass == 0 ? p.pre : p.out;
-        const int64_t ldo = pass == 0 ? p.ldp : p.ldo;
-        const bool to_bf16 = pass == 0 || MODE != kLinForward ? C::kBf16 : p.out_bf16 != 0;
-        const bool biased = !plain && p.bias != nullptr, added = !plain && pass == 1 && p.residual != nullptr;
-        auto finish = [&](int i, int j, int q, float (&v)[4]) {
-          const int ml = row_of(i, q * 4), left = m_left - ml;
+      // One product after the other goes through the wave's own part of LDS, 32 rows n of 32
+      // float32, 16-byte chunk c of row n at c ^ (n % 8), so that a lane gets 8 columns of a row
+      // and the epilogue stands in the code once.
+      char* own = lds + S * C::kStage + wave * C::kOutBytes;
+      // what the epilogue reads of a product's place: asked for two products ahead
+      struct Beside {
+        Raw8<T> bias, residual[2];
+      };
+      auto ask = [&](int block, Beside& x) {
+        if constexpr (MODE == kLinForward) {
+          const int64_t m = em0 + wm + block / NT * 32 + (lane & 3) * 8;
+          const int left = (int)(M - m < 8 ? M - m : 8);
+          if (p.bias != nullptr) load_raw(x.bias, (const T*)p.bias + m, left);
+          if (p.residual != nullptr) {
 #pragma unroll
-          for (int e = 0; e < 4; ++e) v[e] = acc[i][j][q * 4 + e];
-          if (plain || left <= 0) return;
-          if (biased) {
-            float b[4];
-            load_some<T, 4>((const T*)p.bias + em0 + mw + ml, left, b);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] += b[e];
-          }
-          if (pass == 1 && p.act != ARCS_ACT_NONE) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] = act_value(v[e], p.act, p.cap);
-          }
-          const int64_t n = en0 + wn + j * 32 + fr;
-          if (added && n < N) {
-            float r[4];
-            load_some<T, 4>((const T*)p.residual + n * p.ldr + em0 + mw + ml, left, r);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) v[e] += r[e];
-          }
-        };
-        if (!to_bf16) {
-#pragma unroll
-          for (int j = 0; j < NT; ++j) {
-            const int64_t n = en0 + wn + j * 32 + fr;
-#pragma unroll
-            for (int i = 0; i < MT; ++i)
-#pragma unroll
-              for (int q = 0; q < 4; ++q) {
-                float v[4];
-                finish(i, j, q, v);
-                const int left = m_left - row_of(i, q * 4);
-                if (n < N && left > 0) store_some<float, 4>((float*)to + n * ldo + em0 + mw + row_of(i, q * 4), left, v);
-              }
-          }
-        } else {
-          // 32 rows n of kOutM columns at a time through the wave's own part of LDS, so
-          // that whole lines are stored.  16-byte chunk c of row n at c ^ n.
-          constexpr int kOutM = C::kOutM, kChunks = kOutM / 8, kTiles = kOutM / 32;
-          char* own = lds + (SHARED ? 0 : S * C::kStage + wave * C::kOutBytes);
-#pragma unroll
-          for (int j = 0; j < NT; ++j)
-#pragma unroll
-            for (int i0 = 0; i0 < MT; i0 += kTiles) {
-#pragma unroll
-              for (int i = i0; i < i0 + kTiles; ++i)
-#pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                  float v[4];
-                  finish(i, j, q, v);
-                  bf16x4 w;
-#pragma unroll
-                  for (int e = 0; e < 4; ++e) w[e] = (__bf16)v[e];
-                  const int ml = row_of(i - i0, q * 4) + 4 * fh;
-                  *(bf16x4*)(own + fr * (kOutM * 2) + (((ml >> 3) ^ (fr & (kChunks - 1))) * 16) + (ml & 4) * 2) = w;
-                }
-              wait_lds();
-              const int64_t ms = em0 + wm + i0 * 32;
-#pragma unroll
-              for (int t = 0; t < 32 * kChunks / 64; ++t) {
-                const int nl = (t * 64 + lane) / kChunks, c = (t * 64 + lane) % kChunks;
-                const int64_t n = en0 + wn + j * 32 + nl, m = ms + c * 8;
-                const u32x4 v = *(const u32x4*)(own + nl * (kOutM * 2) + ((c ^ (nl & (kChunks - 1))) * 16));
-                if (n >= N || m >= M) continue;
-                uint16_t* at = (uint16_t*)to + n * ldo + m;
-                if (m + 8 <= M) {
-                  store16(at, v);
-                } else {
-#pragma unroll
-                  for (int e = 0; e < 8; ++e)
-                    if (m + e < M) at[e] = (uint16_t)(v[e >> 1] >> (16 * (e & 1)));
-                }
-              }
-              wait_lds();  // read before the next columns are written
+            for (int t = 0; t < 2; ++t) {
+              const int64_t n = en0 + wn + block % NT * 32 + t * 16 + (lane >> 2);
+              load_raw(x.residual[t], (const T*)p.residual + n * p.ldr + m, n < N ? left : 0);
             }
+          }
         }
+      };
+      auto finish = [&](int block, const Beside& x) {
+        asm volatile("" : "+s"(block));  // a branch for each product, not a select of their registers
+#pragma unroll
+        for (int c = 0; c < MT * NT; ++c) {
+          if (block != c) continue;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const f32x16& y = acc[c / NT][c % NT];
+            const f32x4 v = {y[q * 4], y[q * 4 + 1], y[q * 4 + 2], y[q * 4 + 3]};
+            *(f32x4*)(own + fr * 128 + (((q * 2 + fh) ^ (fr & 7)) * 16)) = v;
+          }
+        }
+        wait_lds();
+        const int64_t m = em0 + wm + block / NT * 32 + (lane & 3) * 8;
+        const int left = (int)(M - m < 8 ? M - m : 8);
+        float bias[8], residual[8];
+        widen_raw(x.bias, bias);
+#pragma unroll
+        for (int t = 0; t < 2; ++t) {
+          const int nl = t * 16 + (lane >> 2), c = (lane & 3) * 2;
+          const int64_t n = en0 + wn + block % NT * 32 + nl;
+          const f32x4 y0 = *(const f32x4*)(own + nl * 128 + ((c ^ (nl & 7)) * 16));
+          const f32x4 y1 = *(const f32x4*)(own + nl * 128 + (((c + 1) ^ (nl & 7)) * 16));
+          float v[8] = {y0[0], y0[1], y0[2], y0[3], y1[0], y1[1], y1[2], y1[3]};
+          widen_raw(x.residual[t], residual);
+          if (n < N && left > 0) linear_finish<T, MODE == kLinForward, 8>(p, n, m, left, v, bias, residual);
+        }
+        wait_lds();  // read before the next product is written
+      };
+      constexpr int kBlocks = MT * NT;
+      Beside x = {}, y = {};
+      ask(0, x);
+      if constexpr (kBlocks > 1) {
+        ask(1, y);
+        for (int block = 0; block < kBlocks; block += 2) {
+          finish(block, x);
+          if (block + 2 < kBlocks) ask(block + 2, x);
+          finish(block + 1, y);
+          if (block + 3 < kBlocks) ask(block + 3, y);
+        }
+      } else {
+        finish(0, x);
       }
     }
     if (!more) break;
@@ -426,82 +427,34 @@ __global__ __launch_bounds__(256) void linear_join_kernel(LinearProduct p) {
   f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll 4
   for (int w = lo; w < hi; ++w) sum += *(const f32x4*)(part + (int64_t)w * (BN * BM));
-  const int left = (int)(p.M - m < 4 ? p.M - m : 4);
   float v[4] = {sum[0], sum[1], sum[2], sum[3]};
-  if (FORWARD) {
-    if (p.bias != nullptr) {
-      float b[4];
-      load_some<T, 4>((const T*)p.bias + m, left, b);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] += b[e];
-    }
-    if (p.pre != nullptr) store_some<T, 4>((T*)p.pre + n * p.ldp + m, left, v);
-    if (p.act != ARCS_ACT_NONE) {
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] = act_value(v[e], p.act, p.cap);
-    }
-    if (p.residual != nullptr) {
-      float r[4];
-      load_some<T, 4>((const T*)p.residual + n * p.ldr + m, left, r);
-#pragma unroll
-      for (int e = 0; e < 4; ++e) v[e] += r[e];
-    }
-    if (p.out_bf16) store_some<__bf16, 4>((__bf16*)p.out + n * p.ldo + m, left, v);
-    else store_some<float, 4>((float*)p.out + n * p.ldo + m, left, v);
-  } else {
-    store_some<T, 4>((T*)p.out + n * p.ldo + m, left, v);
-  }
+  const int left = (int)(p.M - m < 4 ? p.M - m : 4);
+  float bias[4] = {}, residual[4] = {};
+  if (FORWARD && p.bias != nullptr) load_some<T, 4>((const T*)p.bias + m, left, bias);
+  if (FORWARD && p.residual != nullptr) load_some<T, 4>((const T*)p.residual + n * p.ldr + m, left, residual);
+  linear_finish<T, FORWARD, 4>(p, n, m, left, v, bias, residual);
 }
 
-namespace {
-
-int64_t tiles(int64_t n, int64_t t) { return (n + t - 1) / t; }
+inline int64_t linear_tiles(int64_t n, int64_t t) { return (n + t - 1) / t; }
 
 template <typename T, int MODE, int WM, int WN, int MT, int NT, int S>
-void launch_tile(const LinearProduct& p, hipStream_t stream) {
+bool launch_linear_tile(const LinearProduct& p, hipStream_t stream) {
   using C = LinTile<T, MODE, WM, WN, MT, NT, S>;
+  if (p.shape.columns != C::BM || p.shape.rows != C::BN) return false;
   if (p.shape.workers > 0) {
     hipLaunchKernelGGL((linear_tile_kernel<T, MODE, WM, WN, MT, NT, S, true>), dim3((unsigned)p.shape.workers),
                        dim3(C::kThreads), 0, stream, p);
-    hipLaunchKernelGGL((linear_join_kernel<T, MODE == kLinForward>), dim3((unsigned)p.N, (unsigned)tiles(p.M, 1024)),
-                       dim3(256), 0, stream, p);
-    return;
+    hipLaunchKernelGGL((linear_join_kernel<T, MODE == kLinForward>),
+                       dim3((unsigned)p.N, (unsigned)linear_tiles(p.M, 1024)), dim3(256), 0, stream, p);
+    return true;
   }
   // as many workgroups as the compute units hold (by LDS), at most
   constexpr int64_t kMost = 256 * (163840 / C::kLds);
-  const int64_t all = tiles(p.M, C::BM) * tiles(p.N, C::BN);
-  const int64_t blocks = all < kMost ? tiles(all, 8) * 8 : kMost;
+  const int64_t all = linear_tiles(p.M, C::BM) * linear_tiles(p.N, C::BN);
+  const int64_t blocks = all < kMost ? linear_tiles(all, 8) * 8 : kMost;
   hipLaunchKernelGGL((linear_tile_kernel<T, MODE, WM, WN, MT, NT, S, false>), dim3((unsigned)blocks),
                      dim3(C::kThreads), 0, stream, p);
-}
-
-template <typename T, int MODE>
-void launch_mode(const LinearProduct& p, hipStream_t stream) {
-  launch_tile<T, MODE, 2, 2, 2, 2, 2>(p, stream);
-}
-
-}  // namespace
-
-LinearShape linear_shape(int mode, int64_t M, int64_t N, int64_t K, bool bf16) {
-  (void)mode;
-  (void)bf16;
-  const int64_t all = tiles(M, 128) * tiles(N, 128), tiles_k = tiles(K, bf16 ? 64 : 32);
-  LinearShape s = {128, 128, 0};
-  if (all < 256 && all * tiles_k >= 512) s.workers = 256;
-  return s;
-}
-
-hipError_t launch_linear_product(const LinearProduct& p, int mode, int dtype, hipStream_t stream) {
-  if (dtype == ARCS_DTYPE_BF16) {
-    if (mode == kLinForward) launch_mode<__bf16, kLinForward>(p, stream);
-    else if (mode == kLinDhidden) launch_mode<__bf16, kLinDhidden>(p, stream);
-    else launch_mode<__bf16, kLinDweight>(p, stream);
-  } else {
-    if (mode == kLinForward) launch_mode<float, kLinForward>(p, stream);
-    else if (mode == kLinDhidden) launch_mode<float, kLinDhidden>(p, stream);
-    else launch_mode<float, kLinDweight>(p, stream);
-  }
-  return hipGetLastError();
+  return true;
 }
 
 }  // namespace arcs

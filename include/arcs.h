@@ -61,7 +61,7 @@ typedef enum arcs_status {
   ARCS_ERR_BAD_DRY = -14,            /* arcs_sample_dry: breakers NULL or n_breakers outside [0, 64] */
   ARCS_ERR_BAD_HIDDEN = -15,         /* hidden size D outside [1, ARCS_MAX_HIDDEN] */
   ARCS_ERR_BAD_GROUP = -16,          /* arcs_w4_logits: group_size not 32, 64 or 128, or no divisor of D */
-  ARCS_ERR_BAD_ACTIVATION = -17,     /* arcs_linear: no arcs_activation, or softcap not positive and finite */
+  ARCS_ERR_BAD_ACTIVATION = -17,     /* arcs_linear: no arcs_activation, or softcap outside 2^-100 .. 2^100 */
   ARCS_ERR_BAD_BIAS = -18,           /* arcs_adjust_logits: some of the three bias arrays are NULL, not all */
   ARCS_ERR_BAD_MASK = -19,           /* arcs_adjust_logits: mask_rows without a mask, or fewer masks than rows */
   ARCS_ERR_OVERLAP = -20,            /* an output overlaps an input and is not that input in place */
@@ -572,7 +572,7 @@ typedef enum arcs_activation {
  *   weight      device [V, weight_stride] of dtype, weight_stride >= D
  *   bias        device [V] of dtype, or NULL
  *   activation  an arcs_activation; softcap is read for ARCS_ACT_SOFTCAP only,
- *               and has to be positive and finite there
+ *               and has to be within 2^-100 .. 2^100 there
  *   residual    device [N, residual_stride] of dtype, residual_stride >= V, or NULL
  *   out         device [N, out_stride] of out_dtype, out_stride >= V; may be
  *               the residual itself where type and stride are the same
