@@ -174,8 +174,9 @@ struct NormArgs {
   int groups;    // set by the launch
 };
 constexpr int64_t kNormPiece = 4096;  // elements of a piece at most
-// Workgroups of the launches.
-inline int norm_groups(int64_t pieces) { return (int)(pieces < 2048 ? pieces : 2048); }
+// Workgroups of the launches: eight of 256 threads a compute unit at most.
+constexpr int kNormGroups = 2048;
+inline int norm_groups(int64_t pieces) { return (int)(pieces < kNormGroups ? pieces : kNormGroups); }
 hipError_t launch_norm(NormArgs a, bool clip, hipStream_t stream);
 
 hipError_t launch_argmax(const void* logits, int dtype, int64_t B, int64_t V, int64_t stride,

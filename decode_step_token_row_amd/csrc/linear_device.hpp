@@ -143,7 +143,7 @@ struct __attribute__((packed, aligned(2))) Bytes16 {
   u32x4 v;
 };
 struct __attribute__((packed, aligned(2))) Bytes8 {
-  uint32_t x, y;
+  uint64_t v;
 };
 __device__ __forceinline__ u32x4 load16(const void* p) { return ((const Bytes16*)p)->v; }
 __device__ __forceinline__ void store16(void* p, u32x4 v) { ((Bytes16*)p)->v = v; }
