@@ -227,9 +227,15 @@ def linear_workspace_bytes(N: int, V: int, D: int, dtype: int, rows_aligned: boo
 # None).  The caller orders it against the streams that make the inputs and read
 # the results; tensors may be dropped as soon as the call returns.
 # --------------------------------------------------------------------------
+_torch_module = None
+
+
 def _torch():
-    import torch
-    return torch
+    global _torch_module
+    if _torch_module is None:
+        import torch
+        _torch_module = torch
+    return _torch_module
 
 
 def _stream_ptr(stream) -> int:
@@ -771,25 +777,27 @@ def linear_cross_entropy_backward(hidden, weight, targets, lse, grad_loss, tempe
 # --------------------------------------------------------------------------
 # linear layers
 # --------------------------------------------------------------------------
-def _rows_aligned(t, stride: int) -> bool:
-    """Whether the rows of a matrix are on the 16-byte grid, as arcs_linear asks."""
-    each = 16 // t.element_size()
-    return (t.data_ptr() % 16 == 0 and stride % each == 0 and t.shape[1] % each == 0
-            and stride * t.element_size() < 2**23)
-
-
+# One token's call takes as long on the host as on the card, so what follows looks each
+# attribute up once and checks only what the caller gave.
 def _linear_inputs(hidden, weight, activation, softcap):
-    N, D, dev = _hidden_shape(hidden)
-    dt = _dtype_code_of(hidden, "hidden")
-    if weight.dim() != 2:
-        raise ValueError("weight must be [V, D]")
+    """Sizes, device, type code and strides of the two matrices, the activation's code, and
+    whether their rows are on the 16-byte grid as arcs_linear_workspace_bytes asks."""
+    if not hidden.is_cuda:
+        raise ValueError("hidden must be a device tensor")
+    if hidden.dim() != 2 or weight.dim() != 2:
+        raise ValueError("hidden must be [rows, D] and weight [V, D]")
+    N, D = hidden.shape
     V = weight.shape[0]
-    hs = _matrix(hidden, "hidden", hidden.dtype, N, D, dev)
-    ws = _matrix(weight, "weight", hidden.dtype, V, D, dev)
+    dev, dtype = hidden.device, hidden.dtype
+    dt = _dtype_code_of(hidden, "hidden")
+    hs = _matrix(hidden, "hidden", dtype, N, D, dev)
+    ws = _matrix(weight, "weight", dtype, V, D, dev)
     act = ACTIVATIONS.get(activation)
     if act is None:
         raise ValueError(f"activation must be one of {', '.join(ACTIVATIONS)}")
-    return N, V, D, dev, dt, hs, ws, act, float(softcap), _rows_aligned(hidden, hs) and _rows_aligned(weight, ws)
+    size = 4 if dt == DTYPE_F32 else 2
+    aligned = ((hidden.data_ptr() | weight.data_ptr() | (hs | ws | D) * size) & 15) == 0 and max(hs, ws) * size < 2**23
+    return N, V, D, dev, dtype, dt, hs, ws, act, aligned
 
 
 def linear(hidden, weight, bias=None, activation: str = "none", softcap: float = 0.0, residual=None, out=None,
@@ -806,28 +814,31 @@ def linear(hidden, weight, bias=None, activation: str = "none", softcap: float =
     has no autograd graph.
     """
     torch = _torch()
-    N, V, D, dev, dt, hs, ws, act, cap, aligned = _linear_inputs(hidden, weight, activation, softcap)
+    N, V, D, dev, dtype, dt, hs, ws, act, aligned = _linear_inputs(hidden, weight, activation, softcap)
     if bias is not None:
-        _vector(bias, "bias", hidden.dtype, V, dev)
-    rs = 0 if residual is None else _matrix(residual, "residual", hidden.dtype, N, V, dev)
+        _vector(bias, "bias", dtype, V, dev)
+    rs = 0 if residual is None else _matrix(residual, "residual", dtype, N, V, dev)
     with _work_on(dev, stream):
         if out is None:
-            out = torch.empty((N, V), dtype=hidden.dtype if out_dtype is None else out_dtype, device=dev)
-        elif out_dtype is not None and out.dtype != out_dtype:
-            raise ValueError("out is not of out_dtype")
+            out = torch.empty((N, V), dtype=dtype if out_dtype is None else out_dtype, device=dev)
+            os_ = V
+        else:
+            if out_dtype is not None and out.dtype != out_dtype:
+                raise ValueError("out is not of out_dtype")
+            os_ = _matrix(out, "out", out.dtype, N, V, dev)
         odt = _dtype_code_of(out, "out")
-        os_ = _matrix(out, "out", out.dtype, N, V, dev)
-        if out_pre is None and want_pre:
-            out_pre = torch.empty((N, V), dtype=hidden.dtype, device=dev)
         if out_pre is not None:
-            _vector(out_pre, "out_pre", hidden.dtype, N * V, dev)
+            _vector(out_pre, "out_pre", dtype, N * V, dev)
+        elif want_pre:
+            out_pre = torch.empty((N, V), dtype=dtype, device=dev)
         workspace, ws_bytes = _head_workspace(workspace, linear_workspace_bytes(N, V, D, dt, aligned), dev)
-        st = library().arcs_linear(_ptr(hidden), hs, _ptr(weight), ws, dt, N, V, D, _ptr(bias), act, cap,
-                                   _ptr(residual), rs, _ptr(out), odt, os_, _ptr(out_pre), _ptr(workspace), ws_bytes,
-                                   _head_stream(stream, dev))
+        st = library().arcs_linear(hidden.data_ptr(), hs, weight.data_ptr(), ws, dt, N, V, D, _ptr(bias), act, softcap,
+                                   _ptr(residual), rs, out.data_ptr(), odt, os_, _ptr(out_pre), _ptr(workspace),
+                                   ws_bytes, _head_stream(stream, dev))
     if st != OK:
         raise ArcsError(st, "arcs_linear")
-    _head_used(stream, dev, (hidden, weight, bias, residual, workspace), (out, out_pre))
+    if stream is not None:
+        _head_used(stream, dev, (hidden, weight, bias, residual, workspace), (out, out_pre))
     return out if out_pre is None else (out, out_pre)
 
 
@@ -841,29 +852,30 @@ def linear_backward(hidden, weight, grad_out, pre=None, activation: str = "none"
     call's (not needed without an activation).  The residual's gradient is grad_out.
     """
     torch = _torch()
-    N, V, D, dev, dt, hs, ws, act, cap, aligned = _linear_inputs(hidden, weight, activation, softcap)
+    N, V, D, dev, dtype, dt, hs, ws, act, aligned = _linear_inputs(hidden, weight, activation, softcap)
     gdt = _dtype_code_of(grad_out, "grad_out")
     gs = _matrix(grad_out, "grad_out", grad_out.dtype, N, V, dev)
     if pre is not None:
-        _vector(pre, "pre", hidden.dtype, N * V, dev)
+        _vector(pre, "pre", dtype, N * V, dev)
     with _work_on(dev, stream):
         if want_hidden and out_dhidden is None:
-            out_dhidden = torch.empty((N, D), dtype=hidden.dtype, device=dev)
+            out_dhidden = torch.empty((N, D), dtype=dtype, device=dev)
         if want_weight and out_dweight is None:
-            out_dweight = torch.empty((V, D), dtype=hidden.dtype, device=dev)
+            out_dweight = torch.empty((V, D), dtype=dtype, device=dev)
         if want_bias and out_dbias is None:
-            out_dbias = torch.empty(V, dtype=hidden.dtype, device=dev)
+            out_dbias = torch.empty(V, dtype=dtype, device=dev)
         for t, name, n in ((out_dhidden, "out_dhidden", N * D), (out_dweight, "out_dweight", V * D),
                            (out_dbias, "out_dbias", V)):
             if t is not None:
-                _vector(t, name, hidden.dtype, n, dev)
+                _vector(t, name, dtype, n, dev)
         workspace, ws_bytes = _head_workspace(workspace, linear_workspace_bytes(N, V, D, dt, aligned, True), dev)
-        st = library().arcs_linear_backward(_ptr(hidden), hs, _ptr(weight), ws, dt, N, V, D, act, cap, _ptr(pre),
+        st = library().arcs_linear_backward(_ptr(hidden), hs, _ptr(weight), ws, dt, N, V, D, act, softcap, _ptr(pre),
                                             _ptr(grad_out), gdt, gs, _ptr(out_dhidden), _ptr(out_dweight),
                                             _ptr(out_dbias), _ptr(workspace), ws_bytes, _head_stream(stream, dev))
     if st != OK:
         raise ArcsError(st, "arcs_linear_backward")
-    _head_used(stream, dev, (hidden, weight, grad_out, pre, workspace), (out_dhidden, out_dweight, out_dbias))
+    if stream is not None:
+        _head_used(stream, dev, (hidden, weight, grad_out, pre, workspace), (out_dhidden, out_dweight, out_dbias))
     return out_dhidden, out_dweight, out_dbias
 
 
@@ -925,10 +937,12 @@ def adjust_logits(logits, params=None, hist_ids=None, hist_offsets=None, bias_id
     with _work_on(dev, stream):
         if out is None:
             out = torch.empty((B, V), dtype=logits.dtype if out_dtype is None else out_dtype, device=dev)
-        elif out_dtype is not None and out.dtype != out_dtype:
-            raise ValueError("out is not of out_dtype")
+            os_ = V
+        else:
+            if out_dtype is not None and out.dtype != out_dtype:
+                raise ValueError("out is not of out_dtype")
+            os_ = _matrix(out, "out", out.dtype, B, V, dev)
         odt = _dtype_code_of(out, "out")
-        os_ = _matrix(out, "out", out.dtype, B, V, dev)
         if out_status is not None:
             _vector(out_status, "out_status", torch.int32, B, dev)
         st = library().arcs_adjust_logits(_ptr(logits), dt, B, V, stride, _ptr(params), _list_ptr(hist_ids),
@@ -937,8 +951,9 @@ def adjust_logits(logits, params=None, hist_ids=None, hist_offsets=None, bias_id
                                           _ptr(out), odt, os_, _ptr(out_status), _head_stream(stream, dev))
     if st != OK:
         raise ArcsError(st, "arcs_adjust_logits")
-    _head_used(stream, dev, (logits, params, hist_ids, hist_offsets, bias_ids, bias_values, bias_offsets, mask,
-                             mask_rows), (out, out_status))
+    if stream is not None:
+        _head_used(stream, dev, (logits, params, hist_ids, hist_offsets, bias_ids, bias_values, bias_offsets, mask,
+                                 mask_rows), (out, out_status))
     return out
 
 
@@ -1013,7 +1028,8 @@ def _norm_call(tensors, out_norm, workspace, stream, name, *more):
     with _work_on(dev, stream):
         if out_norm is None:
             out_norm = torch.empty(1, dtype=torch.float32, device=dev)
-        _vector(out_norm, "out_norm", torch.float32, 1, dev)
+        else:
+            _vector(out_norm, "out_norm", torch.float32, 1, dev)
         workspace, ws_bytes = _head_workspace(workspace, tensors.workspace_bytes, dev)
         st = getattr(library(), name)(_list_ptr(tensors.plan), tensors.plan_bytes, *more, _ptr(out_norm),
                                       _ptr(workspace), ws_bytes, _head_stream(stream, dev))

@@ -12,9 +12,9 @@ namespace arcs {
 // ---------------------------------------------------------------------------
 // forward, few rows
 // ---------------------------------------------------------------------------
-// A workgroup makes 16 columns of the output for all rows: its waves take the steps of k in
-// turn, weights and hidden states straight from memory to registers (16 bytes a lane: the
-// lane's row, 8 k of bfloat16 or 4 of float32), and their sums meet in LDS.
+// A workgroup makes 16 columns of the output for all rows: its waves take blocks of 128 bytes of k
+// in turn, weights and hidden states straight from memory to registers (a line of each of
+// 16 weight rows in two loads, 16 bytes a lane), U blocks in flight, and their sums meet in LDS.
 constexpr int kFewWaves = 8;
 
 template <typename T>
@@ -41,34 +41,65 @@ __device__ __forceinline__ f32x4 few_product(u32x4 x, u32x4 y, f32x4 c) {
   }
 }
 
-template <typename T>
+template <typename T, int U, int R>
 __global__ __launch_bounds__(kFewWaves * 64) void linear_few_kernel(LinearArgs a) {
-  constexpr int kStep = 64 / sizeof(T);  // k of one product: 16 bytes in each of four lanes of a row
-  __shared__ float part[kFewWaves][16][17];
-  const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-  const int64_t v0 = (int64_t)blockIdx.x * 16;
+  constexpr int E = 16 / sizeof(T), kBlock = 8 * E;  // elements of a load, and of a block of k
+  __shared__ float part[kFewWaves][R][16][17];
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int64_t v0 = (int64_t)blockIdx.x * (16 * R);
   const int r = lane & 15, q = lane >> 4;
   // rows past the last one repeat it, and are not stored
-  const int64_t v = v0 + r < a.V ? v0 + r : a.V - 1;
   const int64_t n = r < a.N ? r : a.N - 1;
-  const T* w = (const T*)a.weight + v * a.weight_stride;
   const T* h = (const T*)a.hidden + n * a.hidden_stride;
-  f32x4 acc = {0.0f, 0.0f, 0.0f, 0.0f};
-#pragma unroll 4
-  for (int64_t k = (int64_t)wave * kStep; k < a.D; k += kFewWaves * kStep) {
-    const int64_t at = k + q * (16 / (int)sizeof(T));
-    acc = few_product<T>(few_load(w, at, a.D), few_load(h, at, a.D), acc);
+  const T* w[R];
+  f32x4 acc[R];
+#pragma unroll
+  for (int i = 0; i < R; ++i) {
+    const int64_t v = v0 + i * 16 + r;
+    w[i] = (const T*)a.weight + (v < a.V ? v : a.V - 1) * a.weight_stride;
+    acc[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+  }
+  const int blocks = (int)(a.D / kBlock);  // whole ones
+  for (int b0 = wave; b0 < blocks; b0 += kFewWaves * U) {
+    u32x4 x[U][R][2], y[U][2];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int b = b0 + u * kFewWaves;
+      if (b >= blocks) continue;
+#pragma unroll
+      for (int t = 0; t < 2; ++t) {
+#pragma unroll
+        for (int i = 0; i < R; ++i) x[u][i][t] = load16(w[i] + b * kBlock + t * 4 * E + q * E);
+        y[u][t] = load16(h + b * kBlock + t * 4 * E + q * E);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      if (b0 + u * kFewWaves >= blocks) continue;
+#pragma unroll
+      for (int t = 0; t < 2; ++t)
+#pragma unroll
+        for (int i = 0; i < R; ++i) acc[i] = few_product<T>(x[u][i][t], y[u][t], acc[i]);
+    }
+  }
+  // what is left of k, by the wave whose turn it is
+  if (wave == blocks % kFewWaves) {
+    for (int64_t k = (int64_t)blocks * kBlock; k < a.D; k += 4 * E)
+#pragma unroll
+      for (int i = 0; i < R; ++i) acc[i] = few_product<T>(few_load(w[i], k + q * E, a.D), few_load(h, k + q * E, a.D), acc[i]);
   }
 #pragma unroll
-  for (int e = 0; e < 4; ++e) part[wave][q * 4 + e][r] = acc[e];
+  for (int i = 0; i < R; ++i)
+#pragma unroll
+    for (int e = 0; e < 4; ++e) part[wave][i][q * 4 + e][r] = acc[i][e];
   __syncthreads();
-  // thread: column v0 + tid % 16 of row tid / 16
-  if (tid >= 256) return;
-  const int c = tid & 15, row = tid >> 4;
+  // thread: column tid % (16 R) of row tid / (16 R)
+  const int c = tid % (16 * R), row = tid / (16 * R);
   if (row >= a.N || v0 + c >= a.V) return;
   float z = 0.0f;
 #pragma unroll
-  for (int i = 0; i < kFewWaves; ++i) z += part[i][c][row];
+  for (int i = 0; i < kFewWaves; ++i) z += part[i][c / 16][c % 16][row];
   if (a.bias != nullptr) z += widen(((const T*)a.bias)[v0 + c]);
   if (a.out_pre != nullptr) ((T*)a.out_pre)[row * a.V + v0 + c] = (T)z;
   float y[1] = {z};
@@ -195,7 +226,15 @@ void pack_operands(LinearArgs& a, const LinearPlan& plan, int dtype, hipStream_t
 template <typename T>
 hipError_t forward(LinearArgs a, int dtype, bool aligned, hipStream_t stream) {
   if (a.N <= kLinearFewRows) {
-    hipLaunchKernelGGL(linear_few_kernel<T>, dim3((unsigned)tiles(a.V, 16)), dim3(kFewWaves * 64), 0, stream, a);
+    // More rows read the hidden states for fewer columns at a time more often, few columns leave
+    // compute units without work: 16 rows x 129,280 x 4,096 210 us with 32 columns a workgroup and
+    // 248 with 16, 8 x 32,000 x 1,001 28 and 33, but one row x 129,280 193 and 168 and 8 x 4,096 x
+    // 4,096 13.6 and 10.2.
+    const dim3 threads(kFewWaves * 64);
+    if (a.N > 4 && a.V >= 16384)
+      hipLaunchKernelGGL((linear_few_kernel<T, 4, 2>), dim3((unsigned)tiles(a.V, 32)), threads, 0, stream, a);
+    else
+      hipLaunchKernelGGL((linear_few_kernel<T, 4, 1>), dim3((unsigned)tiles(a.V, 16)), threads, 0, stream, a);
     return hipGetLastError();
   }
   const LinearPlan plan = linear_plan(a.N, a.V, a.D, dtype, aligned, false);
