@@ -289,25 +289,66 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void linear_tile_kernel(LinearProdu
     __builtin_amdgcn_s_barrier();
     read(0, 0);
     for (int kt = 0; kt < nk; ++kt) {
+      constexpr int kProducts = MT * NT;
+      if constexpr (S == 2) {
+        // Two deep, the next loads go out as soon as every wave has read its last fragments of
+        // the tile: the workgroup meets once more for that, halfway through step 2.
+        constexpr int kHalf = kProducts / 2, kEarly = C::kPer / 2;
 #pragma unroll
-      for (int ks = 0; ks < 3; ++ks) {
-        read(kt, ks + 1);
-        multiply(ks);
-      }
-      const Source from = source(kt + S);
-      wait_loads<(S - 2) * C::kPer>();  // tile kt + 1 has landed
-      wait_lds();                       // this wave's reads of tile kt are done
-      __builtin_amdgcn_s_barrier();
-      read(kt + 1, 0);
-      // the loads go between the products, which run on while one is issued
-      constexpr int kProducts = MT * NT, kEach = (C::kPer + kProducts - 1) / kProducts;
+        for (int ks = 0; ks < 2; ++ks) {
+          read(kt, ks + 1);
+          multiply(ks);
+        }
+        read(kt, 3);
+        const Source from = source(kt + S);
 #pragma unroll
-      for (int q = 0; q < kProducts; ++q) {
-        acc[q / NT][q % NT] = product(fa[1][q / NT], fb[1][q % NT], acc[q / NT][q % NT]);
+        for (int q = 0; q < kHalf; ++q)
+          acc[q / NT][q % NT] = product(fa[0][q / NT], fb[0][q % NT], acc[q / NT][q % NT]);
         __builtin_amdgcn_sched_barrier(0);
+        wait_lds();
+        __builtin_amdgcn_s_barrier();
+        constexpr int kRest = kProducts - kHalf, kEach1 = (kEarly + kRest - 1) / kRest;
 #pragma unroll
-        for (int l = q * kEach; l < (q + 1) * kEach && l < C::kPer; ++l) issue_one(from, l);
-        __builtin_amdgcn_sched_barrier(0);
+        for (int q = kHalf; q < kProducts; ++q) {
+          acc[q / NT][q % NT] = product(fa[0][q / NT], fb[0][q % NT], acc[q / NT][q % NT]);
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int l = (q - kHalf) * kEach1; l < (q - kHalf + 1) * kEach1 && l < kEarly; ++l) issue_one(from, l);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        wait_loads<kEarly>();  // tile kt + 1 has landed
+        __builtin_amdgcn_s_barrier();
+        read(kt + 1, 0);
+        constexpr int kEach2 = (C::kPer - kEarly + kProducts - 1) / kProducts;
+#pragma unroll
+        for (int q = 0; q < kProducts; ++q) {
+          acc[q / NT][q % NT] = product(fa[1][q / NT], fb[1][q % NT], acc[q / NT][q % NT]);
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int l = kEarly + q * kEach2; l < kEarly + (q + 1) * kEach2 && l < C::kPer; ++l) issue_one(from, l);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+      } else {
+#pragma unroll
+        for (int ks = 0; ks < 3; ++ks) {
+          read(kt, ks + 1);
+          multiply(ks);
+        }
+        const Source from = source(kt + S);
+        wait_loads<(S - 2) * C::kPer>();  // tile kt + 1 has landed
+        wait_lds();                       // this wave's reads of tile kt are done
+        __builtin_amdgcn_s_barrier();
+        read(kt + 1, 0);
+        // the loads go between the products, which run on while one is issued
+        constexpr int kEach = (C::kPer + kProducts - 1) / kProducts;
+#pragma unroll
+        for (int q = 0; q < kProducts; ++q) {
+          acc[q / NT][q % NT] = product(fa[1][q / NT], fb[1][q % NT], acc[q / NT][q % NT]);
+          __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+          for (int l = q * kEach; l < (q + 1) * kEach && l < C::kPer; ++l) issue_one(from, l);
+          __builtin_amdgcn_sched_barrier(0);
+        }
       }
     }
     wait_loads<0>();  // no load into LDS outlives its tile
