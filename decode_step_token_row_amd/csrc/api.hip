@@ -7,6 +7,7 @@
 #include <stdint.h>
 
 #include <atomic>
+#include <initializer_list>
 
 #include "arcs.h"
 #include "cross_entropy.hpp"
@@ -218,16 +219,27 @@ int check_linear(const void* hidden, int64_t hidden_stride, const void* weight, 
   return ARCS_OK;
 }
 
-// Whether any two rows of two row-major arrays share bytes.  Rows of equal strides may lie
-// between each other's.
-bool rows_overlap(const void* p, int64_t p_stride, int64_t p_size, const void* q, int64_t q_stride, int64_t q_size,
-                  int64_t rows, int64_t columns) {
-  const __int128 p0 = (intptr_t)p, q0 = (intptr_t)q, ps = (__int128)p_stride * p_size, qs = (__int128)q_stride * q_size;
-  const __int128 pl = (__int128)columns * p_size, ql = (__int128)columns * q_size;
-  if (p0 + ps * (rows - 1) + pl <= q0 || q0 + qs * (rows - 1) + ql <= p0) return false;
-  if (ps != qs || rows == 1) return true;
-  const __int128 d = ((q0 - p0) % ps + ps) % ps;
-  return d < pl || ps - d < ql;
+// A row-major array as its bytes lie.
+struct Rows {
+  const void* p;
+  int64_t stride, rows, columns, size;  // stride and columns in elements of `size` bytes
+};
+
+// Whether any two rows of two arrays share bytes.  Rows of equal strides may lie between
+// each other's.
+bool overlap(const Rows& x, const Rows& y) {
+  if (x.p == nullptr || y.p == nullptr) return false;
+  const __int128 x0 = (intptr_t)x.p, y0 = (intptr_t)y.p, xs = (__int128)x.stride * x.size, ys = (__int128)y.stride * y.size;
+  const __int128 xl = (__int128)x.columns * x.size, yl = (__int128)y.columns * y.size;
+  if (x0 + xs * (x.rows - 1) + xl <= y0 || y0 + ys * (y.rows - 1) + yl <= x0) return false;
+  if (xs != ys || x.rows == 1 || y.rows == 1) return true;
+  const __int128 d = ((y0 - x0) % xs + xs) % xs;
+  return d < xl || xs - d < yl;
+}
+bool overlaps_any(const Rows& x, std::initializer_list<Rows> others) {
+  for (const Rows& y : others)
+    if (overlap(x, y)) return true;
+  return false;
 }
 
 // A list of gradients, and how many pieces it has.
@@ -519,7 +531,13 @@ int arcs_linear(const void* hidden, int64_t hidden_stride, const void* weight, i
   if (misaligned(bias, es) || misaligned(residual, es) || misaligned(out_pre, es) ||
       misaligned(out, element_size(out_dtype)))
     return ARCS_ERR_MISALIGNED;
-  if (residual == out && (out_dtype != dtype || residual_stride != out_stride)) return ARCS_ERR_OVERLAP;
+  const int64_t size = (int64_t)es;
+  const Rows h = {hidden, hidden_stride, N, D, size}, w = {weight, weight_stride, V, D, size}, b = {bias, V, 1, V, size};
+  const Rows r = {residual, residual_stride, N, V, size}, pre = {out_pre, V, N, V, size};
+  const Rows y = {out, out_stride, N, V, (int64_t)element_size(out_dtype)};
+  const bool in_place = residual == out && out_dtype == dtype && (N == 1 || residual_stride == out_stride);
+  if (overlaps_any(y, {h, w, b, pre}) || (!in_place && overlap(y, r)) || overlaps_any(pre, {h, w, b, r}))
+    return ARCS_ERR_OVERLAP;
   arcs::LinearArgs a = {};
   a.hidden = hidden;
   a.hidden_stride = hidden_stride;
@@ -561,6 +579,12 @@ int arcs_linear_backward(const void* hidden, int64_t hidden_stride, const void* 
   if (misaligned(pre, es) || misaligned(grad_out, element_size(grad_dtype)) || misaligned(out_dhidden, es) ||
       misaligned(out_dweight, es) || misaligned(out_dbias, es))
     return ARCS_ERR_MISALIGNED;
+  const int64_t size = (int64_t)es;
+  const Rows h = {hidden, hidden_stride, N, D, size}, w = {weight, weight_stride, V, D, size}, z = {pre, V, N, V, size};
+  const Rows g = {grad_out, grad_stride, N, V, (int64_t)element_size(grad_dtype)};
+  const Rows dh = {out_dhidden, D, N, D, size}, dw = {out_dweight, D, V, D, size}, db = {out_dbias, V, 1, V, size};
+  if (overlaps_any(dh, {h, w, z, g, dw, db}) || overlaps_any(dw, {h, w, z, g, db}) || overlaps_any(db, {h, w, z, g}))
+    return ARCS_ERR_OVERLAP;
   arcs::LinearArgs a = {};
   a.hidden = hidden;
   a.hidden_stride = hidden_stride;
@@ -613,7 +637,8 @@ int arcs_adjust_logits(const void* logits, int dtype, int64_t B, int64_t V, int6
       misaligned(out, element_size(out_dtype)) || misaligned(out_status, 4))
     return ARCS_ERR_MISALIGNED;
   const bool in_place = out == logits && out_dtype == dtype && (B == 1 || out_stride == row_stride);
-  if (!in_place && rows_overlap(logits, row_stride, element_size(dtype), out, out_stride, element_size(out_dtype), B, V))
+  if (!in_place && overlap({logits, row_stride, B, V, (int64_t)element_size(dtype)},
+                           {out, out_stride, B, V, (int64_t)element_size(out_dtype)}))
     return ARCS_ERR_OVERLAP;
   arcs::AdjustArgs a = {};
   a.logits = logits;

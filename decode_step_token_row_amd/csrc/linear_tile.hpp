@@ -293,18 +293,25 @@ __global__ __launch_bounds__(WM* WN * 64, 2) void linear_tile_kernel(LinearProdu
       if constexpr (S == 2) {
         // Two deep, the next loads go out as soon as every wave has read its last fragments of
         // the tile: the workgroup meets once more for that, halfway through step 2.
+        // Two workgroups share a compute unit in tiles of four waves: there the one that multiplies
+        // goes first (512 x 11,008 x 4,096 68 us without, 63 with; 256 x 256 tiles 1 to 3 % slower with).
+        constexpr bool kPriority = C::kWaves == 4;
         constexpr int kHalf = kProducts / 2, kEarly = C::kPer / 2;
 #pragma unroll
         for (int ks = 0; ks < 2; ++ks) {
           read(kt, ks + 1);
+          if (kPriority) __builtin_amdgcn_s_setprio(1);
           multiply(ks);
+          if (kPriority) __builtin_amdgcn_s_setprio(0);
         }
         read(kt, 3);
         const Source from = source(kt + S);
+        if (kPriority) __builtin_amdgcn_s_setprio(1);
 #pragma unroll
         for (int q = 0; q < kHalf; ++q)
           acc[q / NT][q % NT] = product(fa[0][q / NT], fb[0][q % NT], acc[q / NT][q % NT]);
         __builtin_amdgcn_sched_barrier(0);
+        if (kPriority) __builtin_amdgcn_s_setprio(0);
         wait_lds();
         __builtin_amdgcn_s_barrier();
         constexpr int kRest = kProducts - kHalf, kEach1 = (kEarly + kRest - 1) / kRest;

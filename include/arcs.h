@@ -582,7 +582,8 @@ typedef enum arcs_activation {
  *               256-byte aligned, not read before it is written; calls that share
  *               one must be ordered on one stream; may be NULL when none is needed
  * The same call gives the same bits.  Outputs must not overlap inputs (but for
- * the residual) or each other.  Rows of hidden and weight that are not on the
+ * the residual, where that is not the hidden states) or each other
+ * (ARCS_ERR_OVERLAP).  Rows of hidden and weight that are not on the
  * 16-byte grid (pointer, stride and D; strides of 2^23 bytes or more count as such)
  * are copied to the workspace first, unless N is at most 16.
  * Returns ARCS_OK or a negative arcs_status (nothing launched then);

@@ -19,7 +19,7 @@ def arcs():
 BF16, F32 = 0, 1
 NULL, BATCH, VOCAB, STRIDE, DTYPE, SMALL, MISALIGNED, HISTORY, HIDDEN = -1, -2, -3, -4, -5, -6, -8, -9, -15
 ACT, BIAS, MASK, OVERLAP, NORM, PLAN = -17, -18, -19, -20, -21, -22
-_buf = (ctypes.c_uint8 * 65536)()
+_buf = (ctypes.c_uint8 * 131072)()
 BASE = (ctypes.addressof(_buf) + 255) // 256 * 256
 
 
@@ -75,6 +75,11 @@ def backward(arcs, change):
     (dict(out=None), NULL), (dict(odt=7), DTYPE), (dict(os=99), STRIDE), (dict(rs=99), STRIDE), (dict(b=1), MISALIGNED), (dict(r=1), MISALIGNED),
     (dict(pre=1), MISALIGNED), (dict(out=1), MISALIGNED), (dict(odt=F32, out=2), MISALIGNED), (dict(N=2**21, V=2**20, os=2**20, rs=2**20), BATCH),
     (dict(out=0, r=0, odt=F32), OVERLAP), (dict(out=0, r=0, rs=101), OVERLAP),
+    # in place of the hidden states, whose rows other workgroups still read
+    (dict(V=64, rs=64, os=64, out=0, r=0, h=0, w=32768, b=None, pre=None), OVERLAP),
+    (dict(out=8192, r=None, h=0, w=9008, b=None, pre=None), OVERLAP), (dict(out=16384, r=None, h=0, w=32768, b=24000, pre=None), OVERLAP),
+    (dict(out=16384, r=None, h=0, w=32768, b=None, pre=20000), OVERLAP), (dict(out=16384, r=40000, h=0, w=32768, b=None, pre=44000), OVERLAP),
+    (dict(out=16384, r=None, h=0, w=32768, b=None, pre=4000), OVERLAP),
 ])
 def test_linear(arcs, change, status):
     assert linear(arcs, change) == status
@@ -84,6 +89,9 @@ def test_linear(arcs, change, status):
     (dict(g=None), NULL), (dict(dh=None, dw=None, db=None), NULL), (dict(act=4, pre=None), NULL), (dict(gdt=2), DTYPE), (dict(gs=99), STRIDE),
     (dict(g=1), MISALIGNED), (dict(gdt=F32, g=2), MISALIGNED), (dict(pre=1), MISALIGNED), (dict(dh=1), MISALIGNED), (dict(dw=1), MISALIGNED),
     (dict(db=1), MISALIGNED), (dict(V=2**21 - 7), VOCAB), (dict(more=-1), SMALL), (dict(at=None), NULL), (dict(at=64), MISALIGNED),
+    (dict(dh=0, dw=None, db=None), OVERLAP), (dict(dh=None, dw=12000, db=None, h=30000, w=0, pre=None, g=20000), OVERLAP),
+    (dict(dh=40000, dw=44000, db=None, h=30000, w=0, pre=None, g=20000), OVERLAP),
+    (dict(dh=None, dw=None, db=21000, h=30000, w=0, pre=None, g=20000), OVERLAP),
 ])
 def test_linear_backward(arcs, change, status):
     assert backward(arcs, change) == status
