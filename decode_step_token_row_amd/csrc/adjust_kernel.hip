@@ -10,6 +10,14 @@
 // writing them bounds the call; tokens that a mask takes away are not read, and in place only
 // groups of 16 bytes that change are read and written.  The first ids of both lists are asked
 // for before the logits, so that the lists' work is done while the logits come in.
+//
+// 256 rows x 129,280 bfloat16 with 1,024 history ids and 100 biases each, half of the rows
+// masked: 33 us (119 MB, 3.6 TB/s); 59 with an LDS table for counts and one for biases and loads
+// that waited for each other, 42 with one table, 37.5 with the first ids ahead of the logits, 33
+// with the logits kept as they are in memory until the lists are done (52 registers, eight waves a
+// SIMD).  What remains is the chain of a workgroup: offsets, ids and mask, logits, table and
+// barriers, about 5 us, five and a half rounds of it.  37 rows x 50,001 float32 with 20,000 ids: 14 us,
+// most of it the lists.
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 

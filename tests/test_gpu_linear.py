@@ -8,7 +8,8 @@ Tolerances, with u = 2^-24, h = 2^-8 for bfloat16 results and u for float32 ones
   act   no slope of an activation is above 1.13 (gelu's), so e_z comes through at most 1.13 times;
         evaluating it costs at most 8 u |z|: an exponential whose argument x is off by 4 u |x|
         moves z / (1 + e^x) by |z| 4 u |x| e^x / (1 + e^x)^2 <= 1.8 u |z|, three more roundings
-        of the value, and two units for the function itself; the same for erfc and tanh.
+        of the value, and two units each for exp2 and the reciprocal; the rational form of erfc is
+        off by 1.5e-7, which is 1.3 u |z| of z erfc / 2; tanh by 4 u of its argument.
   out   e_y = 1.13 e_z + 8 u |z| + u |y| with the residual's addition, then h (|y| + e_y).
   dz    the slope is at most 1.13 and off by at most 16 u (1 + |z|) (the same functions, a
         few more operations); the product rounds once, and rounding to the type gives h |dz|:
