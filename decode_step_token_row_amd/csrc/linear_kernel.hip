@@ -123,12 +123,13 @@ __global__ __launch_bounds__(kFewWaves * 64) void linear_few_kernel(LinearArgs a
 // instead of 48).  The sums take dz before it is rounded to T; a workgroup's meet in LDS.  dz may be
 // NULL (only dbias is wanted, or grad_out is dz as it is), and so may the sums.
 template <typename T, typename G, int ROWS>
-__global__ __launch_bounds__(256) void linear_dz_kernel(LinearArgs a, T* dz, int64_t ldz, float* sums) {
+__global__ __launch_bounds__(256) void linear_dz_kernel(LinearArgs a, T* dz, int64_t ldz, float* sums, unsigned across) {
   __shared__ __align__(16) float part[8][256];
   const int tid = threadIdx.x, c = (tid & 31) * 8, r = tid >> 5;
-  const int64_t v = (int64_t)blockIdx.x * 256 + c;
+  const unsigned down = blockIdx.x / across;  // more than a grid's y takes
+  const int64_t v0 = (int64_t)(blockIdx.x - down * across) * 256, v = v0 + c;
   const int left = (int)(a.V - v < 8 ? a.V - v : 8);  // <= 0 past V
-  const int64_t n0 = (int64_t)blockIdx.y * (ROWS * 8) + r;
+  const int64_t n0 = (int64_t)down * (ROWS * 8) + r;
   Raw8<G> g[ROWS];
   Raw8<T> z[ROWS];
 #pragma unroll
@@ -160,8 +161,7 @@ __global__ __launch_bounds__(256) void linear_dz_kernel(LinearArgs a, T* dz, int
   float s = 0.0f;
 #pragma unroll
   for (int i = 0; i < 8; ++i) s += part[i][tid];
-  const int64_t at = (int64_t)blockIdx.x * 256 + tid;
-  if (at < a.V) sums[blockIdx.y * a.V + at] = s;
+  if (v0 + tid < a.V) sums[down * a.V + v0 + tid] = s;
 }
 
 // The chunks' sums added up, in an order of their numbers.
@@ -273,9 +273,10 @@ hipError_t forward(LinearArgs a, int dtype, bool aligned, hipStream_t stream) {
 
 template <typename T, typename G>
 void launch_dz(const LinearArgs& a, T* dz, int64_t ldz, float* sums, int64_t chunk_rows, hipStream_t stream) {
-  const dim3 grid((unsigned)tiles(a.V, 256), (unsigned)tiles(a.N, chunk_rows));
-  if (chunk_rows == 8) hipLaunchKernelGGL((linear_dz_kernel<T, G, 1>), grid, dim3(256), 0, stream, a, dz, ldz, sums);
-  else hipLaunchKernelGGL((linear_dz_kernel<T, G, 4>), grid, dim3(256), 0, stream, a, dz, ldz, sums);
+  const unsigned across = (unsigned)tiles(a.V, 256);
+  const dim3 grid((unsigned)(across * tiles(a.N, chunk_rows)));  // below 2^28
+  if (chunk_rows == 8) hipLaunchKernelGGL((linear_dz_kernel<T, G, 1>), grid, dim3(256), 0, stream, a, dz, ldz, sums, across);
+  else hipLaunchKernelGGL((linear_dz_kernel<T, G, 4>), grid, dim3(256), 0, stream, a, dz, ldz, sums, across);
 }
 
 template <typename T>

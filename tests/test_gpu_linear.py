@@ -335,3 +335,23 @@ def test_a_large_call_far_rows(arcs):
     out = arcs.linear(s["hidden"], s["weight"])
     for r in (slice(0, 3), slice(N - 3, N)):
         check_forward(dict(s, hidden=s["hidden"][r]), out[r], None, "none")
+
+
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+def test_more_rows_than_a_grids_second_axis(arcs, dtype):
+    """65,536 workgroups of 32 rows and one more, on whole numbers whose sums float32 holds, so each
+    result is the exact one rounded once."""
+    import torch
+    t = getattr(torch, dtype)
+    N, V, D = 65536 * 32 + 5, 9, 8
+    g = torch.Generator("cuda").manual_seed(9)
+    h = torch.randint(-1, 2, (N, D), generator=g, device="cuda").to(t)
+    w = torch.randint(-2, 3, (V, D), generator=g, device="cuda").to(t)
+    grad = torch.randint(0, 2, (N, V), generator=g, device="cuda").to(t)
+    pre = torch.randint(-1, 2, (N, V), generator=g, device="cuda").to(t)
+    dh, dw, db = arcs.linear_backward(h, w, grad, pre=pre, activation="relu", want_bias=True)
+    dz = torch.where(pre > 0, grad, torch.zeros_like(grad)).float()
+    assert torch.equal(db, dz.double().sum(0).to(t))
+    assert torch.equal(dh, (dz[:, :, None] * w.float()).sum(1).to(t))
+    want = torch.stack([(dz[:, v, None].double() * h.double()).sum(0) for v in range(V)])
+    assert torch.equal(dw, want.to(t))
