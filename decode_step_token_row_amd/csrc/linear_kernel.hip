@@ -340,7 +340,7 @@ hipError_t backward(LinearArgs a, int dtype, bool aligned, hipStream_t stream) {
 // columns, k of 100 .. 11,008), measured in every kind and sharing: what the costs
 // name takes 0.5 % longer in the geometric mean than the best, 25 % at most (of 10 us).  On
 // both sides of the choice, for instance, forward: 4,096 x 4,096 x 4,096 125 us in 256 x 256
-// and 148 in 128 x 128; 512 x 11,008 x 4,096 68 in 128 x 128, 92 in 256 x 256 shared; 256 x
+// and 148 in 128 x 128; 512 x 11,008 x 4,096 63 in 128 x 128, 92 in 256 x 256 shared; 256 x
 // 4,096 x 4,096 23 in 64 x 64, 26 in 128 x 128 shared.  (256 x 128, 256 x 64 and 128 x 64 in
 // bfloat16, other depths of k and four waves of 128 x 128 each gained less than 1 % somewhere.)
 struct TileCost {
