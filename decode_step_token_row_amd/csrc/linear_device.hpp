@@ -18,12 +18,46 @@ constexpr float kLog2E = 1.44269504088896340736f;
 constexpr float kGeluA = 0.79788456080286535588f;  // sqrt(2 / pi)
 constexpr float kGeluB = 0.044715f;
 
-// exp2 and the reciprocal of the vector unit are off by one unit in the last place; an
-// exponential's argument x is rounded, so exp(x) is off by |x| 2^-24 more, which the uses
-// below multiply by something that falls as fast.  (The library's expf and division made dz
-// three times as long as its way through memory.)
+// exp2 and the reciprocal of the vector unit are off by one unit in the last place.  (The
+// library's expf and division made dz three times as long as its way through memory.)
 __device__ __forceinline__ float exp_fast(float x) { return __builtin_amdgcn_exp2f(x * kLog2E); }
 __device__ __forceinline__ float rcp_fast(float x) { return __builtin_amdgcn_rcpf(x); }
+
+// exp(-c (x + dx)) for x >= 0, `high` and `low` being c log2 e in two parts: what the argument's rounding
+// leaves, which would be x 2^-24 of the result, is applied to it as a factor.  (4,096 x 4,096
+// bfloat16, dz without it and without half powers 17.6 us with silu and 19.4 with gelu by tanh, 19.7 and
+// 23.2 with both; the forward product of 4,096 columns of k 135 and 125, 139 and 128.)
+__device__ __forceinline__ float exp2_minus(float t, float rest) {
+  const float y = __builtin_amdgcn_exp2f(-t);
+  return fmaf(y * -0.69314718055994530942f, rest, y);
+}
+__device__ __forceinline__ float exp_minus(float x, float high, float low) {
+  const float t = x * high;
+  return exp2_minus(t, fmaf(x, low, fmaf(x, high, -t)));
+}
+__device__ __forceinline__ float exp_minus(float x, float dx, float high, float low) {
+  const float t = x * high;
+  return exp2_minus(t, fmaf(dx, high, fmaf(x, low, fmaf(x, high, -t))));
+}
+// A constant's float32 value and what that leaves.
+constexpr float high_part(double c) { return (float)c; }
+constexpr float low_part(double c) { return (float)(c - (double)(float)c); }
+
+// exp(-a / 2), 0 past 256.
+__device__ __forceinline__ float half_power(float a) {
+  constexpr double kC = 0.5 * 1.4426950408889634;
+  return exp_minus(__builtin_fminf(a, 256.0f), high_part(kC), low_part(kC));
+}
+// exp(-u), u = sqrt(2 / pi) (a + 0.044715 a^3), 0 past 16; u in two parts, each step with what it leaves.
+__device__ __forceinline__ float half_power_tanh(float a) {
+  constexpr double kB = 0.044715, kC = 0.79788456080286535588 * 1.4426950408889634;
+  a = __builtin_fminf(a, 16.0f);
+  const float aa = a * a, aa_left = fmaf(a, a, -aa);
+  const float s = fmaf(aa, high_part(kB), 1.0f);  // 1 - s is exact, s being at least 1
+  const float s_left = fmaf(aa_left, high_part(kB), fmaf(aa, low_part(kB), fmaf(aa, high_part(kB), 1.0f - s)));
+  const float u = a * s, u_left = fmaf(a, s_left, fmaf(a, s, -u));
+  return exp_minus(u, u_left, high_part(kC), low_part(kC));
+}
 
 // The normal distribution function's smaller tail, Phi(-a) = H exp(-a^2 / 2), a = |z|, as H and
 // h = exp(-a^2 / 4): H falls as slowly as 1 / a, and h is applied twice, so that z h H h keeps its digits
@@ -33,12 +67,9 @@ __device__ __forceinline__ float rcp_fast(float x) { return __builtin_amdgcn_rcp
 // rounding alone would be 2^-24 a^2 / 4 of h.  Past 32 all of it is 0.
 __device__ __forceinline__ float normal_tail(float a, float& h) {
   constexpr double kC = 0.25 * 1.4426950408889634;
-  constexpr float kHigh = (float)kC, kLow = (float)(kC - (double)kHigh);
   a = __builtin_fminf(a, 32.0f);
-  const float aa = a * a, left = fmaf(a, a, -aa), x = aa * kHigh;
-  const float dx = fmaf(left, kHigh, fmaf(aa, kLow, fmaf(aa, kHigh, -x)));
-  const float y = __builtin_amdgcn_exp2f(-x);
-  h = fmaf(y * -0.69314718055994530942f, dx, y);
+  const float aa = a * a;
+  h = exp_minus(aa, fmaf(a, a, -aa), high_part(kC), low_part(kC));
   const float t = rcp_fast(fmaf(0.36f, a, 1.0f));
   float s = fmaf(t, -0.030238168f, 0.13950802f);
   s = fmaf(t, s, -0.22359903f);
@@ -64,7 +95,13 @@ __device__ __forceinline__ float tanh_fast(float u) {
   return fabsf(u) < 0.25f ? s : far;
 }
 
-// act(z) in binary32.  (1 + tanh u) / 2 = 1 / (1 + exp(-2 u)) keeps its digits where it is near 0.
+// z / (1 + exp(-x)), where h = exp(-|x| / 2) and x has the sign of z.  Below 0 that is z h^2 / (1 + h^2),
+// which keeps its digits as long as it is a normal number itself.
+__device__ __forceinline__ float gated(float z, float h) {
+  return (z >= 0.0f ? z : z * h * h) * rcp_fast(fmaf(h, h, 1.0f));
+}
+
+// act(z) in binary32, within 20 2^-24 of itself.  (1 + tanh u) / 2 = 1 / (1 + exp(-2 u)).
 template <int ACT>
 __device__ __forceinline__ float act_value(float z, float cap, float inv_cap) {
   switch (ACT) {
@@ -74,8 +111,8 @@ __device__ __forceinline__ float act_value(float z, float cap, float inv_cap) {
       const float tail = normal_tail(fabsf(z), h);
       return z < 0.0f ? z * h * tail * h : z * (1.0f - tail * h * h);
     }
-    case ARCS_ACT_GELU_TANH: return z * rcp_fast(1.0f + exp_fast(-2.0f * kGeluA * fmaf(kGeluB * z * z, z, z)));
-    case ARCS_ACT_SILU: return z * rcp_fast(1.0f + exp_fast(-z));
+    case ARCS_ACT_GELU_TANH: return gated(z, half_power_tanh(fabsf(z)));
+    case ARCS_ACT_SILU: return gated(z, half_power(fabsf(z)));
     case ARCS_ACT_SOFTCAP: return cap * tanh_fast(z * inv_cap);
     default: return z;
   }
@@ -95,18 +132,17 @@ __device__ __forceinline__ float act_slope(float z, float inv_cap) {
       return z != z ? z : z < 0.0f ? e * (tail - rest) : fmaf(e, rest - tail, 1.0f);
     }
     case ARCS_ACT_GELU_TANH: {
-      const float zz = z * z, u = kGeluA * fmaf(kGeluB * zz, z, z);
-      const float e = exp_fast(-2.0f * fabsf(u)), d = rcp_fast(1.0f + e), ed = e * d;
-      // half = (1 + tanh u) / 2; e is 0 where the rest may be infinite
-      const float half = u >= 0.0f ? d : ed;
-      const float rest = e > 0.0f ? 2.0f * kGeluA * z * ed * d * fmaf(3.0f * kGeluB, zz, 1.0f) : 0.0f;
-      return z != z ? z : half + rest;
+      // half + rest, half = (1 + tanh u) / 2
+      const float a = __builtin_fminf(fabsf(z), 16.0f), h = half_power_tanh(a);
+      const float e = h * h, d = rcp_fast(1.0f + e), ed = e * d;
+      const float rest = 2.0f * kGeluA * a * ed * d * fmaf(3.0f * kGeluB, a * a, 1.0f);
+      return z != z ? z : z >= 0.0f ? d + rest : ed - rest;
     }
     case ARCS_ACT_SILU: {
-      const float e = exp_fast(-fabsf(z)), d = rcp_fast(1.0f + e), ed = e * d;
-      const float s = z >= 0.0f ? d : ed;
-      // z s (1 - s), 0 in the limit
-      return z != z ? z : s + (e > 0.0f ? z * ed * d : 0.0f);
+      // s + z s (1 - s), s = 1 / (1 + exp(-z))
+      const float a = __builtin_fminf(fabsf(z), 256.0f), h = half_power(a);
+      const float e = h * h, d = rcp_fast(1.0f + e), ed = e * d, rest = a * ed * d;
+      return z != z ? z : z >= 0.0f ? d + rest : ed - rest;
     }
     case ARCS_ACT_SOFTCAP: {
       const float e = exp_fast(-2.0f * fabsf(z * inv_cap)), d = rcp_fast(1.0f + e);

@@ -7,6 +7,8 @@ rounds once:
         in float32 where the fused steps round once), 2 more for the reciprocal in its argument: 8.3 u.
   value z < 0: h twice (6), tail (8.3), three products: 17.3; z >= 0: 1 - tail h^2, where what is taken away is
         at most half of 1 and off by 16.3, and two roundings: 18.3 (tail h^2 is at most what remains).
+        z (h^2) / (1 + h^2): h twice (6), three for its denominator with the exponential's error in it at half,
+        2 for the reciprocal, three products: 14.5.
   slope two terms, each of at most two exponentials h, a tail or two reciprocals, and ten roundings:
         6 + 8.3 + 10 of each of the two.
 So values are within 20 u of themselves, and slopes within 32 u of the sum of their terms' sizes.
@@ -39,7 +41,11 @@ def exact(act, z):
     if act == "gelu":
         phi = np.vectorize(math.erfc)(z / -math.sqrt(2)) / 2
         return z * phi, phi, z * np.exp(-z * z / 2) / math.sqrt(2 * math.pi)
-    raise KeyError(act)
+    twice = z if act == "silu" else 2 * math.sqrt(2 / math.pi) * (z + 0.044715 * z ** 3)
+    slope = 1.0 if act == "silu" else 2 * math.sqrt(2 / math.pi) * (1 + 3 * 0.044715 * z * z)
+    small = np.exp(-np.abs(twice))
+    half = np.where(z >= 0, 1.0, small) / (1 + small)
+    return z * half, half, z * slope * small / (1 + small) ** 2
 
 
 def points():
@@ -49,7 +55,7 @@ def points():
     return np.concatenate([a, -a]).astype(np.float32)
 
 
-ACTS = ["gelu"]
+ACTS = ["gelu", "gelu_tanh", "silu"]
 
 
 @pytest.mark.parametrize("rows", [1, 9, 20])
