@@ -20,6 +20,7 @@ constexpr float kGeluB = 0.044715f;
 
 // exp2 and the reciprocal of the vector unit are off by one unit in the last place.  (The
 // library's expf and division made dz three times as long as its way through memory.)
+// exp_fast's argument is rounded, which is |x| 2^-23 of the result: for what falls as fast.
 __device__ __forceinline__ float exp_fast(float x) { return __builtin_amdgcn_exp2f(x * kLog2E); }
 __device__ __forceinline__ float rcp_fast(float x) { return __builtin_amdgcn_rcpf(x); }
 
@@ -82,16 +83,17 @@ __device__ __forceinline__ float normal_tail(float a, float& h) {
   return s * t;
 }
 
-// tanh u: its series to u^9 up to 1/4 (the next term is 8e-9 of it), above that (1 - e) / (1 + e)
-// with e = exp(-2 |u|).
-__device__ __forceinline__ float tanh_fast(float u) {
-  const float w = u * u;
+// c tanh u, u = z / c.  Up to |u| = 1/4 by the series of tanh u to u^9 (the next term is 8e-9 of it), as
+// z + z (tanh u / u - 1), so that z whose u is too small for a number of its own stay what they are; above that
+// c (1 - e) / (1 + e) with e = exp(-2 |u|).
+__device__ __forceinline__ float softcap(float z, float c, float inv_c) {
+  const float u = z * inv_c, w = u * u;
   float s = fmaf(w, 62.0f / 2835.0f, -17.0f / 315.0f);
   s = fmaf(w, s, 2.0f / 15.0f);
   s = fmaf(w, s, -1.0f / 3.0f);
-  s = fmaf(w * s, u, u);
+  s = fmaf(w * s, z, z);
   const float e = exp_fast(-2.0f * fabsf(u));
-  const float far = __builtin_copysignf((1.0f - e) * rcp_fast(1.0f + e), u);
+  const float far = c * __builtin_copysignf((1.0f - e) * rcp_fast(1.0f + e), u);
   return fabsf(u) < 0.25f ? s : far;
 }
 
@@ -113,7 +115,7 @@ __device__ __forceinline__ float act_value(float z, float cap, float inv_cap) {
     }
     case ARCS_ACT_GELU_TANH: return gated(z, half_power_tanh(fabsf(z)));
     case ARCS_ACT_SILU: return gated(z, half_power(fabsf(z)));
-    case ARCS_ACT_SOFTCAP: return cap * tanh_fast(z * inv_cap);
+    case ARCS_ACT_SOFTCAP: return softcap(z, cap, inv_cap);
     default: return z;
   }
 }

@@ -566,8 +566,8 @@ typedef enum arcs_activation {
  * draft head's hidden + silu(weight hidden + bias).  Per row n:
  *   z = hidden[n] weight^T + bias,   out[n] = residual[n] + act(z).
  * Products, sums and the activation are held in binary32 and each result is
- * rounded once to its type: act(z) is within 20 2^-24 of itself for gelu and silu
- * where it is a normal number.  NaN and infinities propagate.
+ * rounded once to its type: act(z) is within 20 2^-24 of itself where it is a
+ * normal number.  NaN and infinities propagate.
  *   hidden      device [N, hidden_stride] of dtype (ARCS_DTYPE_BF16 or
  *               ARCS_DTYPE_F32), hidden_stride >= D, D in 1 .. ARCS_MAX_HIDDEN
  *   weight      device [V, weight_stride] of dtype, weight_stride >= D

@@ -9,6 +9,8 @@ rounds once:
         at most half of 1 and off by 16.3, and two roundings: 18.3 (tail h^2 is at most what remains).
         z (h^2) / (1 + h^2): h twice (6), three for its denominator with the exponential's error in it at half,
         2 for the reciprocal, three products: 14.5.
+        softcap, u = z / c: its two roundings and the two of the exponential's argument reach tanh u at most
+        once, as 4, 2 for exp2, two sums, the reciprocal (2) and two products: 12; below 1/4 less.
   slope two terms, each of at most two exponentials h, a tail or two reciprocals, and ten roundings:
         6 + 8.3 + 10 of each of the two.
 So values are within 20 u of themselves, and slopes within 32 u of the sum of their terms' sizes.
@@ -74,6 +76,23 @@ def test_values(arcs, act, rows):
     for row in (out[0], out[-1]):
         far = np.abs(row.cpu().numpy().astype(np.float64) - want) - 20 * U * np.abs(want) - 2.0 ** -147
         assert far.max() <= 0, (float(z[far.argmax()]), float(row[far.argmax()]), want[far.argmax()])
+
+
+@pytest.mark.parametrize("rows", [1, 20])
+@pytest.mark.parametrize("cap", [2.0 ** -100, 1e-3, 1.5, 30.0, 1e10, 2.0 ** 100])
+def test_softcap(arcs, cap, rows):
+    """From pre-activations whose z / c float32 does not hold to those far beyond c."""
+    import torch
+    z = points()
+    w = torch.zeros(len(z), 4, device="cuda")
+    w[:, 0] = torch.from_numpy(z)
+    h = torch.zeros(rows, 4, device="cuda")
+    h[:, 0] = 1.0
+    got = arcs.linear(h, w, activation="softcap", softcap=cap)[-1].cpu().numpy().astype(np.float64)
+    c = float(np.float32(cap))
+    want = c * np.tanh(z.astype(np.float64) / c)
+    far = np.abs(got - want) - 20 * U * np.abs(want) - 2.0 ** -147
+    assert far.max() <= 0, (float(z[far.argmax()]), got[far.argmax()], want[far.argmax()])
 
 
 @pytest.mark.parametrize("act", ACTS)
