@@ -947,7 +947,7 @@ def adjust_logits(logits, params=None, hist_ids=None, hist_offsets=None, bias_id
             _vector(out_status, "out_status", torch.int32, B, dev)
         st = library().arcs_adjust_logits(_ptr(logits), dt, B, V, stride, _ptr(params), _list_ptr(hist_ids),
                                           _ptr(hist_offsets), _list_ptr(bias_ids), _list_ptr(bias_values),
-                                          _ptr(bias_offsets), _ptr(mask), masks, mask_stride, _ptr(mask_rows),
+                                          _ptr(bias_offsets), _list_ptr(mask), masks, mask_stride, _ptr(mask_rows),
                                           _ptr(out), odt, os_, _ptr(out_status), _head_stream(stream, dev))
     if st != OK:
         raise ArcsError(st, "arcs_adjust_logits")

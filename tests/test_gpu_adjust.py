@@ -267,6 +267,15 @@ def test_masked_rows_sample_allowed_tokens_only(arcs):
             assert int(st[b]) == arcs.ROW_NOTHING_ALLOWED and not c["bits"][b].any()
 
 
+def test_a_mask_without_rows_is_refused(arcs):
+    """torch has no address for it, and it is not the same as no mask."""
+    import torch
+    x = torch.zeros(2, 64, device="cuda")
+    for rows in (None, torch.full((2,), -1, dtype=torch.int32, device="cuda")):
+        with pytest.raises(arcs.ArcsError):
+            arcs.adjust_logits(x, mask=torch.empty(0, 2, dtype=torch.int32, device="cuda"), mask_rows=rows)
+
+
 def test_side_stream_and_replays(arcs):
     import torch
     c = make(9, 7000, "bf16", 9, 200, 50, 4)
