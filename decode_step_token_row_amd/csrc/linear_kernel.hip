@@ -185,15 +185,17 @@ __global__ __launch_bounds__(256) void linear_dbias_kernel(const float* sums, in
 
 // Rows of `columns` elements to rows of ld, zeros behind them.
 template <typename T>
-__global__ __launch_bounds__(256) void linear_pack_kernel(const T* from, int64_t stride, int64_t columns, T* to, int64_t ld) {
+__global__ __launch_bounds__(256) void linear_pack_kernel(const T* from, int64_t stride, int64_t rows, int64_t columns, T* to,
+                                                          int64_t ld) {
   constexpr int kEach = 16 / sizeof(T);
-  const int64_t row = blockIdx.x;
-  const T* p = from + row * stride;
-  for (int64_t c = threadIdx.x * kEach; c < ld; c += 256 * kEach) {
-    const int64_t left = columns - c;
-    float v[kEach];
-    load_some<T, kEach>(p + c, (int)(left < kEach ? left > 0 ? left : 0 : kEach), v);
-    store_some<T, kEach>(to + row * ld + c, kEach, v);
+  for (int64_t row = blockIdx.x; row < rows; row += gridDim.x) {
+    const T* p = from + row * stride;
+    for (int64_t c = threadIdx.x * kEach; c < ld; c += 256 * kEach) {
+      const int64_t left = columns - c;
+      float v[kEach];
+      load_some<T, kEach>(p + c, (int)(left < kEach ? left > 0 ? left : 0 : kEach), v);
+      store_some<T, kEach>(to + row * ld + c, kEach, v);
+    }
   }
 }
 
@@ -215,8 +217,10 @@ size_t slab_bytes(int mode, int64_t M, int64_t N, int64_t K, bool bf16) {
 
 template <typename T>
 void pack(const void*& rows, int64_t& stride, int64_t count, int64_t columns, char* to, int64_t ld, hipStream_t stream) {
-  hipLaunchKernelGGL(linear_pack_kernel<T>, dim3((unsigned)count), dim3(256), 0, stream, (const T*)rows, stride, columns,
-                     (T*)to, ld);
+  // a launch holds fewer than 2^32 threads, the head's 2^24 rows have as many
+  const int64_t blocks = count < (int64_t(1) << 20) ? count : int64_t(1) << 20;
+  hipLaunchKernelGGL(linear_pack_kernel<T>, dim3((unsigned)blocks), dim3(256), 0, stream, (const T*)rows, stride, count,
+                     columns, (T*)to, ld);
   rows = to;
   stride = ld;
 }
@@ -274,7 +278,8 @@ hipError_t forward(LinearArgs a, int dtype, bool aligned, hipStream_t stream) {
 template <typename T, typename G>
 void launch_dz(const LinearArgs& a, T* dz, int64_t ldz, float* sums, int64_t chunk_rows, hipStream_t stream) {
   const unsigned across = (unsigned)tiles(a.V, 256);
-  const dim3 grid((unsigned)(across * tiles(a.N, chunk_rows)));  // below 2^28
+  // below 2^24 workgroups, whose threads a launch holds: as many would be for 2^37 elements of grad_out and dz each
+  const dim3 grid((unsigned)(across * tiles(a.N, chunk_rows)));
   if (chunk_rows == 8) hipLaunchKernelGGL((linear_dz_kernel<T, G, 1>), grid, dim3(256), 0, stream, a, dz, ldz, sums, across);
   else hipLaunchKernelGGL((linear_dz_kernel<T, G, 4>), grid, dim3(256), 0, stream, a, dz, ldz, sums, across);
 }

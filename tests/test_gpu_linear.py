@@ -355,3 +355,19 @@ def test_more_rows_than_a_grids_second_axis(arcs, dtype):
     assert torch.equal(dh, (dz[:, :, None] * w.float()).sum(1).to(t))
     want = torch.stack([(dz[:, v, None].double() * h.double()).sum(0) for v in range(V)])
     assert torch.equal(dw, want.to(t))
+
+
+@pytest.mark.parametrize("D", [8, 9])
+@pytest.mark.parametrize("N", [16, 17])
+def test_the_largest_vocabulary(arcs, N, D):
+    """2^24 columns, whose rows off the 16-byte grid are more than a launch has workgroups of 256
+    threads for; whole numbers, so each result is exact."""
+    import torch
+    V = 2 ** 24
+    g = torch.Generator("cuda").manual_seed(D)
+    h = torch.randint(-2, 3, (N, D), generator=g, device="cuda").to(torch.bfloat16)
+    w = torch.randint(-3, 4, (V, D), generator=g, device="cuda", dtype=torch.int8).to(torch.bfloat16)
+    out = arcs.linear(h, w)
+    for at in range(0, V, V // 8):
+        want = sum(h[:, None, d].float() * w[None, at: at + V // 8, d].float() for d in range(D))
+        assert torch.equal(out[:, at: at + V // 8].float(), want)
