@@ -335,15 +335,36 @@ hipError_t launch_adjust(AdjustArgs a, int dtype, int out_dtype, int64_t B, hipS
   a.slices = (int)((a.V + kAdjustSlice - 1) / kAdjustSlice);
   // one workgroup more a row looks the mask through where the status is wanted
   a.per_row = a.slices + (a.out_status != nullptr && a.mask != nullptr ? 1 : 0);
-  const unsigned blocks = (unsigned)(B * a.per_row);
-  if (dtype == ARCS_DTYPE_BF16) {
-    if (out_dtype == ARCS_DTYPE_BF16) launch<__bf16, __bf16>(a, blocks, stream);
-    else launch<__bf16, float>(a, blocks, stream);
-  } else {
-    if (out_dtype == ARCS_DTYPE_BF16) launch<float, __bf16>(a, blocks, stream);
-    else launch<float, float>(a, blocks, stream);
+  // A launch holds fewer than 2^32 threads: more rows take several.
+  const int64_t most = ((int64_t(1) << 24) - 1) / a.per_row, element = dtype == ARCS_DTYPE_BF16 ? 2 : 4;
+  const int64_t out_element = out_dtype == ARCS_DTYPE_BF16 ? 2 : 4;
+  for (int64_t b = 0; b < B; b += most) {
+    const int64_t rows = B - b < most ? B - b : most;
+    const unsigned blocks = (unsigned)(rows * a.per_row);
+    if (dtype == ARCS_DTYPE_BF16) {
+      if (out_dtype == ARCS_DTYPE_BF16) launch<__bf16, __bf16>(a, blocks, stream);
+      else launch<__bf16, float>(a, blocks, stream);
+    } else {
+      if (out_dtype == ARCS_DTYPE_BF16) launch<float, __bf16>(a, blocks, stream);
+      else launch<float, float>(a, blocks, stream);
+    }
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    // the next rows' parts of what is listed by rows
+    a.logits = (const char*)a.logits + rows * a.stride * element;
+    a.out = (char*)a.out + rows * a.out_stride * out_element;
+    if (a.params != nullptr) a.params += rows;
+    if (a.hist_offsets != nullptr) a.hist_offsets += rows;
+    if (a.bias_offsets != nullptr) a.bias_offsets += rows;
+    if (a.mask_rows != nullptr) {
+      a.mask_rows += rows;
+    } else if (a.mask != nullptr) {
+      a.mask += rows * a.mask_stride;
+      a.masks -= rows;
+    }
+    if (a.out_status != nullptr) a.out_status += rows;
   }
-  return hipGetLastError();
+  return hipSuccess;
 }
 
 }  // namespace arcs

@@ -309,3 +309,23 @@ def test_rows_past_32_bits(arcs):
     ids = torch.tensor([V - 1, 3], dtype=torch.int32, device="cuda")
     arcs.adjust_logits(x, bias_ids=ids, bias_values=torch.tensor([2.0, 1.0], device="cuda"), bias_offsets=n, out=x)
     assert float(x[-1, -1]) == 2.0 and float(x[-1, 3]) == 1.0 and float(x[-1].sum()) == 3.0 and not x[:-1].any()
+
+
+@pytest.mark.parametrize("own_masks", [False, True])
+def test_more_rows_than_one_launch_takes(arcs, own_masks):
+    """2^24 rows of 20 tokens, in place and with another type: each has a bias for one token, and a mask (two by
+    number, or its own) that takes another."""
+    import torch
+    B, V = 2 ** 24 + 3, 20
+    row = torch.arange(B, device="cuda")
+    x = (row % 128)[:, None].to(torch.bfloat16).expand(B, V).contiguous()
+    masks = torch.tensor([~1, ~2], dtype=torch.int32, device="cuda")[:, None]  # without token 0, without token 1
+    c = dict(bias_ids=(row % V).to(torch.int32), bias_values=(row % 64).float(), bias_offsets=torch.arange(B + 1, device="cuda"))
+    c.update(dict(mask=masks[row % 2].contiguous()) if own_masks else dict(mask=masks.contiguous(), mask_rows=(row % 2).to(torch.int32)))
+    want = x.clone()
+    want[row, row % V] += (row % 64).to(torch.bfloat16)
+    want[row, row % 2] = float("-inf")
+    st = torch.full((B,), 99, dtype=torch.int32, device="cuda")
+    assert torch.equal(arcs.adjust_logits(x, out_dtype=torch.float32, out_status=st, **c), want.float()) and not st.any()
+    arcs.adjust_logits(x, out=x, **c)
+    assert torch.equal(x, want)
