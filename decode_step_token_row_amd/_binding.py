@@ -966,7 +966,8 @@ class TensorList:
 
     ``tensors`` bfloat16 or float32, contiguous, on one device, of any shape; ``outs`` a
     tensor of as many elements for each, where clip_gradients writes, or None: in place.  The
-    list keeps the tensors alive.  Memory that overlaps (the same tensor twice, say) is refused.
+    list keeps the tensors alive, and its plan: a captured graph that holds a call needs the list
+    as long as it is replayed.  Memory that overlaps (the same tensor twice, say) is refused.
     """
 
     def __init__(self, tensors, outs=None):
@@ -998,6 +999,7 @@ class TensorList:
         if st != OK:
             raise ArcsError(st, "arcs_gradient_plan")
         self.plan = torch.from_numpy(plan).to(self.device)
+        self.plan_stream = _head_stream(None, self.device)  # whose memory it is
         self.plan_bytes = size
         self.workspace_bytes = int(library().arcs_gradient_workspace_bytes(size))
 
@@ -1031,12 +1033,16 @@ def _norm_call(tensors, out_norm, workspace, stream, name, *more):
         else:
             _vector(out_norm, "out_norm", torch.float32, 1, dev)
         workspace, ws_bytes = _head_workspace(workspace, tensors.workspace_bytes, dev)
+        on = _head_stream(stream, dev)
         st = getattr(library(), name)(_list_ptr(tensors.plan), tensors.plan_bytes, *more, _ptr(out_norm),
-                                      _ptr(workspace), ws_bytes, _head_stream(stream, dev))
+                                      _ptr(workspace), ws_bytes, on)
     if st != OK:
         raise ArcsError(st, name)
     if stream is not None:
         _head_used(stream, dev, (tensors.plan, workspace, *tensors.tensors), (out_norm, *tensors.outs))
+    elif on != tensors.plan_stream:
+        # the plan is the list's own: a list dropped right after the call must not give it back yet
+        _used_on(torch.cuda.current_stream(dev), tensors.plan)
     return out_norm
 
 

@@ -217,3 +217,24 @@ def test_views_and_broadcasts(arcs):
         arcs.adjust_logits(want, mask=torch.zeros(30, 1, dtype=torch.int32, device="cuda"))
     with pytest.raises((ValueError, arcs.ArcsError)):
         arcs.adjust_logits(want, mask=torch.zeros(29, 2, dtype=torch.int32, device="cuda"))
+
+
+def test_a_list_dropped_after_a_call_on_another_current_stream(arcs):
+    """The list's plan belongs to the stream that it was made on; a call on another current stream
+    keeps it until that stream is through.  (Nothing is written to the memory that is asked for.)"""
+    import torch
+    x = torch.ones(1_000_000, device="cuda")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    plans = arcs.TensorList([x])
+    at, size = plans.plan.data_ptr(), plans.plan_bytes
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(BUSY)
+        norm = arcs.clip_gradients(plans, 10.0)
+    del plans
+    others = [torch.empty(size, dtype=torch.uint8, device="cuda") for _ in range(8)]
+    busy = not side.query()
+    taken = at in [t.data_ptr() for t in others]
+    side.synchronize()
+    assert busy and not taken
+    assert float(norm) == 1000.0 and float(x[0]) == float(x[-1]) == float(torch.tensor(0.01))
