@@ -670,7 +670,7 @@ int arcs_adjust_logits(const void* logits, int dtype, int64_t B, int64_t V, int6
 typedef struct arcs_tensor {
   const void* data;  /* device, aligned to its element; may be NULL when count is 0 */
   void* out;         /* where arcs_clip_gradients writes: `data` (in place, of the same type)
-                        or memory that overlaps no tensor; NULL: arcs_gradient_norm only */
+                        or memory that overlaps no tensor; NULL: it writes nothing for this one */
   int64_t count;     /* >= 0 */
   int32_t dtype;
   int32_t out_dtype;
@@ -706,8 +706,10 @@ int arcs_gradient_norm(const void* plan, size_t plan_bytes, float* out_norm, voi
  * finite, every element times max_norm / norm (taken in binary64, rounded to
  * binary32 and then to its output's type).  Otherwise the elements keep their
  * values: tensors in place are not touched, others are copied to their outputs.
+ * The norm is compared and divided by in binary64: gradients whose norm is past
+ * binary32's range are scaled too, and out_norm[0] is infinity then.
  *   max_norm    >= 0 (ARCS_ERR_BAD_NORM for NaN and negative values)
- * Every tensor of the plan needs its `out`.
+ * Tensors of the plan without an `out` count in the norm and are not written.
  */
 int arcs_clip_gradients(const void* plan, size_t plan_bytes, double max_norm, float* out_norm, void* workspace,
                         size_t workspace_bytes, void* stream);

@@ -224,3 +224,27 @@ def test_a_training_step_of_a_block_in_front_of_the_head(arcs):
     check_norm(arcs.clip_gradients(arcs.TensorList(before, outs=outs), total / 2), total)
     for a, t in zip(outs, before):
         check_scaled(a, t, 0.5)
+
+
+def test_tensors_without_an_out_count_and_are_not_written(arcs):
+    """A plan of the C interface whose first and last tensors have no `out`."""
+    import torch
+    a, b, c = (torch.full((n,), v, device="cuda") for n, v in ((9000, 2.0), (5000, 3.0), (7, 100.0)))
+    records = np.zeros(3, arcs.TENSOR_DTYPE)
+    records["data"] = [t.data_ptr() for t in (a, b, c)]
+    records["out"] = [0, b.data_ptr(), 0]
+    records["count"] = [t.numel() for t in (a, b, c)]
+    records["dtype"] = records["out_dtype"] = arcs.DTYPE_F32
+    lib = arcs.library()
+    size = lib.arcs_gradient_plan_bytes(records.ctypes.data, 3)
+    host = np.zeros(size, np.uint8)
+    assert lib.arcs_gradient_plan(records.ctypes.data, 3, host.ctypes.data, size) == 0
+    plan, norm = torch.from_numpy(host).cuda(), torch.empty(1, device="cuda")
+    need = lib.arcs_gradient_workspace_bytes(size)
+    work = torch.empty(need, dtype=torch.uint8, device="cuda")
+    want = float(np.sqrt(9000 * 4.0 + 5000 * 9.0 + 7 * 1e4))
+    stream = torch.cuda.current_stream().cuda_stream
+    assert lib.arcs_clip_gradients(plan.data_ptr(), size, want / 2, norm.data_ptr(), work.data_ptr(), need, stream) == 0
+    check_norm(norm, want)
+    assert (a == 2.0).all() and (c == 100.0).all()
+    check_scaled(b, torch.full((5000,), 3.0), 0.5)
