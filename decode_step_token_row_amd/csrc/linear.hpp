@@ -9,6 +9,7 @@
 #include <stdint.h>
 
 #include "arcs.h"
+#include "linear_shape.hpp"
 
 namespace arcs {
 
@@ -38,20 +39,6 @@ struct LinearArgs {
   void* out_dbias;       // [V] of T, or NULL
   char* workspace;
 };
-
-// One product of the tile kernels: C[m, n] = sum_k A[m, k] B[n, k], and its tiles.
-//   FORWARD  m: V, n: N, k: D    rows of both operands run along k
-//   DHIDDEN  m: D, n: N, k: V    rows of A (the weight) run along m
-//   DWEIGHT  m: D, n: V, k: N    rows of both run along m and n
-enum LinearMode { kLinForward, kLinDhidden, kLinDweight };
-struct LinearShape {
-  int rows;     // of the tile along n; 0: no tiles (the few-rows kernel)
-  int columns;  // of the tile along m
-  int workers;  // workgroups that share all tiles evenly, each a part of k of some; 0: whole tiles
-};
-// The tiles of a product: of those built for the mode and type, and of the ways to share them,
-// the ones that cost least.
-LinearShape linear_shape(int mode, int64_t M, int64_t N, int64_t K, bool bf16);
 
 // The workspace's parts, in bytes from its start.
 struct LinearPlan {

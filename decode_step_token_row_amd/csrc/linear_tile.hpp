@@ -530,8 +530,6 @@ __global__ __launch_bounds__(256) void linear_join_kernel(LinearProduct p) {
   linear_finish<T, FORWARD, 4>(p, n, m, left, v, bias, residual);
 }
 
-inline int64_t linear_tiles(int64_t n, int64_t t) { return (n + t - 1) / t; }
-
 template <typename T, int MODE, int WM, int WN, int MT, int NT, int S>
 bool launch_linear_tile(const LinearProduct& p, hipStream_t stream) {
   using C = LinTile<T, MODE, WM, WN, MT, NT, S>;
