@@ -222,7 +222,7 @@ __global__ __launch_bounds__(kThreads) void adjust_kernel(AdjustArgs a) {
     }
   }
 
-  // The biases of the slice's tokens, 256 entries of the list at a time: those of the slice in
+  // The biases of the slice's tokens, kThreads entries of the list at a time: those of the slice in
   // list order in LDS; the first entry of a token adds all of its token's.
   if (biased) {
     if (counted) __syncthreads();

@@ -12,14 +12,15 @@ namespace arcs {
 // ---------------------------------------------------------------------------
 // forward, few rows
 // ---------------------------------------------------------------------------
-// A workgroup makes 16 columns of the output for all rows: its waves take blocks of 128 bytes of k
+// A workgroup makes 16 R columns of the output for all rows: its waves take blocks of 128 bytes of k
 // in turn, weights and hidden states straight from memory to registers (a line of each of
 // 16 weight rows in two loads, 16 bytes a lane), U blocks in flight, and their sums meet in LDS.
 // Reading the weights bounds it: one row x 32,000 x 2,048 takes 22.5 to 24 us (131 MB, 5.6 TB/s; a
 // copy reaches 4.8 read and written), one row x 129,280 x 4,096 168 (6.3 TB/s); eight rows x 4,096
-// x 4,096 take 9.8 to 10.3 us, of which about 4 are a launch with next to no work.  Two, four and
-// eight blocks in flight: 27.7, 24.2 and 29.9 us for the first; asked for half a line at a time
-// and four steps ahead it took 27.9.
+// x 4,096 take 9.8 to 10.3 us, of which about 4 are a launch with next to no work.  float32 takes
+// twice the bytes: 54 us for the first (4.8 TB/s), 19 for the last.  Two, four and eight blocks in
+// flight, bfloat16: 27.7, 24.2 and 29.9 us for the first; asked for half a line at a time and four
+// steps ahead it took 27.9.
 constexpr int kFewWaves = 8;
 
 template <typename T>
@@ -118,10 +119,14 @@ __global__ __launch_bounds__(kFewWaves * 64) void linear_few_kernel(LinearArgs a
 // backward: dz and the columns' sums
 // ---------------------------------------------------------------------------
 // A workgroup has 256 columns of ROWS * 8 rows: a thread 8 columns of ROWS rows, all loaded at
-// once.  Reading grad_out and z and writing dz bounds it: 4,096 x 4,096 in bfloat16 takes 22 us
-// (100 MB; 54 with rows one after the other and the library's exp and division, 1,037 x 5,003 11
-// instead of 48).  The sums take dz before it is rounded to T; a workgroup's meet in LDS.  dz may be
-// NULL (only dbias is wanted, or grad_out is dz as it is), and so may the sums.
+// once.  Reading grad_out and z and writing dz bounds it, and the activation's slope is close behind: 4,096 x
+// 4,096 in bfloat16 takes 23 us with silu (100 MB; 54 with rows one after the other and the library's
+// exp and division), 1,037 x 5,003 with gelu by tanh 14.  dz is rounded to T, as the matrix instructions
+// of bfloat16 take both operands in it and float32's run at a tenth of their rate, and z was in the forward
+// pass, as that halves what is kept between the two: the gradients are 0.0024 from the exact ones in the
+// norm, 0.0023 were z in float32, and 0.0017 with nothing rounded but themselves.  The sums take dz
+// before it is rounded to T; a workgroup's meet in LDS.  dz may be NULL (only dbias is wanted, or
+// grad_out is dz as it is), and so may the sums.
 template <typename T, typename G, int ROWS>
 __global__ __launch_bounds__(256) void linear_dz_kernel(LinearArgs a, T* dz, int64_t ldz, float* sums, unsigned across) {
   __shared__ __align__(16) float part[8][256];

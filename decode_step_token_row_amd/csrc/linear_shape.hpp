@@ -22,9 +22,9 @@ struct LinearShape {
 // loads, then for each round of tiles `step` (`alone` where no compute unit has two) for
 // each 128 bytes of k and `end` for the results; shared tiles cost their parts' way
 // through memory (bytes per microsecond) and `join` for the second launch.  Fitted to the times
-// of 51 sizes of each mode in bfloat16 and 13 in float32 (17 .. 4,096 rows, 200 .. 130,000
-// columns, k of 100 .. 11,008), measured in every kind and sharing: what the costs
-// name takes 0.5 % longer in the geometric mean than the best, 25 % at most (of 10 us).  On
+// of 47 sizes of the forward product and 42 of each gradient in bfloat16, 13 of each in float32 (17 .. 4,096
+// rows, 200 .. 130,000 columns, k of 100 .. 11,008), measured in every kind and sharing: what the
+// costs name takes 0.4 % longer in the geometric mean than the best, 24 % at most (of 13 us).  On
 // both sides of the choice, for instance, forward: 4,096 x 4,096 x 4,096 125 us in 256 x 256
 // and 148 in 128 x 128; 512 x 11,008 x 4,096 63 in 128 x 128, 92 in 256 x 256 shared; 256 x
 // 4,096 x 4,096 23 in 64 x 64, 26 in 128 x 128 shared.  (256 x 128, 256 x 64 and 128 x 64 in

@@ -12,19 +12,22 @@
 // results do not depend on timing.
 //
 // What bounds it, at 4,096 x 4,096 x 4,096 in bfloat16 (256 tiles of 256 x 256, one a compute
-// unit): forward 120 us (1,150 TFLOP/s), dhidden 113 to 116, dweight 110 to 115; a large
-// library product reaches 1,450 TFLOP/s.  The matrix units are busy 68 % of the cycles.  Without the
-// loads the loop takes 82 us, without the LDS reads 106 to 116: the way of 1.07 GB from L2 to
-// LDS is what is not hidden.  Steps that counted: the next loads halfway through the third of
-// the four steps instead of in the last, with a second meeting of the workgroup for it (head of 256
-// rows 306 -> 286 us); priority for the multiplying workgroup of two on a compute unit.
-// Steps that did not: loads spread over the whole tile with a third place for A (121 us), four waves
-// of 128 x 128 (116 to 125), walks along k begun at different places, other cache policies of
-// the loads.  Rows of a power-of-two length cost the forward pass more than the others (4,032
+// unit): forward 114 to 120 us (1,150 to 1,200 TFLOP/s), dhidden 109 to 116, dweight 110 to 115; a large
+// library product reaches 1,450 TFLOP/s.  The matrix units are busy 60 % of a gradient's cycles; the rest is
+// the way of 1.07 GB from L2 to LDS, as far as the products do not cover it.  Steps that counted: the
+// next loads halfway through the third of the four steps instead of in the last, with a second meeting of
+// the workgroup for it (head of 256 rows 306 -> 286 us); priority for the multiplying workgroup of two
+// on a compute unit.  Steps that did not: loads spread over the whole tile with a third place for A (121
+// us), four waves of 128 x 128 (116 to 125), walks along k begun at different places, other cache policies
+// of the loads.  Rows of a power-of-two length cost the forward pass more than the others (4,032
 // columns of k were 13 % faster before the second meeting).
-// The epilogue with bias, silu, residual and z written beside the output adds 14 us to the forward
+// The epilogue with bias, silu, residual and z written beside the output adds 9 to 14 us to the forward
 // pass of that size (100 MB more, 20 us at the rate of a copy); it added 45 while every
-// element had its own branch on the activation and its residual was waited for.
+// element had its own branch on the activation and its residual was waited for.  One kernel has all of
+// the epilogue's choices, and the 256 x 256 forward one keeps 15 vector registers in scratch memory for
+// them (64 bytes a lane, filled before and read after the loop over k), the 128 x 128 one 129 scalar
+// registers in lanes of vector registers: the former writes 83 MB for 67 MB of results, the gradients,
+// which keep theirs, 35.
 #pragma once
 
 #include <hip/hip_runtime.h>

@@ -610,8 +610,9 @@ int arcs_linear(const void* hidden, int64_t hidden_stride, const void* weight, i
  *                must be given; each is written whole, not added to
  *   workspace    arcs_linear_backward_workspace_bytes()
  * dz is rounded to dtype before the products (as z was), and summed for out_dbias
- * before that; sums are held in binary32 or more.  Other arguments and errors as the
- * forward call; ARCS_ERR_BAD_VOCAB also for V above 2^21 - 8.
+ * before that; sums are held in binary32 or more.  act'(z) is within 32 2^-24 of the
+ * sum of its terms' sizes (for the softcap, 16 (1 + |z / softcap|) 2^-24 of itself).
+ * Other arguments and errors as the forward call; ARCS_ERR_BAD_VOCAB also for V above 2^21 - 8.
  */
 int arcs_linear_backward(const void* hidden, int64_t hidden_stride, const void* weight, int64_t weight_stride,
                          int dtype, int64_t N, int64_t V, int64_t D, int activation, float softcap,

@@ -13,7 +13,10 @@ rounds once:
         once, as 4, 2 for exp2, two sums, the reciprocal (2) and two products: 12; below 1/4 less.
   slope two terms, each of at most two exponentials h, a tail or two reciprocals, and ten roundings:
         6 + 8.3 + 10 of each of the two.
-So values are within 20 u of themselves, and slopes within 32 u of the sum of their terms' sizes.
+        softcap: 4 e / (1 + e)^2 with e = exp(-2 |u|): four roundings of the argument, 8 |u|, 2 for exp2, two
+        reciprocals of a sum (6), three products: 11 + 8 |u| of itself.
+So values are within 20 u of themselves, and slopes within 32 u of the sum of their terms' sizes, the
+softcap's within 16 (1 + |u|) of themselves.
 Values below the smallest normal number are off by steps of 2^-149; the exponential h^2 of a
 slope is below it from 87 on, and multiplied by at most 2^12.
 """
@@ -93,6 +96,21 @@ def test_softcap(arcs, cap, rows):
     want = c * np.tanh(z.astype(np.float64) / c)
     far = np.abs(got - want) - 20 * U * np.abs(want) - 2.0 ** -147
     assert far.max() <= 0, (float(z[far.argmax()]), got[far.argmax()], want[far.argmax()])
+
+
+@pytest.mark.parametrize("cap", [2.0 ** -100, 1e-3, 1.5, 30.0, 1e10, 2.0 ** 100])
+def test_the_slope_of_softcap(arcs, cap):
+    """1 - tanh^2 (z / c), which is below the smallest normal number past 44."""
+    import torch
+    z = points()
+    h, w = torch.zeros(1, 4, device="cuda"), torch.zeros(len(z), 4, device="cuda")
+    pre = torch.from_numpy(z).cuda()[None]
+    _, _, db = arcs.linear_backward(h, w, torch.ones_like(pre), pre=pre, activation="softcap", softcap=cap, want_bias=True)
+    with np.errstate(all="ignore"):
+        u = np.minimum(np.abs(z.astype(np.float64)) / float(np.float32(cap)), 300.0)
+        want = 1 / np.cosh(u) ** 2
+    far = np.abs(db.cpu().numpy().astype(np.float64) - want) - 16 * U * (1 + u) * want - 2.0 ** -123
+    assert far.max() <= 0, (float(z[far.argmax()]), float(db[far.argmax()]), want[far.argmax()])
 
 
 @pytest.mark.parametrize("act", ACTS)
