@@ -968,6 +968,8 @@ class TensorList:
     tensor of as many elements for each, where clip_gradients writes, or None: in place.  The
     list keeps the tensors alive, and its plan: a captured graph that holds a call needs the list
     as long as it is replayed.  Memory that overlaps (the same tensor twice, say) is refused.
+    Making a list takes the host longer than a call (86 us for 12 tensors, 4.8 ms for 1,500): it is
+    for gradients that are written to the same memory in every step.
     """
 
     def __init__(self, tensors, outs=None):
