@@ -248,3 +248,11 @@ def test_tensors_without_an_out_count_and_are_not_written(arcs):
     check_norm(norm, want)
     assert (a == 2.0).all() and (c == 100.0).all()
     check_scaled(b, torch.full((5000,), 3.0), 0.5)
+
+
+def test_a_list_of_empty_tensors(arcs):
+    import torch
+    ts = [torch.empty(0, device="cuda"), torch.empty(0, 5, dtype=torch.bfloat16, device="cuda")]
+    plan = arcs.TensorList(ts)
+    out = torch.full((1,), 7.0, device="cuda")
+    assert float(arcs.gradient_norm(plan)) == 0.0 and float(arcs.clip_gradients(plan, 0.0, out_norm=out)) == 0.0 and float(out) == 0.0

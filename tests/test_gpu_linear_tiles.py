@@ -122,3 +122,31 @@ def test_replays_of_large_tiles(arcs):
         torch.cuda.synchronize()
         for a, b in zip(held, want):
             assert torch.equal(a, b)
+
+
+def far_rows(x, stride):
+    """The rows of x, `stride` elements apart."""
+    import torch
+    wide = torch.empty((x.shape[0] - 1) * stride + x.shape[1], dtype=x.dtype, device="cuda").as_strided(x.shape, (stride, 1))
+    wide.copy_(x)
+    return wide
+
+
+@pytest.mark.parametrize("over", [-1, 0])
+@pytest.mark.parametrize("dtype", ["bf16", "f32"])
+def test_rows_that_lie_far_apart(arcs, dtype, over):
+    """Rows just below 2^23 bytes apart, which the tiles read where they are (256 of them are 2^31 bytes), and
+    2^23 bytes apart, which are copied; grad_out too."""
+    import torch
+    t = types()[dtype]
+    size = 2 if dtype == "bf16" else 4
+    stride = 2 ** 23 // size + over * (16 // size)
+    g = torch.Generator("cuda").manual_seed(3)
+    for N, V, D in ((9, 70, 72), (256, 34968, 200), (300, 248, 264)):
+        h, w, b, grad = whole(g, 2, t, N, D), whole(g, 2, t, V, D), whole(g, 3, t, V), whole(g, 1, t, N, V)
+        x = far_rows(h, stride)
+        y = far_rows(w, stride) if V < 300 else w
+        z = far_rows(grad, stride)
+        assert torch.equal(arcs.linear(x, y, bias=b, out_dtype=torch.float32), (times(h, w.T) + b.double()).float())
+        dh, dw, db = arcs.linear_backward(x, y, z, want_bias=True)
+        assert torch.equal(dh, times(grad, w).to(t)) and torch.equal(dw, times(grad.T, h).to(t)) and torch.equal(db, grad.double().sum(0).to(t))
