@@ -151,7 +151,7 @@ struct AdjustArgs {
   // set by the launch
   int slices, per_row;
 };
-// Whether the launch grid holds the call.
+// Whether the call is within the sizes arcs.h names (more rows than one launch holds go in several).
 bool adjust_fits(int64_t B, int64_t V);
 hipError_t launch_adjust(AdjustArgs a, int dtype, int out_dtype, int64_t B, hipStream_t stream);
 
